@@ -25,7 +25,9 @@ EXPORTS = ("moe_create", "moe_destroy", "moe_route", "moe_route_hash", "moe_perm
            "moe_workspace_bytes", "moe_last_error", "moe_set_gemm_path", "moe_set_stage_events",
            "moe_kernel_launches", "moe_permute_noalloc", "moe_set_trace", "moe_route_forward",
            "moe_set_route_prune", "moe_set_wait_limit", "moe_test_stall_next_decode", "moe_test_decode_split",
-           "moe_set_decode_kernel", "moe_decode_info")
+           "moe_set_decode_kernel", "moe_decode_info", "moe_dispatch", "moe_dispatch_backward",
+           "moe_combine", "moe_combine_backward", "moe_route_backward", "moe_quantize_rows",
+           "moe_expert_product")
 
 
 class MoeError(RuntimeError):
@@ -63,7 +65,7 @@ def load_library(build: bool = True) -> C.CDLL:
     if not path.exists():
         raise ImportError(f"libmoe.so not found at {path}")
     L = C.CDLL(str(path))
-    vp, i, f = C.c_void_p, C.c_int, C.c_float
+    vp, i, f, ll = C.c_void_p, C.c_int, C.c_float, C.c_longlong
     sigs = {
         "moe_create": ([C.POINTER(moe_config), C.POINTER(moe_weights), vp, C.POINTER(vp)], i),
         "moe_destroy": ([vp], i),
@@ -89,6 +91,13 @@ def load_library(build: bool = True) -> C.CDLL:
         "moe_test_decode_split": ([C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.POINTER(C.c_int)], i),
         "moe_set_decode_kernel": ([vp, i], i),
         "moe_decode_info": ([vp, C.POINTER(C.c_int)], i),
+        "moe_dispatch": ([vp, i, ll, i, i, i, vp, i, vp, vp, ll, vp], i),
+        "moe_dispatch_backward": ([vp, i, ll, i, i, i, vp, vp, i, ll, vp], i),
+        "moe_combine": ([vp, i, ll, vp, i, i, i, vp, vp, i, ll, vp], i),
+        "moe_combine_backward": ([vp, i, ll, vp, i, ll, vp, i, i, i, vp, i, vp, vp, ll, vp, vp], i),
+        "moe_route_backward": ([vp, vp, vp, i, i, i, f, vp, vp], i),
+        "moe_quantize_rows": ([vp, i, ll, i, i, i, vp, ll, vp, vp], i),
+        "moe_expert_product": ([vp, ll, i, vp, i, vp, vp, i, i, vp, vp, i, i, vp, i, ll, vp], i),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
@@ -123,6 +132,27 @@ def _ptr(t, dtype, shape=None, name="tensor"):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
+
+
+MOE_F32, MOE_BF16, MOE_F16 = range(3)
+
+
+def _rows(t, name, rows=None, width=None):
+    """(pointer, moe_dtype, stride) of a 2-D CUDA tensor of rows whose elements are adjacent."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.int8: None}.get(t.dtype, -1)
+    if code == -1 or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor of float32, bfloat16 or float16 rows, got {t.dtype} {tuple(t.shape)}")
+    n, m = t.shape
+    if (rows is not None and n != rows) or (width is not None and m != width):
+        raise ValueError(f"{name} must have shape ({n if rows is None else rows}, {m if width is None else width}), "
+                         f"got {tuple(t.shape)}")
+    step, inner = t.stride()
+    if m > 1 and inner != 1:
+        raise ValueError(f"the elements of a row of {name} must be adjacent")
+    return t.data_ptr(), code, (step if n > 1 else m)
 
 
 def _hptr(t, dtype, shape, name):
@@ -393,3 +423,128 @@ def moe_kernel_launches(layer: Layer) -> int:
 def moe_last_error(layer: Optional[Layer] = None) -> str:
     m = load_library().moe_last_error(layer.ptr if layer else None)
     return m.decode() if m else ""
+
+
+def _slots(row_dst, T, name="row_dst"):
+    """(pointer, top_k) of the slots [T][top_k], also given flat."""
+    import torch
+    n = row_dst.numel()
+    if T < 1 or n % T or not 1 <= n // T <= 8:
+        raise ValueError(f"{name} must hold T * top_k positions with top_k in [1, 8], got {n} for T = {T}")
+    return _ptr(row_dst, torch.int32, None, name), n // T
+
+
+def moe_dispatch(x, offsets, row_dst, xs, stream=None):
+    """xs[row_dst[t, j]] = x[t]; zeros past the last placed row.  x [T][H] and
+    xs [T * top_k][H] in one of float32, bfloat16, float16; offsets [E + 1] and
+    row_dst [T * top_k] as moe_permute writes them."""
+    import torch
+    T, H = x.shape
+    if T == 0:
+        return
+    dst, k = _slots(row_dst, T)
+    px, dt, sx = _rows(x, "x")
+    ps, dts, ss = _rows(xs, "xs", T * k, H)
+    if dt is None or dts != dt:
+        raise ValueError("x and xs must have one floating dtype")
+    _check(load_library().moe_dispatch(px, dt, sx, T, k, H, _ptr(offsets, torch.int32, None, "offsets"),
+                                       offsets.numel() - 1, dst, ps, ss, _stream(stream)))
+
+
+def moe_dispatch_backward(dxs, row_dst, dx, stream=None):
+    """dx[t] = sum_j dxs[row_dst[t, j]]; dx in dxs's dtype or float32."""
+    T, H = dx.shape
+    if T == 0:
+        return
+    dst, k = _slots(row_dst, T)
+    ps, dts, ss = _rows(dxs, "dxs", T * k, H)
+    px, dt, sx = _rows(dx, "dx")
+    if dt is None or dts is None:
+        raise ValueError("dxs and dx must be floating tensors")
+    _check(load_library().moe_dispatch_backward(ps, dts, ss, T, k, H, dst, px, dt, sx, _stream(stream)))
+
+
+def moe_combine(y, w, row_dst, out, stream=None):
+    """out[t] = sum_j w[t, j] * y[row_dst[t, j]]; out in y's dtype or float32."""
+    import torch
+    T, H = out.shape
+    if T == 0:
+        return
+    dst, k = _slots(row_dst, T)
+    py, dty, sy = _rows(y, "y", T * k, H)
+    po, dto, so = _rows(out, "out")
+    if dty is None or dto is None:
+        raise ValueError("y and out must be floating tensors")
+    _check(load_library().moe_combine(py, dty, sy, _ptr(w, torch.float32, (T, k), "w"), T, k, H, dst, po, dto, so,
+                                      _stream(stream)))
+
+
+def moe_combine_backward(dout, y, w, offsets, row_dst, dy, dw, stream=None):
+    """dy[row_dst[t, j]] = w[t, j] * dout[t] (zeros past the last placed row)
+    and dw[t, j] = <dout[t], y[row_dst[t, j]]>; dout in y's dtype or float32."""
+    import torch
+    T, H = dout.shape
+    if T == 0:
+        return
+    dst, k = _slots(row_dst, T)
+    pd, dtd, sd = _rows(dout, "dout")
+    py, dty, sy = _rows(y, "y", T * k, H)
+    pg, dtg, sg = _rows(dy, "dy", T * k, H)
+    if dtd is None or dty is None or dtg != dty:
+        raise ValueError("y and dy must have one floating dtype, and dout be a floating tensor")
+    _check(load_library().moe_combine_backward(pd, dtd, sd, py, dty, sy, _ptr(w, torch.float32, (T, k), "w"), T, k, H,
+                                               _ptr(offsets, torch.int32, None, "offsets"), offsets.numel() - 1, dst,
+                                               pg, sg, _ptr(dw, torch.float32, (T, k), "dw"), _stream(stream)))
+
+
+def moe_route_backward(logits, ids, dw, dlogits, w_scale: float = 1.5, stream=None):
+    """Gradient of moe_route's weights: dlogits [T][E] from dw [T][k]."""
+    import torch
+    T, E = logits.shape
+    k = ids.shape[1]
+    if T == 0:
+        return
+    _check(load_library().moe_route_backward(_ptr(logits, torch.float32, (T, E), "logits"),
+                                             _ptr(ids, torch.int32, (T, k), "ids"),
+                                             _ptr(dw, torch.float32, (T, k), "dw"), T, E, k, float(w_scale),
+                                             _ptr(dlogits, torch.float32, (T, E), "dlogits"), _stream(stream)))
+
+
+def moe_quantize_rows(x, q, scale, gated: bool = False, stream=None):
+    """x [rows][K] (gated: [rows][2 K], SiLU of the first half times the second)
+    to int8 q [rows][K] with one float32 scale a row."""
+    import torch
+    rows, K = q.shape
+    if rows == 0:
+        return
+    px, dt, sx = _rows(x, "x", rows, 2 * K if gated else K)
+    pq, dtq, sq = _rows(q, "q")
+    if dt is None or dtq is not None:
+        raise ValueError("x must be a floating tensor and q int8")
+    _check(load_library().moe_quantize_rows(px, dt, sx, int(bool(gated)), rows, K, pq, sq,
+                                            _ptr(scale, torch.float32, (rows,), "scale"), _stream(stream)))
+
+
+def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, top_k: int = 1, stream=None):
+    """out[p] = scale[r] * w_scale[e] * (wq[e] q[r]) for the positions p of expert
+    e's segment; r = row_src[p] // top_k, or p without row_src.  q [rows][K] and
+    wq [E][N][K] int8, w_scale [E][N], out [R][N]; offsets [E + 1] may be left
+    out with one expert."""
+    import torch
+    R, N = out.shape
+    if R == 0:
+        return
+    if wq.dim() != 3:
+        raise ValueError(f"wq must have shape (E, N, K), got {tuple(wq.shape)}")
+    E, _, K = wq.shape
+    pq, dtq, sq = _rows(q, "q", None, K)
+    po, dto, so = _rows(out, "out")
+    if dtq is not None or dto is None:
+        raise ValueError("q must be int8 and out a floating tensor")
+    rows = q.shape[0]
+    _check(load_library().moe_expert_product(
+        pq, sq, rows, _ptr(scale, torch.float32, (rows,), "scale"), K, _ptr(wq, torch.int8, (E, N, K), "wq"),
+        _ptr(w_scale, torch.float32, (E, N), "w_scale"), E, N,
+        None if offsets is None else _ptr(offsets, torch.int32, (E + 1,), "offsets"),
+        None if row_src is None else _ptr(row_src, torch.int32, (R,), "row_src"), int(top_k), R, po, dto, so,
+        _stream(stream)))

@@ -1,0 +1,260 @@
+// int_product.cu -- rows in 8-bit integers with one scale each
+// (moe_quantize_rows) and their product with 8-bit integer experts over the
+// sorted segments (moe_expert_product; C entries at the end).
+//
+//   out[p, n] = scale[r] w_scale[e, n] sum_i q[r, i] wq[e, n, i]
+//
+// for the positions p of expert e's segment, r the row that position p reads.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "layer.h"
+#include "rows.cuh"
+
+namespace moe {
+namespace {
+
+// ----------------------------------------------------------- quantize_rows --
+// v = x, or silu(x[c]) * x[K + c] of a gated row of 2 K (expf and IEEE
+// division).  scale = max|v| / 127 and q = rint(127 v / max|v|): dividing the
+// exact 127 v (for bf16 and fp16 x) by the maximum, not v by the rounded scale,
+// keeps values half way between two codes half way.  A maximum above 2^119 is
+// scaled down first (127 v would overflow).  A row with an infinity or a NaN
+// gets scale NaN, so that its products are NaN, and codes 0.
+template <typename A, int C, bool kGated>
+__device__ __forceinline__ void quant_load(const A* row, int K, int c, float (&v)[C]) {
+    const Chunk<A, C> a = load_chunk<A, C>(row + c);
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = to_f32(a.v[i]);
+    if (kGated) {
+        const Chunk<A, C> u = load_chunk<A, C>(row + K + c);
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = __fmul_rn(__fdiv_rn(v[i], 1.f + expf(-v[i])), to_f32(u.v[i]));
+    }
+}
+
+template <typename A, int C, bool kGated>
+__global__ void __launch_bounds__(256) k_quantize_rows(const A* __restrict__ x, long long xs, long long rows, int K,
+                                                       int8_t* __restrict__ q, long long qs,
+                                                       float* __restrict__ scale) {
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ float part[8];
+    for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
+        const A* row = x + r * xs;
+        float most = 0.f;  // of |v|, infinite where one is not finite
+        for (int c = threadIdx.x * C; c < K; c += blockDim.x * C) {
+            float v[C];
+            quant_load<A, C, kGated>(row, K, c, v);
+#pragma unroll
+            for (int i = 0; i < C; ++i) most = fmaxf(most, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : INFINITY);
+        }
+        most = warp_max(most);
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = most;
+        __syncthreads();
+        most = part[0];
+        for (int a = 1; a < (int)(blockDim.x >> 5); ++a) most = fmaxf(most, part[a]);
+        const bool live = most > 0.f && most < INFINITY;
+        const float down = most > 0x1p119f ? 0x1p-8f : 1.f;
+        if (threadIdx.x == 0) scale[r] = most < INFINITY ? __fdiv_rn(most, 127.f) : NAN;
+        for (int c = threadIdx.x * C; c < K; c += blockDim.x * C) {
+            float v[C];
+            quant_load<A, C, kGated>(row, K, c, v);
+            Chunk<int8_t, C> out;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                out.v[i] = live ? (int8_t)__float2int_rn(__fdiv_rn(__fmul_rn(v[i] * down, 127.f), most * down)) : 0;
+            *reinterpret_cast<Chunk<int8_t, C>*>(q + r * qs + c) = out;
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- segments --
+// Segment of expert e, held inside [0, R] whatever the offsets are.
+__device__ __forceinline__ int segment_at(const int32_t* offsets, int e, int R) {
+    return min(max(offsets ? offsets[e] : (e ? R : 0), 0), R);
+}
+
+struct Product {
+    const int8_t* q; long long qs; int rows; const float* scale; int K;
+    const int8_t* wq; const float* w_scale; int E, N;
+    const int32_t* offsets; const int32_t* row_src; int k;
+    int R; void* out; long long os;
+};
+
+// Row of q that position p reads, or -1.
+__device__ __forceinline__ int source_row(const Product& a, int p) {
+    const int r = a.row_src ? (a.row_src[p] < 0 ? -1 : a.row_src[p] / a.k) : p;
+    return r < a.rows ? r : -1;
+}
+
+// --------------------------------------------------------- any size, simple --
+// One block a tile of 32 positions of one segment x 32 channels: 32-byte steps
+// of K through shared memory, four products an instruction (__dp4a), exact
+// 32-bit integer sums.  Reads K byte by byte, so any K, stride and alignment.
+template <typename O>
+__global__ void __launch_bounds__(256) k_product_any(const Product a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ int sm_e, sm_j;
+    __shared__ int8_t xs[32][36], ws[32][36];
+    __shared__ int src[32];
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        int left = blockIdx.y;
+        sm_e = -1;
+        for (int e = 0; e < a.E; ++e) {
+            const int n = (max(segment_at(a.offsets, e + 1, a.R) - segment_at(a.offsets, e, a.R), 0) + 31) / 32;
+            if (left < n) {
+                sm_e = e;
+                sm_j = left;
+                break;
+            }
+            left -= n;
+        }
+    }
+    __syncthreads();
+    const int e = sm_e, n0 = blockIdx.x * 32;
+    if (e < 0) return;
+    const int p0 = segment_at(a.offsets, e, a.R) + 32 * sm_j;
+    const int count = min(32, segment_at(a.offsets, e + 1, a.R) - p0);
+    if (tid < 32) src[tid] = tid < count ? source_row(a, p0 + tid) : -1;
+    __syncthreads();
+    const int tx = tid & 15, ty = tid >> 4;  // channels tx, tx + 16; positions ty, ty + 16
+    int acc[2][2] = {{0, 0}, {0, 0}};
+    for (int k0 = 0; k0 < a.K; k0 += 32) {
+        for (int i = tid; i < 32 * 32; i += 256) {
+            const int r = i >> 5, c = k0 + (i & 31);
+            xs[r][i & 31] = c < a.K && src[r] >= 0 ? a.q[src[r] * a.qs + c] : 0;
+            ws[r][i & 31] = c < a.K && n0 + r < a.N ? a.wq[((long long)e * a.N + n0 + r) * a.K + c] : 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < 32; c += 4)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __dp4a(*reinterpret_cast<const int*>(&xs[ty + 16 * i][c]),
+                                       *reinterpret_cast<const int*>(&ws[tx + 16 * j][c]), acc[i][j]);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int p = ty + 16 * i, n = n0 + tx + 16 * j;
+            if (p >= count || n >= a.N) continue;
+            const float s = src[p] >= 0 ? a.scale[src[p]] : 0.f;
+            reinterpret_cast<O*>(a.out)[(long long)(p0 + p) * a.os + n] =
+                from_f32<O>((float)acc[i][j] * s * a.w_scale[(long long)e * a.N + n]);
+        }
+}
+
+// Positions past the last segment are written as zeros.
+template <typename O>
+__global__ void __launch_bounds__(256) k_product_tail(const Product a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    for (long long p = segment_at(a.offsets, a.E, a.R) + (long long)blockIdx.x; p < a.R; p += gridDim.x)
+        for (int n = threadIdx.x; n < a.N; n += blockDim.x) reinterpret_cast<O*>(a.out)[p * a.os + n] = from_f32<O>(0.f);
+}
+
+// ----------------------------------------------------------------- entries --
+moe_status fail(moe_status st, const char* fmt, ...) {
+    char buf[200];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    set_thread_error(buf);
+    return st;
+}
+
+moe_status launched(cudaError_t e, const char* what) {
+    return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+template <typename A, int C>
+cudaError_t quantize_c(bool gated, const void* x, long long xs, long long rows, int K, int8_t* q, long long qs,
+                       float* scale, cudaStream_t s) {
+    auto* f = gated ? k_quantize_rows<A, C, true> : k_quantize_rows<A, C, false>;
+    return launch_pdl(f, dim3((unsigned)rows), dim3(256), 0, s, (const A*)x, xs, rows, K, q, qs, scale);
+}
+
+template <typename A>
+cudaError_t quantize_a(bool gated, const void* x, long long xs, long long rows, int K, int8_t* q, long long qs,
+                       float* scale, cudaStream_t s) {
+    constexpr int W = 16 / (int)sizeof(A);
+    if (K % W == 0 && row_align(x, xs * (long long)sizeof(A)) >= 16 && row_align(q, qs) >= (unsigned)W)
+        return quantize_c<A, W>(gated, x, xs, rows, K, q, qs, scale, s);
+    return quantize_c<A, 1>(gated, x, xs, rows, K, q, qs, scale, s);
+}
+
+template <typename O>
+cudaError_t product_o(const Product& a, cudaStream_t s) {
+    // at most one partly filled tile an expert
+    const long long tiles = (long long)a.R / 32 + (a.E < a.R ? a.E : a.R);
+    cudaError_t e = cudaSuccess;
+    if (tiles > 65535) return cudaErrorInvalidConfiguration;
+    e = launch_pdl(k_product_any<O>, dim3((a.N + 31) / 32, (unsigned)tiles), dim3(256), 0, s, a);
+    if (e == cudaSuccess && a.offsets) e = launch_pdl(k_product_tail<O>, dim3(a.R < 152 ? a.R : 152), dim3(256), 0, s, a);
+    return e;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_quantize_rows(const void* x, moe_dtype dtype, long long x_stride, int gated, int rows, int K,
+                                        int8_t* q, long long q_stride, float* scale, moe_stream_t stream) {
+    const char* what = "moe_quantize_rows";
+    if (!dtype_ok(dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype", what);
+    if (rows < 0 || rows > (1 << 30)) return fail(MOE_ERR_INVALID_ARG, "%s: rows must be in [0, 2^30]", what);
+    if (K < 1 || K > 131072) return fail(MOE_ERR_INVALID_ARG, "%s: K must be in [1, 131072]", what);
+    if (x_stride < (gated ? 2LL : 1LL) * K || q_stride < K || x_stride > (1LL << 40) || q_stride > (1LL << 40))
+        return fail(MOE_ERR_INVALID_ARG, "%s: a row stride is below the row or above 2^40", what);
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !scale) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
+    if ((uintptr_t)x % dtype_size(dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: x is not aligned to its elements", what);
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    if (dtype == MOE_F32) e = quantize_a<float>(gated != 0, x, x_stride, rows, K, q, q_stride, scale, s);
+    else if (dtype == MOE_BF16) e = quantize_a<__nv_bfloat16>(gated != 0, x, x_stride, rows, K, q, q_stride, scale, s);
+    else e = quantize_a<__half>(gated != 0, x, x_stride, rows, K, q, q_stride, scale, s);
+    return launched(e, what);
+}
+
+extern "C" moe_status moe_expert_product(const int8_t* q, long long q_stride, int q_rows, const float* scale, int K,
+                                         const int8_t* wq, const float* w_scale, int n_experts, int N,
+                                         const int32_t* offsets, const int32_t* row_src, int top_k, int R, void* out,
+                                         moe_dtype out_dtype, long long out_stride, moe_stream_t stream) {
+    const char* what = "moe_expert_product";
+    if (!dtype_ok(out_dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype", what);
+    if (K < 1 || K > 131072) return fail(MOE_ERR_INVALID_ARG, "%s: K must be in [1, 131072]", what);
+    if (N < 1 || N > (1 << 20)) return fail(MOE_ERR_INVALID_ARG, "%s: N must be in [1, 2^20]", what);
+    if (n_experts < 1 || n_experts > kMaxExperts)
+        return fail(MOE_ERR_INVALID_ARG, "%s: n_experts must be in [1, 1024]", what);
+    if (R < 0 || R > (1 << 20) || q_rows < 0) return fail(MOE_ERR_INVALID_ARG, "%s: R must be in [0, 2^20]", what);
+    if (!row_src && q_rows < R) return fail(MOE_ERR_INVALID_ARG, "%s: q has fewer rows than out", what);
+    if (row_src && (top_k < 1 || top_k > kMaxTopK))
+        return fail(MOE_ERR_INVALID_ARG, "%s: top_k must be in [1, 8]", what);
+    if (!offsets && n_experts != 1) return fail(MOE_ERR_INVALID_ARG, "%s: several experts need offsets", what);
+    if (q_stride < K || out_stride < N || q_stride > (1LL << 40) || out_stride > (1LL << 40))
+        return fail(MOE_ERR_INVALID_ARG, "%s: a row stride is below the row or above 2^40", what);
+    if (R == 0) return MOE_OK;
+    if (!q || !scale || !wq || !w_scale || !out) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
+    if ((uintptr_t)out % dtype_size(out_dtype))
+        return fail(MOE_ERR_INVALID_ARG, "%s: out is not aligned to its elements", what);
+    const Product a{q, q_stride, q_rows, scale, K, wq, w_scale, n_experts, N, offsets, row_src, top_k, R, out,
+                    out_stride};
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    if (out_dtype == MOE_F32) e = product_o<float>(a, s);
+    else if (out_dtype == MOE_BF16) e = product_o<__nv_bfloat16>(a, s);
+    else e = product_o<__half>(a, s);
+    return launched(e, what);
+}

@@ -351,6 +351,109 @@ moe_status moe_permute_noalloc(const int32_t* ids, int T, int top_k, int n_exper
                                int32_t* offsets, int32_t* row_src, int32_t* row_dst,
                                moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Rows in the experts' order: moving tokens to their sorted positions and
+ * back, the gradients of both, and the product of the sorted rows with
+ * 8-bit integer experts.  These calls stand next to the layer for experts
+ * that the layer does not hold (a training step's own expert products, other
+ * weight formats): they need no moe_layer, take moe_permute's offsets,
+ * row_src and row_dst, and follow the conventions above (device pointers,
+ * asynchronous on `stream`, no allocation, no synchronisation, capturable;
+ * messages through moe_last_error(NULL)).
+ *  - Rows are given by a base and a stride in elements from one row to the
+ *    next (>= the row's width); elements of a row are adjacent.  No
+ *    alignment beyond the element's is needed; 16-byte aligned rows whose
+ *    width is a multiple of 16 bytes move fastest.
+ *  - R = T * top_k sorted positions; row_dst device i32 [T][top_k] is a
+ *    slot's position, and anything outside [0, R) an empty slot.  Positions
+ *    from offsets[n_experts] on hold no row: they are never read, and a call
+ *    that writes sorted rows writes zeros there.
+ *  - T = 0 (or no rows) is allowed: nothing is enqueued, and pointers may be
+ *    NULL.  Outputs must not overlap inputs.
+ *  - Sums are held in fp32 (integer products in 32-bit integers or exactly
+ *    in fp32) and rounded once, in a fixed order: equal calls give equal bits.
+ *  - There is no device flag: out-of-range positions are skipped quietly. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
+
+/* Tokens to sorted positions: xs[row_dst[t][j]] = x[t] for every filled slot.
+ *   x device dtype [T][hidden]; xs device dtype [R][hidden], every row of
+ *   which is written; offsets device i32 [n_experts + 1].                  */
+moe_status moe_dispatch(const void* x, moe_dtype dtype, long long x_stride, int T, int top_k, int hidden,
+                        const int32_t* offsets, int n_experts, const int32_t* row_dst, void* xs,
+                        long long xs_stride, moe_stream_t stream);
+
+/* Gradient of moe_dispatch: dx[t] = sum over the filled slots of
+ * dxs[row_dst[t][j]], in ascending position.
+ *   dxs device dtype [R][hidden]; dx device dx_dtype [T][hidden], dx_dtype
+ *   being dtype or MOE_F32.                                               */
+moe_status moe_dispatch_backward(const void* dxs, moe_dtype dtype, long long dxs_stride, int T, int top_k,
+                                 int hidden, const int32_t* row_dst, void* dx, moe_dtype dx_dtype,
+                                 long long dx_stride, moe_stream_t stream);
+
+/* Sorted rows back to tokens with the routing weights (guide, section 3.2):
+ * out[t] = sum over the filled slots of w[t][j] * y[row_dst[t][j]], in
+ * ascending position (ascending expert id, the layer's own order).  The
+ * weight of an empty slot is not read; a token without a filled slot gets 0.
+ *   y device dtype [R][hidden]; w device f32 [T][top_k]; out device
+ *   out_dtype [T][hidden], out_dtype being dtype or MOE_F32.              */
+moe_status moe_combine(const void* y, moe_dtype dtype, long long y_stride, const float* w, int T, int top_k,
+                       int hidden, const int32_t* row_dst, void* out, moe_dtype out_dtype,
+                       long long out_stride, moe_stream_t stream);
+
+/* Gradient of moe_combine, both parts in one pass over y:
+ *   dy[row_dst[t][j]] = w[t][j] * dout[t]      device dtype [R][hidden]
+ *   dw[t][j] = <dout[t], y[row_dst[t][j]]>     device f32 [T][top_k], 0 for
+ *                                              an empty slot
+ * dout device dout_dtype [T][hidden], dout_dtype being dtype or MOE_F32.   */
+moe_status moe_combine_backward(const void* dout, moe_dtype dout_dtype, long long dout_stride,
+                                const void* y, moe_dtype dtype, long long y_stride, const float* w, int T,
+                                int top_k, int hidden, const int32_t* offsets, int n_experts,
+                                const int32_t* row_dst, void* dy, long long dy_stride, float* dw,
+                                moe_stream_t stream);
+
+/* Gradient of the learned router's weights (moe_route): with
+ * s = sqrt(softplus(logit)) and S the sum of s over a token's kept experts,
+ *   w_j = w_scale * s_j / S,
+ *   dlogits[t][ids_j] = (w_scale / S^2) * sum_i s_i (dw_j - dw_i)
+ *                       * sigmoid(logit_j) / (2 s_j), all others 0.
+ * The selection itself has no gradient.  Slots whose id is outside
+ * [0, n_experts) are not kept; with tail pruning this is the gradient of
+ * the linear rescaling (rho = 1), whose kept weights sum to w_scale.
+ *   logits device f32 [T][n_experts]; ids device i32 [T][top_k]; dw device
+ *   f32 [T][top_k]; dlogits device f32 [T][n_experts], overwritten.       */
+moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* dw, int T,
+                              int n_experts, int top_k, float w_scale, float* dlogits,
+                              moe_stream_t stream);
+
+/* Rows to 8-bit integers, one scale a row: with m the row's largest |v|,
+ *   scale = m / 127,  q = 127 v / m rounded to nearest, half to even
+ * (scale 0 and codes 0 for a row of zeros; scale NaN and codes 0 for a row
+ * with an infinity or a NaN, whose products are then NaN).
+ *   gated = 0: v = x, device dtype [rows][K]
+ *   gated = 1: v = SiLU(x[c]) * x[K + c], device dtype [rows][2 K]: the gate
+ *              and up halves of an expert's first product (guide, section 4)
+ *   q device i8 [rows][K]; scale device f32 [rows]; 1 <= K <= 131072.     */
+moe_status moe_quantize_rows(const void* x, moe_dtype dtype, long long x_stride, int gated, int rows, int K,
+                             int8_t* q, long long q_stride, float* scale, moe_stream_t stream);
+
+/* Sorted rows times 8-bit integer experts with a scale for each row and each
+ * output channel: for the positions p of expert e's segment
+ *   out[p][n] = scale[r] * w_scale[e][n] * sum_i q[r][i] * wq[e][n][i]
+ *   q device i8 [q_rows][K], scale device f32 [q_rows]; wq device i8
+ *   [n_experts][N][K], w_scale device f32 [n_experts][N] (both dense); out
+ *   device out_dtype [R][N], every row of which is written.
+ *   offsets device i32 [n_experts + 1], non-decreasing; NULL with one
+ *   expert: all R rows are its own (a dense product).
+ *   row_src device i32 [R]: position p reads row r = row_src[p] / top_k (the
+ *   tokens quantised once, read by each of their experts; an r outside
+ *   [0, q_rows) reads as zeros); NULL: r = p.
+ * The integer sum is exact while |sum| <= 2^24 and else accurate to fp32's
+ * rounding.  1 <= K <= 131072, 1 <= N <= 2^20, R <= 2^20.                 */
+moe_status moe_expert_product(const int8_t* q, long long q_stride, int q_rows, const float* scale, int K,
+                              const int8_t* wq, const float* w_scale, int n_experts, int N,
+                              const int32_t* offsets, const int32_t* row_src, int top_k, int R, void* out,
+                              moe_dtype out_dtype, long long out_stride, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
