@@ -9,8 +9,7 @@
 #include <cstdarg>
 #include <cstdio>
 
-#include "layer.h"
-#include "rows.cuh"
+#include "int_product.cuh"
 
 namespace moe {
 namespace {
@@ -71,25 +70,6 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const A* __restrict__ x, 
     }
 }
 
-// ---------------------------------------------------------------- segments --
-// Segment of expert e, held inside [0, R] whatever the offsets are.
-__device__ __forceinline__ int segment_at(const int32_t* offsets, int e, int R) {
-    return min(max(offsets ? offsets[e] : (e ? R : 0), 0), R);
-}
-
-struct Product {
-    const int8_t* q; long long qs; int rows; const float* scale; int K;
-    const int8_t* wq; const float* w_scale; int E, N;
-    const int32_t* offsets; const int32_t* row_src; int k;
-    int R; void* out; long long os;
-};
-
-// Row of q that position p reads, or -1.
-__device__ __forceinline__ int source_row(const Product& a, int p) {
-    const int r = a.row_src ? (a.row_src[p] < 0 ? -1 : a.row_src[p] / a.k) : p;
-    return r < a.rows ? r : -1;
-}
-
 // --------------------------------------------------------- any size, simple --
 // One block a tile of 32 positions of one segment x 32 channels: 32-byte steps
 // of K through shared memory, four products an instruction (__dp4a), exact
@@ -106,7 +86,7 @@ __global__ void __launch_bounds__(256) k_product_any(const Product a) {
         int left = blockIdx.y;
         sm_e = -1;
         for (int e = 0; e < a.E; ++e) {
-            const int n = (max(segment_at(a.offsets, e + 1, a.R) - segment_at(a.offsets, e, a.R), 0) + 31) / 32;
+            const int n = (max(segment_at(a, e + 1) - segment_at(a, e), 0) + 31) / 32;
             if (left < n) {
                 sm_e = e;
                 sm_j = left;
@@ -118,8 +98,8 @@ __global__ void __launch_bounds__(256) k_product_any(const Product a) {
     __syncthreads();
     const int e = sm_e, n0 = blockIdx.x * 32;
     if (e < 0) return;
-    const int p0 = segment_at(a.offsets, e, a.R) + 32 * sm_j;
-    const int count = min(32, segment_at(a.offsets, e + 1, a.R) - p0);
+    const int p0 = segment_at(a, e) + 32 * sm_j;
+    const int count = min(32, segment_at(a, e + 1) - p0);
     if (tid < 32) src[tid] = tid < count ? source_row(a, p0 + tid) : -1;
     __syncthreads();
     const int tx = tid & 15, ty = tid >> 4;  // channels tx, tx + 16; positions ty, ty + 16
@@ -158,7 +138,7 @@ template <typename O>
 __global__ void __launch_bounds__(256) k_product_tail(const Product a) {
     pdl_launch_dependents();
     pdl_wait();
-    for (long long p = segment_at(a.offsets, a.E, a.R) + (long long)blockIdx.x; p < a.R; p += gridDim.x)
+    for (long long p = segment_at(a, a.E) + (long long)blockIdx.x; p < a.R; p += gridDim.x)
         for (int n = threadIdx.x; n < a.N; n += blockDim.x) reinterpret_cast<O*>(a.out)[p * a.os + n] = from_f32<O>(0.f);
 }
 
@@ -253,7 +233,8 @@ extern "C" moe_status moe_expert_product(const int8_t* q, long long q_stride, in
                     out_stride};
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (out_dtype == MOE_F32) e = product_o<float>(a, s);
+    if (product_tc_fits(a)) e = launch_product_tc(a, out_dtype, s);
+    else if (out_dtype == MOE_F32) e = product_o<float>(a, s);
     else if (out_dtype == MOE_BF16) e = product_o<__nv_bfloat16>(a, s);
     else e = product_o<__half>(a, s);
     return launched(e, what);

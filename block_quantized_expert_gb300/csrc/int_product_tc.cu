@@ -1,0 +1,437 @@
+// int_product_tc.cu -- the product with 8-bit integer experts on the tensor
+// cores (moe_expert_product).
+//
+// This part's tensor cores have no fast 8-bit integer form, but an 8-bit integer is
+// exact in fp16, a product of two is exact in fp32 and so is a sum of them up
+// to 2^24: the codes are turned into fp16 on the way to tcgen05.mma.kind::f16
+// with fp32 accumulators.  A sum passes 2^24 only for K > 1024 and codes that
+// nearly all are extreme and agree in sign; it is then rounded like any fp32 sum.
+//
+// One CTA per SM walks tiles of 128 output channels (A, one tensor-memory lane
+// a channel) x up to kCap positions of one segment (B).  K goes in units of 64:
+//   warp 16      TMA of 128 channels x 128 bytes of codes into a ring
+//   warps 0-3    codes of one channel a thread -> fp16 -> tensor memory (A
+//                operand: it takes no shared-memory bandwidth from B)
+//   warps 4-11   token codes: global -> registers (kAhead units ahead) -> fp16
+//                -> shared memory, rows of 128 bytes, 128-byte swizzle; the
+//                token row is looked up here, so that a gather costs nothing
+//   warp 17      one thread issues the MMAs (N = the tile's rows rounded to 16)
+//   warps 12-15  accumulators -> scales -> out, while the next tile is summed
+//                (two accumulators)
+#include <cuda.h>
+
+#include <mutex>
+
+#include "int_product.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+bool make_byte_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows);
+
+namespace {
+
+using namespace tc;
+
+constexpr int kUnit = 64;             // K of one unit (128 bytes of fp16)
+constexpr int kThreads = 18 * 32;
+constexpr int kRawBytes = 128 * 128;  // one ring slot of weight codes
+constexpr int kAhead = 3;             // units of token codes held in registers
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+template <int kCap>
+struct Cfg {
+    static constexpr int kBBytes = kCap * 128;           // one unit of tokens in fp16
+    static constexpr int kSlots = kCap > 64 ? 4 : 8;     // units in flight to the MMA
+    static constexpr int kRaw = kCap > 64 ? 7 : 9;       // weight ring
+    static constexpr int kPasses = kCap / 64;            // 64 token rows a pass of the loaders
+    static constexpr int kACol = 512 - 32 * kSlots;      // tensor-memory column of the A units
+    static constexpr int kDCols = kCap > 64 ? 192 : 64;  // columns of one accumulator
+    static constexpr int kSmem = 1024 + kSlots * kBBytes + kRaw * kRawBytes;
+    static_assert(kCap % 64 == 0 && 2 * kDCols <= kACol && kCap <= kDCols, "tensor memory");
+};
+
+// D[tmem] (+)= A[tmem] B[smem]^T, fp16 operands, fp32 accumulators.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Four codes to two words of two fp16: with the sign bit turned, byte b = code
+// + 128 under the high byte 0x64 reads 1024 + b, from which 1152 is taken; all exact.
+__device__ __forceinline__ void codes_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = v ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+struct Tile {
+    int e, n0, p0, count;
+};
+
+__device__ uint32_t g_product_err;
+
+template <int kCap, typename O>
+__global__ void __launch_bounds__(kThreads, 1) k_product_tc(const Product a, const __grid_constant__ CUtensorMap wmap) {
+    using C = Cfg<kCap>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[2 * C::kRaw + 2 * C::kSlots + 4];
+    __shared__ int first[kMaxExperts + 1];  // token tiles before each expert
+    __shared__ int scan[32];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t b_base = base, raw_base = base + C::kSlots * C::kBBytes;
+    const uint32_t bar0 = smem_u32(bars);
+    auto raw_full = [&](int i) { return bar0 + 8u * i; };
+    auto raw_empty = [&](int i) { return bar0 + 8u * (C::kRaw + i); };
+    auto full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + i); };
+    auto empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + C::kSlots + i); };
+    auto d_full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kSlots + i); };
+    auto d_empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kSlots + 2 + i); };
+    volatile int* abort = &abort_flag;
+    if (tid == 0) {
+        for (int i = 0; i < C::kRaw; ++i) {
+            mbar_init(raw_full(i), 1);
+            mbar_init(raw_empty(i), 4);
+        }
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(full(i), 12);
+            mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(d_full(i), 1);
+            mbar_init(d_empty(i), 4);
+        }
+        abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&wmap);
+    }
+    if (warp == 17) tmem_alloc(smem_u32(&tmem_slot), 512);
+    pdl_wait();
+
+    // token tiles of every expert: ceil(count / kCap) of nearly equal size
+    {
+        int mine = 0;
+        const int per = (a.E + kThreads - 1) / kThreads;
+        for (int i = 0; i < per; ++i) {
+            const int e = tid * per + i;
+            if (e < a.E) mine += (max(segment_at(a, e + 1) - segment_at(a, e), 0) + kCap - 1) / kCap;
+        }
+        int run = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, run, o);
+            if (lane >= o) run += v;
+        }
+        if (lane == 31) scan[warp] = run;
+        __syncthreads();
+        int before = run - mine;
+        for (int i = 0; i < warp; ++i) before += scan[i];
+        for (int i = 0; i < per; ++i) {
+            const int e = tid * per + i;
+            if (e < a.E) {
+                first[e] = before;
+                before += (max(segment_at(a, e + 1) - segment_at(a, e), 0) + kCap - 1) / kCap;
+                if (e == a.E - 1) first[a.E] = before;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int m_tiles = (a.N + 127) / 128;
+    const long long tiles = (long long)first[a.E] * m_tiles;
+    const int units = (a.K + kUnit - 1) / kUnit;
+
+    // Tile t: the channels of one token tile follow each other.
+    auto tile_at = [&](long long t) {
+        const int tt = (int)(t / m_tiles);
+        int lo = 0, hi = a.E - 1;  // last e with first[e] <= tt
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first[mid] <= tt) lo = mid; else hi = mid - 1;
+        }
+        Tile w;
+        w.e = lo;
+        w.n0 = (int)(t % m_tiles) * 128;
+        const int begin = segment_at(a, lo), count = segment_at(a, lo + 1) - begin, n = first[lo + 1] - first[lo];
+        const int step = n < 8 ? ((count + n - 1) / n + 15) / 16 * 16 : kCap;  // at most kCap
+        w.p0 = begin + (tt - first[lo]) * step;
+        w.count = min(step, begin + count - w.p0);
+        return w;
+    };
+    bool ok = true;
+
+    if (warp == 16) {
+        // ------------------------------------------------- weight codes (TMA) --
+        if (lane == 0) {
+            int i = 0;
+            for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const Tile w = tile_at(t);
+                for (int k0 = 0; k0 < a.K && ok; k0 += 128, ++i) {
+                    const int s = i % C::kRaw;
+                    ok = mbar_wait(raw_empty(s), ((i / C::kRaw) & 1) ^ 1, kWaitNs, abort);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(raw_full(s), kRawBytes);
+                    tma_load_2d(raw_base + s * kRawBytes, &wmap, k0, w.e * a.N + w.n0, raw_full(s));
+                }
+            }
+        }
+    } else if (warp == 17) {
+        // ------------------------------------------------------------- MMA --
+        if (lane == 0) {
+            int g = 0, n = 0;
+            for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
+                const Tile w = tile_at(t);
+                const uint32_t cols = (w.count + 15) / 16 * 16;
+                const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u >> 4) << 24);
+                const int b = n & 1;
+                const uint32_t d = tmem + b * C::kDCols;
+                ok = mbar_wait(d_empty(b), ((n >> 1) & 1) ^ 1, kWaitNs, abort);
+                tc_fence_after();
+                for (int u = 0; u < units && ok; ++u, ++g) {
+                    const int s = g % C::kSlots;
+                    ok = mbar_wait(full(s), (g / C::kSlots) & 1, kWaitNs, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int steps = min(4, (a.K - u * kUnit + 15) / 16);
+                    const uint64_t bd = desc_sw128(b_base + s * C::kBBytes);
+                    for (int i = 0; i < steps; ++i)
+                        mma_f16_ts(d, tmem + C::kACol + s * 32 + i * 8, bd + (uint64_t)(i * 2), idesc, (u | i) != 0);
+                    mma_commit(empty(s));
+                }
+                if (ok) mma_commit(d_full(b));
+            }
+        }
+    } else if (warp < 4) {
+        // --------------------------------------------- weights to tensor memory --
+        const int r = warp * 32 + lane;
+        int i = 0, g = 0;
+        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int k0 = 0; k0 < a.K && ok; k0 += 128, ++i) {
+                const int rs = i % C::kRaw;
+                ok = mbar_wait(raw_full(rs), (i / C::kRaw) & 1, kWaitNs, abort);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const uint32_t row = raw_base + rs * kRawBytes + r * 128;
+                uint4 v[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
+                                 : "r"(row + ((c ^ (r & 7)) << 4)));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(raw_empty(rs));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (k0 + 64 * h >= a.K) break;
+                    uint32_t f[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        codes_to_f16(v[4 * h + c].x, f[8 * c], f[8 * c + 1]);
+                        codes_to_f16(v[4 * h + c].y, f[8 * c + 2], f[8 * c + 3]);
+                        codes_to_f16(v[4 * h + c].z, f[8 * c + 4], f[8 * c + 5]);
+                        codes_to_f16(v[4 * h + c].w, f[8 * c + 6], f[8 * c + 7]);
+                    }
+                    const int s = g % C::kSlots;
+                    ok = mbar_wait(empty(s), ((g / C::kSlots) & 1) ^ 1, kWaitNs, abort);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    tmem_st32(tmem + ((uint32_t)(warp * 32) << 16) + C::kACol + s * 32, f);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full(s));
+                    ++g;
+                }
+            }
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------- tokens to shared memory --
+        const int bw = warp - 4, sub = lane & 3;
+        int g = 0;
+        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const Tile w = tile_at(t);
+            const int8_t* src[C::kPasses];
+#pragma unroll
+            for (int i = 0; i < C::kPasses; ++i) {
+                const int row = i * 64 + bw * 8 + (lane >> 2);
+                const int r = row < w.count ? source_row(a, w.p0 + row) : -1;
+                src[i] = r >= 0 ? a.q + (long long)r * a.qs + sub * 16 : nullptr;
+            }
+            const int passes = (w.count + 63) / 64;
+            uint4 buf[kAhead][C::kPasses];
+            auto load = [&](uint4 (&v)[C::kPasses], int u) {
+                const int k = u * kUnit + sub * 16;
+#pragma unroll
+                for (int i = 0; i < C::kPasses; ++i) {
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (src[i] && k < a.K) v[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + u * kUnit));
+                }
+            };
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (j < units) load(buf[j], j);
+            for (int u0 = 0; u0 < units && ok; u0 += kAhead) {
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int u = u0 + j;
+                    if (u >= units || !ok) break;
+                    const int s = g % C::kSlots;
+                    ok = mbar_wait(empty(s), ((g / C::kSlots) & 1) ^ 1, kWaitNs, abort);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < C::kPasses; ++i) {
+                        if (i >= passes) break;
+                        uint32_t f[8];
+                        codes_to_f16(buf[j][i].x, f[0], f[1]);
+                        codes_to_f16(buf[j][i].y, f[2], f[3]);
+                        codes_to_f16(buf[j][i].z, f[4], f[5]);
+                        codes_to_f16(buf[j][i].w, f[6], f[7]);
+                        const int row = i * 64 + bw * 8 + (lane >> 2), x = row & 7;
+                        const uint32_t at = b_base + s * C::kBBytes + row * 128;
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * sub) ^ x) << 4)), "r"(f[0]),
+                                     "r"(f[1]), "r"(f[2]), "r"(f[3]) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * sub + 1) ^ x) << 4)),
+                                     "r"(f[4]), "r"(f[5]), "r"(f[6]), "r"(f[7]) : "memory");
+                    }
+                    if (u + kAhead < units) load(buf[j], u + kAhead);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full(s));
+                    ++g;
+                }
+            }
+        }
+    } else {
+        // -------------------------------------------------------- epilogue --
+        const int ew = warp - 12, et = tid - 12 * 32;
+        O* out = reinterpret_cast<O*>(a.out);
+        for (long long p = segment_at(a, a.E) + (long long)blockIdx.x; p < a.R; p += gridDim.x)
+            for (int n = et; n < a.N; n += 128) out[p * a.os + n] = from_f32<O>(0.f);
+        int n = 0;
+        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
+            const Tile w = tile_at(t);
+            const int b = n & 1;
+            float rs[kCap / 32];  // lane i: scale of rows i, 32 + i, ...
+#pragma unroll
+            for (int i = 0; i < kCap / 32; ++i) {
+                const int c = 32 * i + lane, r = c < w.count ? source_row(a, w.p0 + c) : -1;
+                rs[i] = r >= 0 ? a.scale[r] : 0.f;
+            }
+            const int ch = w.n0 + ew * 32 + lane;
+            const float cs = ch < a.N ? a.w_scale[(long long)w.e * a.N + ch] : 0.f;
+            ok = mbar_wait(d_full(b), (n >> 1) & 1, kWaitNs, abort);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            O* dst = out + (long long)w.p0 * a.os + ch;
+#pragma unroll
+            for (int i = 0; i < kCap / 32; ++i) {
+                const int c0 = 32 * i;
+                if (c0 >= w.count) break;
+                uint32_t v[32];
+                tmem_ld32(tmem + ((uint32_t)(ew * 32) << 16) + b * C::kDCols + c0, v);
+                tmem_ld_wait();
+                if (c0 + 32 >= w.count) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(d_empty(b));
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float s = __shfl_sync(0xFFFFFFFFu, rs[i], c);
+                    if (c0 + c < w.count && ch < a.N)
+                        dst[(long long)(c0 + c) * a.os] = from_f32<O>(__uint_as_float(v[c]) * s * cs);
+                }
+            }
+        }
+    }
+    if (!ok) {
+        *abort = 1;
+        raise_flag(&g_product_err, ERR_TIMEOUT);
+        spin_ns(20000000ull);  // copies in flight land
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 17) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int kCap, typename O>
+cudaError_t launch_cap(const Product& a, int grid, const CUtensorMap& map, cudaStream_t s) {
+    static std::mutex lock;
+    static bool ready[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    {
+        std::lock_guard<std::mutex> hold(lock);
+        if (dev >= 64 || !ready[dev]) {
+            e = cudaFuncSetAttribute(k_product_tc<kCap, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kCap>::kSmem);
+            if (e != cudaSuccess) return e;
+            if (dev < 64) ready[dev] = true;
+        }
+    }
+    return launch_pdl(k_product_tc<kCap, O>, dim3(grid), dim3(kThreads), Cfg<kCap>::kSmem, s, a, map);
+}
+
+template <typename O>
+cudaError_t launch_o(const Product& a, const CUtensorMap& map, cudaStream_t s) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const long long most = ((long long)a.R / 64 + (a.E < a.R ? a.E : a.R)) * ((a.N + 127) / 128);  // tiles, at most
+    const int grid = (int)(most < sms ? most : sms);
+    // Few rows an expert: short accumulators and a longer ring of weights.
+    return (long long)a.R <= 40LL * a.E ? launch_cap<64, O>(a, grid, map, s) : launch_cap<192, O>(a, grid, map, s);
+}
+
+}  // namespace
+
+bool product_tc_fits(const Product& a) {
+    return a.K % 16 == 0 && a.qs % 16 == 0 && (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.wq % 16 == 0;
+}
+
+cudaError_t launch_product_tc(const Product& a, moe_dtype out, cudaStream_t s) {
+    CUtensorMap map;
+    if (!make_byte_map(&map, a.wq, (uint64_t)a.K, (uint64_t)a.E * a.N, 128)) return cudaErrorInvalidValue;
+    if (out == MOE_F32) return launch_o<float>(a, map, s);
+    if (out == MOE_BF16) return launch_o<__nv_bfloat16>(a, map, s);
+    return launch_o<__half>(a, map, s);
+}
+
+}  // namespace moe
