@@ -13,6 +13,8 @@ import ctypes as C
 from dataclasses import dataclass
 from typing import Optional
 
+import torch
+
 from . import _build
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_OOM, MOE_ERR_CUDA, MOE_ERR_TIMEOUT = range(6)
@@ -113,14 +115,12 @@ def _check(status: int, layer_ptr=None):
 
 
 def _stream(stream) -> int:
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch.cuda.current_stream() without the Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t, dtype, shape=None, name="tensor"):
-    import torch
     if t is None:
         raise ValueError(f"{name} is None")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -135,16 +135,17 @@ def _ptr(t, dtype, shape=None, name="tensor"):
 
 
 MOE_F32, MOE_BF16, MOE_F16 = range(3)
+_ROW_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.int8: None}
 
 
 def _rows(t, name, rows=None, width=None):
-    """(pointer, moe_dtype, stride) of a 2-D CUDA tensor of rows whose elements are adjacent."""
-    import torch
+    """(pointer, moe_dtype, stride) of a 2-D CUDA tensor of rows whose elements
+    are adjacent; the moe_dtype of int8 rows is None."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.int8: None}.get(t.dtype, -1)
-    if code == -1 or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D tensor of float32, bfloat16 or float16 rows, got {t.dtype} {tuple(t.shape)}")
+    if t.dim() != 2 or t.dtype not in _ROW_TYPES:
+        raise ValueError(f"{name} must be a 2-D tensor of rows in float32, bfloat16, float16 or int8, "
+                         f"got {t.dtype} {tuple(t.shape)}")
     n, m = t.shape
     if (rows is not None and n != rows) or (width is not None and m != width):
         raise ValueError(f"{name} must have shape ({n if rows is None else rows}, {m if width is None else width}), "
@@ -152,11 +153,10 @@ def _rows(t, name, rows=None, width=None):
     step, inner = t.stride()
     if m > 1 and inner != 1:
         raise ValueError(f"the elements of a row of {name} must be adjacent")
-    return t.data_ptr(), code, (step if n > 1 else m)
+    return t.data_ptr(), _ROW_TYPES[t.dtype], (step if n > 1 else m)
 
 
 def _hptr(t, dtype, shape, name):
-    import torch
     if not isinstance(t, torch.Tensor) or t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous host {dtype} tensor")
     if tuple(t.shape) != tuple(shape):
@@ -205,7 +205,6 @@ def moe_workspace_bytes(cfg: MoeConfig) -> int:
 def moe_create(cfg: MoeConfig, weights: dict, stream=None) -> Layer:
     """weights: dict of CUDA tensors named as the fields of moe_weights (uint8;
     NVFP4 layers also float32 gate_g, up_g, down_g [E])."""
-    import torch
     lib = load_library()
     H, I, E = cfg.hidden, cfg.inter, cfg.n_experts
     nv = cfg.weight_format == MOE_WEIGHTS_NVFP4
@@ -292,7 +291,6 @@ def moe_set_stage_events(layer: Layer, events):
 
 
 def moe_route(layer: Layer, logits, ids, w, stream=None):
-    import torch
     T = logits.shape[0]
     c = layer.cfg
     st = load_library().moe_route(layer.ptr, _ptr(logits, torch.float32, (T, c.n_experts), "logits"), T,
@@ -302,7 +300,6 @@ def moe_route(layer: Layer, logits, ids, w, stream=None):
 
 
 def moe_route_hash(layer: Layer, token_ids, tid2eid, ids, w, stream=None):
-    import torch
     T = token_ids.shape[0]
     V = tid2eid.shape[0]
     c = layer.cfg
@@ -314,7 +311,6 @@ def moe_route_hash(layer: Layer, token_ids, tid2eid, ids, w, stream=None):
 
 
 def moe_permute(layer: Layer, ids, offsets, row_src, row_dst, stream=None):
-    import torch
     T = ids.shape[0]
     c = layer.cfg
     R = T * c.top_k
@@ -328,7 +324,6 @@ def moe_permute(layer: Layer, ids, offsets, row_src, row_dst, stream=None):
 def moe_permute_noalloc(ids, n_experts: int, offsets, row_src, row_dst, stream=None):
     """The grouping of moe_permute without a layer and without allocating
     (scratch in a static device array; T * top_k <= 65536)."""
-    import torch
     T, k = ids.shape
     R = T * k
     st = load_library().moe_permute_noalloc(
@@ -340,7 +335,6 @@ def moe_permute_noalloc(ids, n_experts: int, offsets, row_src, row_dst, stream=N
 
 
 def moe_quantize(layer: Layer, x, q, s, stream=None):
-    import torch
     T = x.shape[0]
     H = layer.cfg.hidden
     st = load_library().moe_quantize(layer.ptr, _ptr(x, torch.int16, (T, H), "x"), T,
@@ -351,7 +345,6 @@ def moe_quantize(layer: Layer, x, q, s, stream=None):
 
 def moe_forward(layer: Layer, x, ids, w, out, stream=None):
     """x: int16 CUDA tensor [T][H] holding bf16 bits (or a bfloat16 tensor)."""
-    import torch
     T = x.shape[0]
     c = layer.cfg
     if x.dtype == torch.bfloat16:
@@ -365,7 +358,6 @@ def moe_forward(layer: Layer, x, ids, w, out, stream=None):
 
 def moe_route_forward(layer: Layer, logits, x, ids, w, out, stream=None):
     """Routing and layer in one call (ids, w and out are written)."""
-    import torch
     T = x.shape[0]
     c = layer.cfg
     if x.dtype == torch.bfloat16:
@@ -380,7 +372,6 @@ def moe_route_forward(layer: Layer, logits, x, ids, w, out, stream=None):
 
 def moe_forward_host(layer: Layer, x, logits, out, stream=None):
     """Host tensors (pinned for overlap): x int16 [T][H], logits f32 [T][E], out f32 [T][H]."""
-    import torch
     T = x.shape[0]
     c = layer.cfg
     st = load_library().moe_forward_host(layer.ptr, _hptr(x, torch.int16, (T, c.hidden), "x"),
@@ -391,7 +382,6 @@ def moe_forward_host(layer: Layer, x, logits, out, stream=None):
 
 
 def moe_hidden(layer: Layer, T: int, hq, hs, stream=None):
-    import torch
     c = layer.cfg
     R = T * c.top_k
     st = load_library().moe_hidden(layer.ptr, T, _ptr(hq, torch.uint8, (R, c.inter), "hq"),
@@ -408,7 +398,6 @@ def moe_check(layer: Layer, stream=None) -> int:
 
 def moe_set_trace(layer: Layer, buf):
     """buf: CUDA int64 tensor of >= max(48 * num_sms + 4, 8 * num_sms + 1024) entries, or None."""
-    import torch
     if buf is None:
         _check(load_library().moe_set_trace(layer.ptr, None, 0), layer.ptr)
         return
@@ -427,7 +416,6 @@ def moe_last_error(layer: Optional[Layer] = None) -> str:
 
 def _slots(row_dst, T, name="row_dst"):
     """(pointer, top_k) of the slots [T][top_k], also given flat."""
-    import torch
     n = row_dst.numel()
     if T < 1 or n % T or not 1 <= n // T <= 8:
         raise ValueError(f"{name} must hold T * top_k positions with top_k in [1, 8], got {n} for T = {T}")
@@ -438,7 +426,6 @@ def moe_dispatch(x, offsets, row_dst, xs, stream=None):
     """xs[row_dst[t, j]] = x[t]; zeros past the last placed row.  x [T][H] and
     xs [T * top_k][H] in one of float32, bfloat16, float16; offsets [E + 1] and
     row_dst [T * top_k] as moe_permute writes them."""
-    import torch
     T, H = x.shape
     if T == 0:
         return
@@ -466,7 +453,6 @@ def moe_dispatch_backward(dxs, row_dst, dx, stream=None):
 
 def moe_combine(y, w, row_dst, out, stream=None):
     """out[t] = sum_j w[t, j] * y[row_dst[t, j]]; out in y's dtype or float32."""
-    import torch
     T, H = out.shape
     if T == 0:
         return
@@ -482,7 +468,6 @@ def moe_combine(y, w, row_dst, out, stream=None):
 def moe_combine_backward(dout, y, w, offsets, row_dst, dy, dw, stream=None):
     """dy[row_dst[t, j]] = w[t, j] * dout[t] (zeros past the last placed row)
     and dw[t, j] = <dout[t], y[row_dst[t, j]]>; dout in y's dtype or float32."""
-    import torch
     T, H = dout.shape
     if T == 0:
         return
@@ -499,7 +484,6 @@ def moe_combine_backward(dout, y, w, offsets, row_dst, dy, dw, stream=None):
 
 def moe_route_backward(logits, ids, dw, dlogits, w_scale: float = 1.5, stream=None):
     """Gradient of moe_route's weights: dlogits [T][E] from dw [T][k]."""
-    import torch
     T, E = logits.shape
     k = ids.shape[1]
     if T == 0:
@@ -513,7 +497,6 @@ def moe_route_backward(logits, ids, dw, dlogits, w_scale: float = 1.5, stream=No
 def moe_quantize_rows(x, q, scale, gated: bool = False, stream=None):
     """x [rows][K] (gated: [rows][2 K], SiLU of the first half times the second)
     to int8 q [rows][K] with one float32 scale a row."""
-    import torch
     rows, K = q.shape
     if rows == 0:
         return
@@ -530,7 +513,6 @@ def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, t
     e's segment; r = row_src[p] // top_k, or p without row_src.  q [rows][K] and
     wq [E][N][K] int8, w_scale [E][N], out [R][N]; offsets [E + 1] may be left
     out with one expert."""
-    import torch
     R, N = out.shape
     if R == 0:
         return

@@ -9,15 +9,15 @@
 //
 // One CTA per SM walks tiles of 128 output channels (A, one tensor-memory lane
 // a channel) x up to kCap positions of one segment (B).  K goes in units of 64:
-//   warp 16      TMA of 128 channels x 128 bytes of codes into a ring
-//   warps 0-3    codes of one channel a thread -> fp16 -> tensor memory (A
-//                operand: it takes no shared-memory bandwidth from B)
-//   warps 4-11   token codes: global -> registers (kAhead units ahead) -> fp16
-//                -> shared memory, rows of 128 bytes, 128-byte swizzle; the
-//                token row is looked up here, so that a gather costs nothing
-//   warp 17      one thread issues the MMAs (N = the tile's rows rounded to 16)
-//   warps 12-15  accumulators -> scales -> out, while the next tile is summed
-//                (two accumulators)
+//   kAGroups warpgroups  codes of one channel a thread -> fp16 -> tensor memory
+//                        (the A operand: it takes no shared-memory bandwidth from B)
+//   kBWarps warps        token codes: global -> registers (kAhead units ahead) ->
+//                        fp16 -> shared memory, rows of 128 bytes, 128-byte swizzle;
+//                        the token row is looked up here: a gather costs nothing
+//   4 warps              accumulators -> scales -> out, while the next tile is
+//                        summed (two accumulators)
+//   1 thread             TMA of 128 channels x 128 bytes of codes into a ring
+//   1 thread             the MMAs (N = the tile's rows rounded to 16)
 #include <cuda.h>
 
 #include <mutex>
@@ -34,7 +34,6 @@ namespace {
 using namespace tc;
 
 constexpr int kUnit = 64;             // K of one unit (128 bytes of fp16)
-constexpr int kThreads = 18 * 32;
 constexpr int kRawBytes = 128 * 128;  // one ring slot of weight codes
 constexpr int kAhead = 3;             // units of token codes held in registers
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -44,19 +43,42 @@ struct Cfg {
     static constexpr int kBBytes = kCap * 128;           // one unit of tokens in fp16
     static constexpr int kSlots = kCap > 64 ? 4 : 8;     // units in flight to the MMA
     static constexpr int kRaw = kCap > 64 ? 7 : 9;       // weight ring
-    static constexpr int kPasses = kCap / 64;            // 64 token rows a pass of the loaders
+    static constexpr int kAGroups = kCap > 64 ? 2 : 4;   // warpgroups that turn weights
+    static constexpr int kBWarps = kCap > 64 ? 8 : 4;    // warps that turn tokens
+    static constexpr int kPasses = kCap / (8 * kBWarps); // 8 token rows a warp and pass
+    static constexpr int kAWarps = 4 * kAGroups;
+    static constexpr int kEpi = kAWarps + kBWarps;       // first epilogue warp; then TMA, then MMA
+    static constexpr int kThreads = (kEpi + 6) * 32;
     static constexpr int kACol = 512 - 32 * kSlots;      // tensor-memory column of the A units
     static constexpr int kDCols = kCap > 64 ? 192 : 64;  // columns of one accumulator
     static constexpr int kSmem = 1024 + kSlots * kBBytes + kRaw * kRawBytes;
     static_assert(kCap % 64 == 0 && 2 * kDCols <= kACol && kCap <= kDCols, "tensor memory");
 };
 
-// D[tmem] (+)= A[tmem] B[smem]^T, fp16 operands, fp32 accumulators.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// One lane of the warp, the same one each time: 1 there, 0 elsewhere.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r;
+}
+
+// D[tmem] (+)= A[tmem] B[smem]^T, fp16 operands, fp32 accumulators; called by the
+// whole warp, issued by the lane with `on`.  Under an `if` on the lane instead,
+// the operands are no longer uniform over the warp and an issue takes 147
+// cycles whatever N is; so it takes 60 for N <= 64 and N / 2 above (measured).
+__device__ __forceinline__ void mma_f16_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_by(uint32_t on, uint32_t bar) {
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar), "r"(on)
         : "memory");
 }
 
@@ -88,6 +110,14 @@ __device__ __forceinline__ void codes_to_f16(uint32_t v, uint32_t& lo, uint32_t&
     hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// 16 bytes, or zeros; volatile, so that it is issued here and not at its use.
+__device__ __forceinline__ void ld_ahead(uint4& v, const int8_t* p, bool on) {
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %5, 0;\nmov.b32 %0, 0;\nmov.b32 %1, 0;\nmov.b32 %2, 0;\nmov.b32 %3, 0;\n"
+        "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)on));
+}
+
 struct Tile {
     int e, n0, p0, count;
 };
@@ -95,7 +125,7 @@ struct Tile {
 __device__ uint32_t g_product_err;
 
 template <int kCap, typename O>
-__global__ void __launch_bounds__(kThreads, 1) k_product_tc(const Product a, const __grid_constant__ CUtensorMap wmap) {
+__global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Product a, const __grid_constant__ CUtensorMap wmap) {
     using C = Cfg<kCap>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[2 * C::kRaw + 2 * C::kSlots + 4];
@@ -119,10 +149,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_product_tc(const Product a, con
     if (tid == 0) {
         for (int i = 0; i < C::kRaw; ++i) {
             mbar_init(raw_full(i), 1);
-            mbar_init(raw_empty(i), 4);
+            mbar_init(raw_empty(i), 8);
         }
         for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(full(i), 12);
+            mbar_init(full(i), 4 + C::kBWarps);
             mbar_init(empty(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -133,13 +163,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_product_tc(const Product a, con
         fence_mbar_init();
         prefetch_tmap(&wmap);
     }
-    if (warp == 17) tmem_alloc(smem_u32(&tmem_slot), 512);
+    if (warp == C::kEpi + 5) tmem_alloc(smem_u32(&tmem_slot), 512);
     pdl_wait();
 
     // token tiles of every expert: ceil(count / kCap) of nearly equal size
     {
         int mine = 0;
-        const int per = (a.E + kThreads - 1) / kThreads;
+        const int per = (a.E + C::kThreads - 1) / C::kThreads;
         for (int i = 0; i < per; ++i) {
             const int e = tid * per + i;
             if (e < a.E) mine += (max(segment_at(a, e + 1) - segment_at(a, e), 0) + kCap - 1) / kCap;
@@ -190,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_product_tc(const Product a, con
     };
     bool ok = true;
 
-    if (warp == 16) {
+    if (warp == C::kEpi + 4) {
         // ------------------------------------------------- weight codes (TMA) --
         if (lane == 0) {
             int i = 0;
@@ -205,98 +235,100 @@ __global__ void __launch_bounds__(kThreads, 1) k_product_tc(const Product a, con
                 }
             }
         }
-    } else if (warp == 17) {
+    } else if (warp == C::kEpi + 5) {
         // ------------------------------------------------------------- MMA --
-        if (lane == 0) {
-            int g = 0, n = 0;
-            for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
-                const Tile w = tile_at(t);
-                const uint32_t cols = (w.count + 15) / 16 * 16;
-                const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u >> 4) << 24);
-                const int b = n & 1;
-                const uint32_t d = tmem + b * C::kDCols;
-                ok = mbar_wait(d_empty(b), ((n >> 1) & 1) ^ 1, kWaitNs, abort);
+        const uint32_t on = elect_lane();
+        int g = 0, n = 0;
+        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
+            const uint32_t cols = (tile_at(t).count + 15) / 16 * 16;
+            const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u >> 4) << 24);
+            const int b = n & 1;
+            const uint32_t d = tmem + b * C::kDCols;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(d_empty(b), ((n >> 1) & 1) ^ 1, kWaitNs, abort));
+            tc_fence_after();
+            for (int u = 0; u < units && ok; ++u, ++g) {
+                const int s = g % C::kSlots;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full(s), (g / C::kSlots) & 1, kWaitNs, abort));
+                if (!ok) break;
+                // the loaders' stores, seen through the barrier, before the MMA's own reads; the
+                // fence stands here because there it would wait for the loads that run ahead
+                fence_async_shared();
                 tc_fence_after();
-                for (int u = 0; u < units && ok; ++u, ++g) {
-                    const int s = g % C::kSlots;
-                    ok = mbar_wait(full(s), (g / C::kSlots) & 1, kWaitNs, abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const int steps = min(4, (a.K - u * kUnit + 15) / 16);
-                    const uint64_t bd = desc_sw128(b_base + s * C::kBBytes);
-                    for (int i = 0; i < steps; ++i)
-                        mma_f16_ts(d, tmem + C::kACol + s * 32 + i * 8, bd + (uint64_t)(i * 2), idesc, (u | i) != 0);
-                    mma_commit(empty(s));
+                const uint64_t bd = desc_sw128(b_base + s * C::kBBytes);
+                const uint32_t ad = tmem + C::kACol + s * 32;
+                if (a.K - u * kUnit >= kUnit) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mma_f16_ts(on, d, ad + i * 8, bd + (uint64_t)(i * 2), idesc, (u | i) != 0);
+                } else {
+                    for (int i = 0; i < (a.K - u * kUnit + 15) / 16; ++i)
+                        mma_f16_ts(on, d, ad + i * 8, bd + (uint64_t)(i * 2), idesc, (u | i) != 0);
                 }
-                if (ok) mma_commit(d_full(b));
+                mma_commit_by(on, empty(s));
             }
+            if (ok) mma_commit_by(on, d_full(b));
         }
-    } else if (warp < 4) {
+    } else if (warp < C::kAWarps) {
         // --------------------------------------------- weights to tensor memory --
-        const int r = warp * 32 + lane;
-        int i = 0, g = 0;
-        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            for (int k0 = 0; k0 < a.K && ok; k0 += 128, ++i) {
-                const int rs = i % C::kRaw;
+        // group q of kAGroups takes the units u = q, q + kAGroups, ... of a tile;
+        // two units share a ring slot, each of them frees half of it
+        const int lanes = (warp & 3) * 32, r = lanes + lane, group = warp >> 2;
+        int i0 = 0, g0 = 0;
+        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x, i0 += (units + 1) / 2, g0 += units) {
+            for (int u = group; u < units; u += C::kAGroups) {
+                const int i = i0 + (u >> 1), rs = i % C::kRaw, g = g0 + u, s = g % C::kSlots;
                 ok = mbar_wait(raw_full(rs), (i / C::kRaw) & 1, kWaitNs, abort);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 const uint32_t row = raw_base + rs * kRawBytes + r * 128;
-                uint4 v[8];
+                uint4 v[4];
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
+                for (int c = 0; c < 4; ++c)
                     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                                  : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
-                                 : "r"(row + ((c ^ (r & 7)) << 4)));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(raw_empty(rs));
+                                 : "r"(row + (((4 * (u & 1) + c) ^ (r & 7)) << 4)));
+                uint32_t f[32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (k0 + 64 * h >= a.K) break;
-                    uint32_t f[32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        codes_to_f16(v[4 * h + c].x, f[8 * c], f[8 * c + 1]);
-                        codes_to_f16(v[4 * h + c].y, f[8 * c + 2], f[8 * c + 3]);
-                        codes_to_f16(v[4 * h + c].z, f[8 * c + 4], f[8 * c + 5]);
-                        codes_to_f16(v[4 * h + c].w, f[8 * c + 6], f[8 * c + 7]);
-                    }
-                    const int s = g % C::kSlots;
-                    ok = mbar_wait(empty(s), ((g / C::kSlots) & 1) ^ 1, kWaitNs, abort);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    tmem_st32(tmem + ((uint32_t)(warp * 32) << 16) + C::kACol + s * 32, f);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full(s));
-                    ++g;
+                for (int c = 0; c < 4; ++c) {
+                    codes_to_f16(v[c].x, f[8 * c], f[8 * c + 1]);
+                    codes_to_f16(v[c].y, f[8 * c + 2], f[8 * c + 3]);
+                    codes_to_f16(v[c].z, f[8 * c + 4], f[8 * c + 5]);
+                    codes_to_f16(v[c].w, f[8 * c + 6], f[8 * c + 7]);
                 }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(raw_empty(rs));
+                    if (u == units - 1 && !(u & 1)) mbar_arrive(raw_empty(rs));  // no second unit
+                }
+                ok = mbar_wait(empty(s), ((g / C::kSlots) & 1) ^ 1, kWaitNs, abort);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                tmem_st32(tmem + ((uint32_t)lanes << 16) + C::kACol + s * 32, f);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full(s));
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < C::kEpi) {
         // ------------------------------------------- tokens to shared memory --
-        const int bw = warp - 4, sub = lane & 3;
+        const int bw = warp - C::kAWarps, sub = lane & 3;
         int g = 0;
         for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             const Tile w = tile_at(t);
             const int8_t* src[C::kPasses];
 #pragma unroll
             for (int i = 0; i < C::kPasses; ++i) {
-                const int row = i * 64 + bw * 8 + (lane >> 2);
+                const int row = (i * C::kBWarps + bw) * 8 + (lane >> 2);
                 const int r = row < w.count ? source_row(a, w.p0 + row) : -1;
                 src[i] = r >= 0 ? a.q + (long long)r * a.qs + sub * 16 : nullptr;
             }
-            const int passes = (w.count + 63) / 64;
+            const int passes = (w.count + 8 * C::kBWarps - 1) / (8 * C::kBWarps);
             uint4 buf[kAhead][C::kPasses];
             auto load = [&](uint4 (&v)[C::kPasses], int u) {
                 const int k = u * kUnit + sub * 16;
 #pragma unroll
-                for (int i = 0; i < C::kPasses; ++i) {
-                    v[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (src[i] && k < a.K) v[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + u * kUnit));
-                }
+                for (int i = 0; i < C::kPasses; ++i) ld_ahead(v[i], src[i] + u * kUnit, src[i] != nullptr && k < a.K);
             };
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
@@ -318,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_product_tc(const Product a, con
                         codes_to_f16(buf[j][i].y, f[2], f[3]);
                         codes_to_f16(buf[j][i].z, f[4], f[5]);
                         codes_to_f16(buf[j][i].w, f[6], f[7]);
-                        const int row = i * 64 + bw * 8 + (lane >> 2), x = row & 7;
+                        const int row = (i * C::kBWarps + bw) * 8 + (lane >> 2), x = row & 7;
                         const uint32_t at = b_base + s * C::kBBytes + row * 128;
                         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * sub) ^ x) << 4)), "r"(f[0]),
                                      "r"(f[1]), "r"(f[2]), "r"(f[3]) : "memory");
@@ -326,7 +358,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_product_tc(const Product a, con
                                      "r"(f[4]), "r"(f[5]), "r"(f[6]), "r"(f[7]) : "memory");
                     }
                     if (u + kAhead < units) load(buf[j], u + kAhead);
-                    fence_async_shared();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full(s));
                     ++g;
@@ -335,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_product_tc(const Product a, con
         }
     } else {
         // -------------------------------------------------------- epilogue --
-        const int ew = warp - 12, et = tid - 12 * 32;
+        const int ew = warp - C::kEpi, et = tid - C::kEpi * 32;
         O* out = reinterpret_cast<O*>(a.out);
         for (long long p = segment_at(a, a.E) + (long long)blockIdx.x; p < a.R; p += gridDim.x)
             for (int n = et; n < a.N; n += 128) out[p * a.os + n] = from_f32<O>(0.f);
@@ -384,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_product_tc(const Product a, con
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 17) {
+    if (warp == C::kEpi + 5) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -405,7 +436,7 @@ cudaError_t launch_cap(const Product& a, int grid, const CUtensorMap& map, cudaS
             if (dev < 64) ready[dev] = true;
         }
     }
-    return launch_pdl(k_product_tc<kCap, O>, dim3(grid), dim3(kThreads), Cfg<kCap>::kSmem, s, a, map);
+    return launch_pdl(k_product_tc<kCap, O>, dim3(grid), dim3(Cfg<kCap>::kThreads), Cfg<kCap>::kSmem, s, a, map);
 }
 
 template <typename O>

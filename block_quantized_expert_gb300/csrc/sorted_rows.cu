@@ -21,9 +21,41 @@ namespace moe {
 
 namespace {
 
+// A token's filled slots: pos[a] and wt[a] for a < m, in ascending position;
+// w = nullptr stands for ones.
+struct Slots {
+    int m;
+    int pos[kMaxTopK];
+    float wt[kMaxTopK];
+};
+
+// Written by one warp: lane j < k ranks its own position among the others.  The
+// block synchronises before it reads them.
+__device__ __forceinline__ void find_slots(Slots& s, const int32_t* row_dst, const float* w, long long t, int k, int R) {
+    constexpr unsigned kAll = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31;
+    const int p = lane < k ? row_dst[t * k + lane] : -1;
+    const bool on = p >= 0 && p < R;
+    const float wj = on && w ? w[t * k + lane] : 1.f;
+    const unsigned filled = __ballot_sync(kAll, on);
+    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxTopK; ++i) {
+        const int q = __shfl_sync(kAll, p, i);
+        if (((filled >> i) & 1u) && (q < p || (q == p && i < lane))) ++rank;
+    }
+    if (on) {
+        s.pos[rank] = p;
+        s.wt[rank] = wj;
+    }
+    if (lane == 0) s.m = __popc(filled);
+}
+
 // ---------------------------------------------------------------- dispatch --
 // xs[row_dst[t, j]] = x[t], in words of V: types do not matter to a copy.
-// Reads T H, writes R H elements.
+// Block (t, y) moves the words y * 128 + i, + 128 gridDim.y, ... of token t, one
+// word a thread.  Reads T H, writes R H elements; at T = 8192, k = 6, H = 4096,
+// bf16: 71.7 us, 6.6 TB/s (four words a thread: 73.6).
 template <typename V>
 __global__ void __launch_bounds__(128) k_dispatch(const char* __restrict__ x, long long x_pitch, int T, int k,
                                                   int words, const int32_t* __restrict__ placed,
@@ -31,70 +63,85 @@ __global__ void __launch_bounds__(128) k_dispatch(const char* __restrict__ x, lo
                                                   long long xs_pitch) {
     pdl_launch_dependents();
     pdl_wait();
-    const long long R = (long long)T * k;
-    for (long long t = blockIdx.x; t < T; t += gridDim.x) {
-        const V* src = reinterpret_cast<const V*>(x + t * x_pitch);
-        for (int c = threadIdx.x; c < words; c += blockDim.x) {
-            const V v = src[c];
-            for (int j = 0; j < k; ++j) {
-                const long long p = row_dst[t * k + j];
-                if (p >= 0 && p < R) reinterpret_cast<V*>(xs + p * xs_pitch)[c] = v;
-            }
+    const int R = T * k, first = blockIdx.y * 128 + threadIdx.x, step = gridDim.y * 128;
+    const long long t = blockIdx.x;
+    const V* src = reinterpret_cast<const V*>(x + t * x_pitch);
+    for (int c = first; c < words; c += step) {
+        const V v = src[c];
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j) {
+            if (j >= k) break;
+            const int p = row_dst[t * k + j];
+            if (p >= 0 && p < R) reinterpret_cast<V*>(xs + (long long)p * xs_pitch)[c] = v;
         }
     }
     // positions past the last placed row
     const V zero = V();
-    for (long long p = max(*placed, 0) + (long long)blockIdx.x; p < R; p += gridDim.x)
-        for (int c = threadIdx.x; c < words; c += blockDim.x) reinterpret_cast<V*>(xs + p * xs_pitch)[c] = zero;
+    for (long long p = max(*placed, 0) + t; p < R; p += gridDim.x)
+        for (int c = first; c < words; c += step) reinterpret_cast<V*>(xs + p * xs_pitch)[c] = zero;
 }
 
 // ----------------------------------------------------------------- combine --
 // out[t] = sum_j w[t, j] y[row_dst[t, j]] over the filled slots in ascending
 // position, which is ascending expert id, the order of the layer's own
-// combine; w = NULL stands for ones (the gradient of dispatch).  The sum is
-// held in fp32 and rounded once.
-template <typename A, typename O, int C>
+// combine; w = NULL stands for ones (the gradient of dispatch).  All rows of a
+// chunk are on their way before the first is added; the sum is held in fp32
+// and rounded once.  T = 8192, k = 6, H = 4096, bf16: 88 us to fp32 and 78.5 us
+// to bf16, 6.0 to 6.1 TB/s; with one chunk a thread instead of four, 115 and 101:
+// a block waits for its token's positions first.  Several tokens a block, their
+// positions looked up together, gave the same 88.
+template <typename A, typename O, int C, int U>
 __global__ void __launch_bounds__(128) k_combine_rows(const A* __restrict__ y, long long ys,
                                                       const float* __restrict__ w, int T, int k, int H,
                                                       const int32_t* __restrict__ row_dst, O* __restrict__ out,
                                                       long long os) {
     pdl_launch_dependents();
     pdl_wait();
-    const long long R = (long long)T * k;
-    for (long long t = blockIdx.x; t < T; t += gridDim.x) {
-        long long pos[kMaxTopK];
-        float wt[kMaxTopK];
-        int m = 0;  // filled slots, kept sorted by position
-        for (int j = 0; j < k; ++j) {
-            const long long p = row_dst[t * k + j];
-            if (p < 0 || p >= R) continue;
-            int a = m++;
-            for (; a > 0 && pos[a - 1] > p; --a) {
-                pos[a] = pos[a - 1];
-                wt[a] = wt[a - 1];
-            }
-            pos[a] = p;
-            wt[a] = w ? w[t * k + j] : 1.f;
-        }
-        for (int c = threadIdx.x * C; c < H; c += blockDim.x * C) {
-            float acc[C];
+    __shared__ Slots s;
+    const long long t = blockIdx.x;
+    if (threadIdx.x < 32) find_slots(s, row_dst, w, t, k, T * k);
+    __syncthreads();
+    const int m = s.m;
+    O* dst = out + t * os;
+    for (int c0 = (blockIdx.y * 128 * U + threadIdx.x) * C; c0 < H; c0 += gridDim.y * 128 * U * C) {
+        Chunk<A, C> v[U][kMaxTopK];
 #pragma unroll
-            for (int i = 0; i < C; ++i) acc[i] = 0.f;
-            for (int a = 0; a < m; ++a) {
-                const Chunk<A, C> v = load_chunk<A, C>(y + pos[a] * ys + c);
+        for (int a = 0; a < kMaxTopK; ++a)
+            if (a < m) {
+                const A* row = y + s.pos[a] * ys + c0;
 #pragma unroll
-                for (int i = 0; i < C; ++i) acc[i] += wt[a] * to_f32(v.v[i]);
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * 128 * C < H) v[u][a] = load_chunk<A, C>(row + u * 128 * C);
             }
-            store_chunk<O, C>(out + t * os + c, acc);
-        }
+        float acc[U][C];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < C; ++i) acc[u][i] = 0.f;
+#pragma unroll
+        for (int a = 0; a < kMaxTopK; ++a)
+            if (a < m) {
+                const float wt = s.wt[a];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < C; ++i) acc[u][i] += wt * to_f32(v[u][a].v[i]);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + u * 128 * C < H) store_chunk<O, C>(dst + c0 + u * 128 * C, acc[u]);
     }
 }
 
 // -------------------------------------------------------- combine_backward --
 // dy[row_dst[t, j]] = w[t, j] dout[t] and dw[t, j] = <dout[t], y[row_dst[t, j]]>
-// (0 for an empty slot): one block a token, dout[t] read once; the dot products
-// are fp32 sums joined by shuffles and then in warp order.
-template <typename A, typename O, int C>
+// (0 for an empty slot).  kGroup warps a slot walk its row of y once, U chunks on
+// their way at a time; the slots of a token stand next to each other, so that
+// dout[t] comes from L1 but once.  The dot product is a fp32 sum a lane, joined
+// by shuffles, then in warp order.  T = 8192, k = 6, H = 4096, bf16, with the
+// router's gradient: 133 us, 6.6 TB/s (one block a token with the k rows of a chunk
+// in flight: 154 to 270).
+template <typename A, typename O, int C, int U, int kGroup>
 __global__ void __launch_bounds__(256) k_combine_backward(const O* __restrict__ dout, long long ds,
                                                           const A* __restrict__ y, long long ys,
                                                           const float* __restrict__ w, int T, int k, int H,
@@ -103,50 +150,56 @@ __global__ void __launch_bounds__(256) k_combine_backward(const O* __restrict__ 
                                                           long long dys, float* __restrict__ dw) {
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ float part[8][kMaxTopK];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const long long R = (long long)T * k;
-    for (long long t = blockIdx.x; t < T; t += gridDim.x) {
-        float dot[kMaxTopK];
+    __shared__ float part[8];
+    constexpr int kStep = 32 * kGroup * C;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first = (threadIdx.x % (32 * kGroup)) * C;
+    const int R = T * k;
+    const long long r = (long long)blockIdx.x * (8 / kGroup) + warp / kGroup;  // slot
+    const int p = r < R ? row_dst[r] : -1;
+    const bool on = p >= 0 && p < R;
+    float dot = 0.f;
+    if (on) {
+        const float wt = w[r];
+        const O* drow = dout + r / k * ds;
+        const A* yrow = y + p * ys;
+        A* grow = dy + p * dys;
+        for (int c0 = first; c0 < H; c0 += U * kStep) {
+            Chunk<O, C> d[U];
+            Chunk<A, C> v[U];
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j) dot[j] = 0.f;
-        for (int c = threadIdx.x * C; c < H; c += blockDim.x * C) {
-            const Chunk<O, C> d = load_chunk<O, C>(dout + t * ds + c);
-#pragma unroll
-            for (int j = 0; j < kMaxTopK; ++j) {
-                if (j >= k) break;
-                const long long p = row_dst[t * k + j];
-                if (p < 0 || p >= R) continue;
-                const float wt = w[t * k + j];
-                const Chunk<A, C> v = load_chunk<A, C>(y + p * ys + c);
-                float g[C];
-#pragma unroll
-                for (int i = 0; i < C; ++i) {
-                    const float f = to_f32(d.v[i]);
-                    dot[j] += f * to_f32(v.v[i]);
-                    g[i] = wt * f;
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * kStep < H) {
+                    v[u] = load_chunk<A, C>(yrow + c0 + u * kStep);
+                    d[u] = load_chunk<O, C>(drow + c0 + u * kStep);
                 }
-                store_chunk<A, C>(dy + p * dys + c, g);
-            }
-        }
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j) {
-            const float s = warp_sum(dot[j]);
-            if (lane == 0) part[warp][j] = s;
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * kStep < H) {
+                    float g[C];
+#pragma unroll
+                    for (int i = 0; i < C; ++i) {
+                        const float f = to_f32(d[u].v[i]);
+                        dot += f * to_f32(v[u].v[i]);
+                        g[i] = wt * f;
+                    }
+                    store_chunk<A, C>(grow + c0 + u * kStep, g);
+                }
         }
-        __syncthreads();
-        if (threadIdx.x < (unsigned)k) {
-            float s = 0.f;
-            for (int a = 0; a < warps; ++a) s += part[a][threadIdx.x];
-            dw[t * k + threadIdx.x] = s;
-        }
-        __syncthreads();
     }
+    dot = warp_sum(dot);
+    if (kGroup > 1) {
+        if (lane == 0) part[warp] = dot;
+        __syncthreads();
+        dot = 0.f;
+        for (int a = 0; a < kGroup; ++a) dot += part[warp / kGroup * kGroup + a];
+    }
+    if (r < R && threadIdx.x % (32 * kGroup) == 0) dw[r] = dot;
     float zero[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) zero[i] = 0.f;
-    for (long long p = max(*placed, 0) + (long long)blockIdx.x; p < R; p += gridDim.x)
-        for (int c = threadIdx.x * C; c < H; c += blockDim.x * C) store_chunk<A, C>(dy + p * dys + c, zero);
+    for (long long q = max(*placed, 0) + r; q < R; q += (long long)gridDim.x * (8 / kGroup))
+        for (int c = first; c < H; c += kStep) store_chunk<A, C>(dy + q * dys + c, zero);
 }
 
 // ---------------------------------------------------------- route_backward --
@@ -216,7 +269,7 @@ moe_status launched(cudaError_t e, const char* what) {
     return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// The checks that every entry shares; MOE_OK with *empty set for T = 0.
+// The checks that every entry shares.
 moe_status check_rows(const char* what, int T, int top_k, int hidden) {
     if (top_k < 1 || top_k > kMaxTopK) return fail(MOE_ERR_INVALID_ARG, "%s: top_k must be in [1, 8]", what);
     if (T < 0 || (long long)T * top_k > (1LL << 30))
@@ -241,10 +294,18 @@ moe_status check_side(const char* what, const char* name, const void* p, long lo
     return MOE_OK;
 }
 
-unsigned blocks_for(long long n) { return (unsigned)(n < (1LL << 30) ? n : (1LL << 30)); }
+// Blocks of 128 threads along one token's `chunks` in the combine: four times U
+// chunks a thread where there are tokens enough to fill the GPU, else U (one token
+// of 4096 fp32: 8 blocks).
+unsigned parts_for(int T, int chunks, int U) {
+    const int per = (T >= 1024 ? 512 : 128) * U;
+    const int n = (chunks + per - 1) / per;
+    return (unsigned)(n < 65535 ? n : 65535);
+}
 
-// Calls f.template operator()<A, O, C>() for the types and the widest C that the
-// rows allow: whole 16-byte words of A, else pairs, else single elements.
+// Calls f.template operator()<A, O, C, U>() for the types and the widest C that
+// the rows allow: whole 16-byte words of A, else pairs, else single elements; of
+// the narrow ones a thread has U on the way at once.
 template <typename A, typename O, typename F>
 cudaError_t by_width(unsigned align_a, unsigned align_o, int hidden, F&& f) {
     constexpr int W = 16 / (int)sizeof(A);
@@ -252,9 +313,9 @@ cudaError_t by_width(unsigned align_a, unsigned align_o, int hidden, F&& f) {
         const unsigned ob = c * (unsigned)sizeof(O) < 16 ? c * (unsigned)sizeof(O) : 16;
         return hidden % c == 0 && align_a >= c * sizeof(A) && align_o >= ob;
     };
-    if (fits(W)) return f.template operator()<A, O, W>();
-    if (fits(2)) return f.template operator()<A, O, 2>();
-    return f.template operator()<A, O, 1>();
+    if (fits(W)) return f.template operator()<A, O, W, 1>();
+    if (fits(2)) return f.template operator()<A, O, 2, 2>();
+    return f.template operator()<A, O, 1, 4>();
 }
 
 template <typename F>
@@ -270,19 +331,27 @@ cudaError_t by_type(moe_dtype a, moe_dtype o, unsigned align_a, unsigned align_o
 struct CombineLaunch {
     const void* y; long long ys; const float* w; int T, k, H; const int32_t* row_dst; void* out; long long os;
     cudaStream_t s;
-    template <typename A, typename O, int C>
+    template <typename A, typename O, int C, int U>
     cudaError_t operator()() const {
-        return launch_pdl(k_combine_rows<A, O, C>, dim3(blocks_for(T)), dim3(128), 0, s, (const A*)y, ys, w, T, k, H,
-                          row_dst, (O*)out, os);
+        return launch_pdl(k_combine_rows<A, O, C, U>, dim3(T, parts_for(T, H / C, U)), dim3(128), 0, s, (const A*)y, ys,
+                          w, T, k, H, row_dst, (O*)out, os);
     }
 };
 
 struct CombineBackwardLaunch {
     const void* dout; long long ds; const void* y; long long ys; const float* w; int T, k, H;
     const int32_t *placed, *row_dst; void* dy; long long dys; float* dw; cudaStream_t s;
-    template <typename A, typename O, int C>
+    template <typename A, typename O, int C, int U>
     cudaError_t operator()() const {
-        return launch_pdl(k_combine_backward<A, O, C>, dim3(blocks_for(T)), dim3(256), 0, s, (const O*)dout, ds,
+        // a whole block a slot where there are slots too few to fill the GPU with half blocks
+        // (150 SMs of 16); with two slots a block and one chunk in flight a thread the long
+        // batch takes 133 us, with a warp a slot 142, with two chunks 162, with four 209
+        const long long R = (long long)T * k;
+        return R < 2400 ? launch<A, O, C, 2 * U, 8>((unsigned)R) : launch<A, O, C, U, 4>((unsigned)((R + 1) / 2));
+    }
+    template <typename A, typename O, int C, int U, int kGroup>
+    cudaError_t launch(unsigned blocks) const {
+        return launch_pdl(k_combine_backward<A, O, C, U, kGroup>, dim3(blocks), dim3(256), 0, s, (const O*)dout, ds,
                           (const A*)y, ys, w, T, k, H, placed, row_dst, (A*)dy, dys, dw);
     }
 };
@@ -290,8 +359,9 @@ struct CombineBackwardLaunch {
 template <typename V>
 cudaError_t dispatch_words(const void* x, long long xp, int T, int k, int bytes, const int32_t* placed,
                            const int32_t* row_dst, void* xs, long long xsp, cudaStream_t s) {
-    return launch_pdl(k_dispatch<V>, dim3(blocks_for(T)), dim3(128), 0, s, (const char*)x, xp, T, k,
-                      bytes / (int)sizeof(V), placed, row_dst, (char*)xs, xsp);
+    const int words = bytes / (int)sizeof(V), parts = (words + 127) / 128;
+    return launch_pdl(k_dispatch<V>, dim3(T, parts < 65535 ? parts : 65535), dim3(128), 0, s, (const char*)x, xp, T, k, words,
+                      placed, row_dst, (char*)xs, xsp);
 }
 
 moe_status combine(const char* what, const void* y, moe_dtype dtype, long long y_stride, const float* w, int T,
@@ -392,6 +462,6 @@ extern "C" moe_status moe_route_backward(const float* logits, const int32_t* ids
     if (st == MOE_OK && !std::isfinite(w_scale)) st = fail(MOE_ERR_INVALID_ARG, "%s: w_scale must be finite", what);
     if (st != MOE_OK || T == 0) return st;
     if (!logits || !ids || !dw || !dlogits) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
-    return launched(launch_pdl(k_route_backward, dim3(blocks_for((T + 3LL) / 4)), dim3(128), 0, (cudaStream_t)stream,
+    return launched(launch_pdl(k_route_backward, dim3((T + 3) / 4), dim3(128), 0, (cudaStream_t)stream,
                                logits, ids, dw, T, n_experts, top_k, w_scale, dlogits), what);
 }
