@@ -8,16 +8,17 @@
 // nearly all are extreme and agree in sign; it is then rounded like any fp32 sum.
 //
 // One CTA per SM walks tiles of 128 output channels (A, one tensor-memory lane
-// a channel) x up to kCap positions of one segment (B).  K goes in units of 64:
+// a channel) x up to kCap positions of one segment (B), K in units:
 //   kAGroups warpgroups  codes of one channel a thread -> fp16 -> tensor memory
 //                        (the A operand: it takes no shared-memory bandwidth from B)
-//   kBWarps warps        token codes: global -> registers (kAhead units ahead) ->
-//                        fp16 -> shared memory, rows of 128 bytes, 128-byte swizzle;
-//                        the token row is looked up here: a gather costs nothing
+//   kBGroups x 4 or 8    token codes: global -> registers, a few units ahead and
+//   warps                across tiles -> fp16 -> shared memory, rows of 128 bytes,
+//                        128-byte swizzle; a gather costs nothing here
 //   4 warps              accumulators -> scales -> out, while the next tile is
 //                        summed (two accumulators)
-//   1 thread             TMA of 128 channels x 128 bytes of codes into a ring
-//   1 thread             the MMAs (N = the tile's rows rounded to 16)
+//   1 warp               TMA of 128 channels x 128 bytes of codes into a ring
+//   1 warp               the MMAs (N = the tile's rows rounded to 16)
+// The groups of one kind take the units in turn.
 #include <cuda.h>
 
 #include <mutex>
@@ -33,26 +34,37 @@ namespace {
 
 using namespace tc;
 
-constexpr int kUnit = 64;             // K of one unit (128 bytes of fp16)
 constexpr int kRawBytes = 128 * 128;  // one ring slot of weight codes
-constexpr int kAhead = 3;             // units of token codes held in registers
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-template <int kCap>
+// Narrow tiles are bound by the stream of weights: long units (fewer waits a
+// byte) and a long ring.  Wide ones are bound by the MMA: 192 positions are
+// the most of which two accumulators and four units fit tensor memory.
+template <int kCap_>
 struct Cfg {
-    static constexpr int kBBytes = kCap * 128;           // one unit of tokens in fp16
-    static constexpr int kSlots = kCap > 64 ? 4 : 8;     // units in flight to the MMA
-    static constexpr int kRaw = kCap > 64 ? 7 : 9;       // weight ring
-    static constexpr int kAGroups = kCap > 64 ? 2 : 4;   // warpgroups that turn weights
-    static constexpr int kBWarps = kCap > 64 ? 8 : 4;    // warps that turn tokens
-    static constexpr int kPasses = kCap / (8 * kBWarps); // 8 token rows a warp and pass
-    static constexpr int kAWarps = 4 * kAGroups;
-    static constexpr int kEpi = kAWarps + kBWarps;       // first epilogue warp; then TMA, then MMA
+    static constexpr int kCap = kCap_;
+    static constexpr bool kWide = kCap > 64;
+    static constexpr int kUnit = kWide ? 64 : 128;         // K of one unit
+    static constexpr int kSlots = 4;                       // units in flight to the MMA
+    static constexpr int kRaw = kWide ? 4 : 8;             // weight ring
+    static constexpr int kPerRaw = 128 / kUnit;            // units in one of its slots
+    static constexpr int kAGroups = 2;
+    static constexpr int kBGroups = 2;
+    static constexpr int kBWarps = kWide ? 8 : 4;          // warps of one token group
+    static constexpr int kLanes = kUnit / 16;              // lanes that share a token's unit
+    static constexpr int kPass = kBWarps * 32 / kLanes;    // token rows a group moves at once
+    static constexpr int kPasses = kCap / kPass;
+    static constexpr int kAhead = kWide ? 1 : 2;           // units of token codes held in registers
+    static constexpr int kSubBytes = kCap * 128;           // 64 of K of all tokens in fp16
+    static constexpr int kBBytes = kSubBytes * (kUnit / 64);
+    static constexpr int kACols = kUnit / 2;               // tensor-memory columns of one unit
+    static constexpr int kACol = 512 - kACols * kSlots;
+    static constexpr int kDCols = kCap;
+    static constexpr int kBFirst = 4 * kAGroups;
+    static constexpr int kEpi = kBFirst + kBGroups * kBWarps;  // first epilogue warp; then TMA, then MMA
     static constexpr int kThreads = (kEpi + 6) * 32;
-    static constexpr int kACol = 512 - 32 * kSlots;      // tensor-memory column of the A units
-    static constexpr int kDCols = kCap > 64 ? 192 : 64;  // columns of one accumulator
     static constexpr int kSmem = 1024 + kSlots * kBBytes + kRaw * kRawBytes;
-    static_assert(kCap % 64 == 0 && 2 * kDCols <= kACol && kCap <= kDCols, "tensor memory");
+    static_assert(kCap % kPass == 0 && kCap % 32 == 0 && 2 * kDCols <= kACol, "tensor memory");
 };
 
 // One lane of the warp, the same one each time: 1 there, 0 elsewhere.
@@ -118,6 +130,10 @@ __device__ __forceinline__ void ld_ahead(uint4& v, const int8_t* p, bool on) {
         : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)on));
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 struct Tile {
     int e, n0, p0, count;
 };
@@ -130,10 +146,12 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[2 * C::kRaw + 2 * C::kSlots + 4];
     __shared__ int first[kMaxExperts + 1];  // token tiles before each expert
+    __shared__ int begin[kMaxExperts + 1];  // its segment
     __shared__ int scan[32];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
+    constexpr unsigned kAll = 0xFFFFFFFFu;
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -149,7 +167,7 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
     if (tid == 0) {
         for (int i = 0; i < C::kRaw; ++i) {
             mbar_init(raw_full(i), 1);
-            mbar_init(raw_empty(i), 8);
+            mbar_init(raw_empty(i), 4 * C::kPerRaw);
         }
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(full(i), 4 + C::kBWarps);
@@ -163,6 +181,7 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
         fence_mbar_init();
         prefetch_tmap(&wmap);
     }
+    // all 512 columns: they start at address 0, which the code below relies on
     if (warp == C::kEpi + 5) tmem_alloc(smem_u32(&tmem_slot), 512);
     pdl_wait();
 
@@ -172,12 +191,14 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
         const int per = (a.E + C::kThreads - 1) / C::kThreads;
         for (int i = 0; i < per; ++i) {
             const int e = tid * per + i;
-            if (e < a.E) mine += (max(segment_at(a, e + 1) - segment_at(a, e), 0) + kCap - 1) / kCap;
+            if (e <= a.E) begin[e] = segment_at(a, e);
+            if (e < a.E) mine += (max(segment_at(a, e + 1) - begin[e], 0) + kCap - 1) / kCap;
         }
+        if (tid == 0) begin[a.E] = segment_at(a, a.E);
         int run = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, run, o);
+            const int v = __shfl_up_sync(kAll, run, o);
             if (lane >= o) run += v;
         }
         if (lane == 31) scan[warp] = run;
@@ -188,7 +209,7 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
             const int e = tid * per + i;
             if (e < a.E) {
                 first[e] = before;
-                before += (max(segment_at(a, e + 1) - segment_at(a, e), 0) + kCap - 1) / kCap;
+                before += (max(begin[e + 1] - begin[e], 0) + kCap - 1) / kCap;
                 if (e == a.E - 1) first[a.E] = before;
             }
         }
@@ -196,14 +217,13 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
     const int m_tiles = (a.N + 127) / 128;
-    const long long tiles = (long long)first[a.E] * m_tiles;
-    const int units = (a.K + kUnit - 1) / kUnit;
+    const int tiles = first[a.E] * m_tiles;  // below 2^28: R <= 2^20, N <= 2^20 and m_tiles tiles a token tile
+    const int units = (a.K + C::kUnit - 1) / C::kUnit;
 
     // Tile t: the channels of one token tile follow each other.
-    auto tile_at = [&](long long t) {
-        const int tt = (int)(t / m_tiles);
+    auto tile_at = [&](int t) {
+        const int tt = t / m_tiles;
         int lo = 0, hi = a.E - 1;  // last e with first[e] <= tt
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -211,11 +231,11 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
         }
         Tile w;
         w.e = lo;
-        w.n0 = (int)(t % m_tiles) * 128;
-        const int begin = segment_at(a, lo), count = segment_at(a, lo + 1) - begin, n = first[lo + 1] - first[lo];
+        w.n0 = (t - tt * m_tiles) * 128;
+        const int count = begin[lo + 1] - begin[lo], n = first[lo + 1] - first[lo];
         const int step = n < 8 ? ((count + n - 1) / n + 15) / 16 * 16 : kCap;  // at most kCap
-        w.p0 = begin + (tt - first[lo]) * step;
-        w.count = min(step, begin + count - w.p0);
+        w.p0 = begin[lo] + (tt - first[lo]) * step;
+        w.count = min(step, begin[lo + 1] - w.p0);
         return w;
     };
     bool ok = true;
@@ -224,9 +244,9 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
         // ------------------------------------------------- weight codes (TMA) --
         if (lane == 0) {
             int i = 0;
-            for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const Tile w = tile_at(t);
-                for (int k0 = 0; k0 < a.K && ok; k0 += 128, ++i) {
+                for (int k0 = 0; k0 < a.K; k0 += 128, ++i) {
                     const int s = i % C::kRaw;
                     ok = mbar_wait(raw_empty(s), ((i / C::kRaw) & 1) ^ 1, kWaitNs, abort);
                     if (!ok) break;
@@ -239,71 +259,79 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
         // ------------------------------------------------------------- MMA --
         const uint32_t on = elect_lane();
         int g = 0, n = 0;
-        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
             const uint32_t cols = (tile_at(t).count + 15) / 16 * 16;
             const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u >> 4) << 24);
             const int b = n & 1;
-            const uint32_t d = tmem + b * C::kDCols;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(d_empty(b), ((n >> 1) & 1) ^ 1, kWaitNs, abort));
+            const uint32_t d = b * C::kDCols;
+            ok = __all_sync(kAll, mbar_wait(d_empty(b), ((n >> 1) & 1) ^ 1, kWaitNs, abort));
             tc_fence_after();
             for (int u = 0; u < units && ok; ++u, ++g) {
                 const int s = g % C::kSlots;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full(s), (g / C::kSlots) & 1, kWaitNs, abort));
+                ok = __all_sync(kAll, mbar_wait(full(s), (g / C::kSlots) & 1, kWaitNs, abort));
                 if (!ok) break;
                 // the loaders' stores, seen through the barrier, before the MMA's own reads; the
                 // fence stands here because there it would wait for the loads that run ahead
                 fence_async_shared();
                 tc_fence_after();
                 const uint64_t bd = desc_sw128(b_base + s * C::kBBytes);
-                const uint32_t ad = tmem + C::kACol + s * 32;
-                if (a.K - u * kUnit >= kUnit) {
+                const uint32_t ad = C::kACol + s * C::kACols;
+                if (a.K - u * C::kUnit >= C::kUnit) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mma_f16_ts(on, d, ad + i * 8, bd + (uint64_t)(i * 2), idesc, (u | i) != 0);
+                    for (int i = 0; i < C::kUnit / 16; ++i)
+                        mma_f16_ts(on, d, ad + i * 8, bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2), idesc,
+                                   (u | i) != 0);
                 } else {
-                    for (int i = 0; i < (a.K - u * kUnit + 15) / 16; ++i)
-                        mma_f16_ts(on, d, ad + i * 8, bd + (uint64_t)(i * 2), idesc, (u | i) != 0);
+                    for (int i = 0; i < (a.K - u * C::kUnit + 15) / 16; ++i)
+                        mma_f16_ts(on, d, ad + i * 8, bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2), idesc,
+                                   (u | i) != 0);
                 }
                 mma_commit_by(on, empty(s));
             }
             if (ok) mma_commit_by(on, d_full(b));
         }
-    } else if (warp < C::kAWarps) {
+    } else if (warp < C::kBFirst) {
         // --------------------------------------------- weights to tensor memory --
-        // group q of kAGroups takes the units u = q, q + kAGroups, ... of a tile;
-        // two units share a ring slot, each of them frees half of it
+        // (with two units a ring slot, each of them frees half of it)
         const int lanes = (warp & 3) * 32, r = lanes + lane, group = warp >> 2;
+        const uint32_t lane_at = (uint32_t)lanes << 16;
         int i0 = 0, g0 = 0;
-        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x, i0 += (units + 1) / 2, g0 += units) {
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, i0 += (units + C::kPerRaw - 1) / C::kPerRaw, g0 += units) {
             for (int u = group; u < units; u += C::kAGroups) {
-                const int i = i0 + (u >> 1), rs = i % C::kRaw, g = g0 + u, s = g % C::kSlots;
-                ok = mbar_wait(raw_full(rs), (i / C::kRaw) & 1, kWaitNs, abort);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                const int i = i0 + u / C::kPerRaw, rs = i % C::kRaw, g = g0 + u, s = g % C::kSlots;
+                const int part = u % C::kPerRaw;
+                ok = __all_sync(kAll, mbar_wait(raw_full(rs), (i / C::kRaw) & 1, kWaitNs, abort));
                 if (!ok) break;
                 const uint32_t row = raw_base + rs * kRawBytes + r * 128;
-                uint4 v[4];
+                uint4 v[C::kUnit / 16];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < C::kUnit / 16; ++c)
                     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                                  : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
-                                 : "r"(row + (((4 * (u & 1) + c) ^ (r & 7)) << 4)));
-                uint32_t f[32];
+                                 : "r"(row + (((C::kUnit / 16 * part + c) ^ (r & 7)) << 4)));
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    codes_to_f16(v[c].x, f[8 * c], f[8 * c + 1]);
-                    codes_to_f16(v[c].y, f[8 * c + 2], f[8 * c + 3]);
-                    codes_to_f16(v[c].z, f[8 * c + 4], f[8 * c + 5]);
-                    codes_to_f16(v[c].w, f[8 * c + 6], f[8 * c + 7]);
+                for (int h = 0; h < C::kUnit / 64; ++h) {
+                    uint32_t f[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        codes_to_f16(v[4 * h + c].x, f[8 * c], f[8 * c + 1]);
+                        codes_to_f16(v[4 * h + c].y, f[8 * c + 2], f[8 * c + 3]);
+                        codes_to_f16(v[4 * h + c].z, f[8 * c + 4], f[8 * c + 5]);
+                        codes_to_f16(v[4 * h + c].w, f[8 * c + 6], f[8 * c + 7]);
+                    }
+                    if (h == 0) {
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(raw_empty(rs));
+                            if (C::kPerRaw == 2 && u == units - 1 && part == 0) mbar_arrive(raw_empty(rs));  // no second unit
+                        }
+                        ok = __all_sync(kAll, mbar_wait(empty(s), ((g / C::kSlots) & 1) ^ 1, kWaitNs, abort));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    tmem_st32(lane_at + C::kACol + s * C::kACols + 32 * h, f);
                 }
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(raw_empty(rs));
-                    if (u == units - 1 && !(u & 1)) mbar_arrive(raw_empty(rs));  // no second unit
-                }
-                ok = mbar_wait(empty(s), ((g / C::kSlots) & 1) ^ 1, kWaitNs, abort);
-                ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                tc_fence_after();
-                tmem_st32(tmem + ((uint32_t)lanes << 16) + C::kACol + s * 32, f);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -312,35 +340,51 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
         }
     } else if (warp < C::kEpi) {
         // ------------------------------------------- tokens to shared memory --
-        const int bw = warp - C::kAWarps, sub = lane & 3;
-        int g = 0;
-        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const int group = (warp - C::kBFirst) / C::kBWarps, bw = (warp - C::kBFirst) % C::kBWarps;
+        const int sub = lane % C::kLanes, row0 = bw * (32 / C::kLanes) + lane / C::kLanes;
+        // where lane's 16 codes of row row0 go: two 16-byte pieces, in an order that
+        // keeps the eight lanes of a store on eight banks
+        const uint32_t at = b_base + (sub >> 2) * C::kSubBytes + row0 * 128;
+        const uint32_t lo = at + (((2 * (sub & 3)) ^ (row0 & 7)) << 4), hi = at + (((2 * (sub & 3) + 1) ^ (row0 & 7)) << 4);
+        const bool odd = sub >= 4;
+        // the stream of this group's units runs kAhead ahead, over the ends of tiles
+        int at_t = blockIdx.x, at_u = group;
+        const int8_t* src[C::kPasses];
+        auto rows_of = [&](int t) {
+            if (t >= tiles) return;
             const Tile w = tile_at(t);
-            const int8_t* src[C::kPasses];
 #pragma unroll
             for (int i = 0; i < C::kPasses; ++i) {
-                const int row = (i * C::kBWarps + bw) * 8 + (lane >> 2);
+                const int row = i * C::kPass + row0;
                 const int r = row < w.count ? source_row(a, w.p0 + row) : -1;
                 src[i] = r >= 0 ? a.q + (long long)r * a.qs + sub * 16 : nullptr;
             }
-            const int passes = (w.count + 8 * C::kBWarps - 1) / (8 * C::kBWarps);
-            uint4 buf[kAhead][C::kPasses];
-            auto load = [&](uint4 (&v)[C::kPasses], int u) {
-                const int k = u * kUnit + sub * 16;
+        };
+        auto load = [&](uint4 (&v)[C::kPasses]) {
+            if (at_t >= tiles) return;
+            const int k = at_u * C::kUnit;
 #pragma unroll
-                for (int i = 0; i < C::kPasses; ++i) ld_ahead(v[i], src[i] + u * kUnit, src[i] != nullptr && k < a.K);
-            };
+            for (int i = 0; i < C::kPasses; ++i) ld_ahead(v[i], src[i] + k, src[i] != nullptr && k + sub * 16 < a.K);
+            at_u += C::kBGroups;
+            if (at_u >= units) {
+                at_u = group;
+                at_t += gridDim.x;
+                rows_of(at_t);
+            }
+        };
+        if (group < units) {
+            uint4 buf[C::kAhead][C::kPasses];
+            rows_of(at_t);
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (j < units) load(buf[j], j);
-            for (int u0 = 0; u0 < units && ok; u0 += kAhead) {
+            for (int j = 0; j < C::kAhead; ++j) load(buf[j]);
+            int t = blockIdx.x, u = group, g0 = 0;
+            int passes = t < tiles ? (tile_at(t).count + C::kPass - 1) / C::kPass : 0;
+            while (t < tiles && ok) {
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const int u = u0 + j;
-                    if (u >= units || !ok) break;
-                    const int s = g % C::kSlots;
-                    ok = mbar_wait(empty(s), ((g / C::kSlots) & 1) ^ 1, kWaitNs, abort);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
+                for (int j = 0; j < C::kAhead; ++j) {
+                    if (t >= tiles || !ok) break;
+                    const int g = g0 + u, s = g % C::kSlots;
+                    ok = __all_sync(kAll, mbar_wait(empty(s), ((g / C::kSlots) & 1) ^ 1, kWaitNs, abort));
                     if (!ok) break;
 #pragma unroll
                     for (int i = 0; i < C::kPasses; ++i) {
@@ -350,17 +394,22 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
                         codes_to_f16(buf[j][i].y, f[2], f[3]);
                         codes_to_f16(buf[j][i].z, f[4], f[5]);
                         codes_to_f16(buf[j][i].w, f[6], f[7]);
-                        const int row = (i * C::kBWarps + bw) * 8 + (lane >> 2), x = row & 7;
-                        const uint32_t at = b_base + s * C::kBBytes + row * 128;
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * sub) ^ x) << 4)), "r"(f[0]),
-                                     "r"(f[1]), "r"(f[2]), "r"(f[3]) : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * sub + 1) ^ x) << 4)),
-                                     "r"(f[4]), "r"(f[5]), "r"(f[6]), "r"(f[7]) : "memory");
+                        const uint32_t to = s * C::kBBytes + i * C::kPass * 128;  // kPass % 8 == 0: the swizzle stays
+                        st_shared16((odd ? hi : lo) + to, odd ? f[4] : f[0], odd ? f[5] : f[1], odd ? f[6] : f[2],
+                                    odd ? f[7] : f[3]);
+                        st_shared16((odd ? lo : hi) + to, odd ? f[0] : f[4], odd ? f[1] : f[5], odd ? f[2] : f[6],
+                                    odd ? f[3] : f[7]);
                     }
-                    if (u + kAhead < units) load(buf[j], u + kAhead);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full(s));
-                    ++g;
+                    load(buf[j]);
+                    u += C::kBGroups;
+                    if (u >= units) {
+                        u = group;
+                        t += gridDim.x;
+                        g0 += units;
+                        if (t < tiles) passes = (tile_at(t).count + C::kPass - 1) / C::kPass;
+                    }
                 }
             }
         }
@@ -368,10 +417,10 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
         // -------------------------------------------------------- epilogue --
         const int ew = warp - C::kEpi, et = tid - C::kEpi * 32;
         O* out = reinterpret_cast<O*>(a.out);
-        for (long long p = segment_at(a, a.E) + (long long)blockIdx.x; p < a.R; p += gridDim.x)
+        for (long long p = begin[a.E] + (long long)blockIdx.x; p < a.R; p += gridDim.x)
             for (int n = et; n < a.N; n += 128) out[p * a.os + n] = from_f32<O>(0.f);
         int n = 0;
-        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
             const Tile w = tile_at(t);
             const int b = n & 1;
             float rs[kCap / 32];  // lane i: scale of rows i, 32 + i, ...
@@ -382,8 +431,7 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
             }
             const int ch = w.n0 + ew * 32 + lane;
             const float cs = ch < a.N ? a.w_scale[(long long)w.e * a.N + ch] : 0.f;
-            ok = mbar_wait(d_full(b), (n >> 1) & 1, kWaitNs, abort);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+            ok = __all_sync(kAll, mbar_wait(d_full(b), (n >> 1) & 1, kWaitNs, abort));
             if (!ok) break;
             tc_fence_after();
             O* dst = out + (long long)w.p0 * a.os + ch;
@@ -392,7 +440,7 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
                 const int c0 = 32 * i;
                 if (c0 >= w.count) break;
                 uint32_t v[32];
-                tmem_ld32(tmem + ((uint32_t)(ew * 32) << 16) + b * C::kDCols + c0, v);
+                tmem_ld32(((uint32_t)(ew * 32) << 16) + b * C::kDCols + c0, v);
                 tmem_ld_wait();
                 if (c0 + 32 >= w.count) {
                     tc_fence_before();
@@ -401,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
                 }
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    const float s = __shfl_sync(0xFFFFFFFFu, rs[i], c);
+                    const float s = __shfl_sync(kAll, rs[i], c);
                     if (c0 + c < w.count && ch < a.N)
                         dst[(long long)(c0 + c) * a.os] = from_f32<O>(__uint_as_float(v[c]) * s * cs);
                 }
@@ -417,7 +465,7 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
     __syncthreads();
     if (warp == C::kEpi + 5) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem_slot, 512);
     }
 }
 
