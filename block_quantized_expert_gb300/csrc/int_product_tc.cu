@@ -16,7 +16,8 @@
 //                        128-byte swizzle; a gather costs nothing here
 //   4 warps              accumulators -> scales -> out, while the next tile is
 //                        summed (two accumulators)
-//   1 warp               TMA of 128 channels x 128 bytes of codes into a ring
+//   1 warp               TMA of 128 channels x 128 bytes of codes into a ring; looks
+//                        up the token rows of the next tile
 //   1 warp               the MMAs (N = the tile's rows rounded to 16)
 // The groups of one kind take the units in turn.
 #include <cuda.h>
@@ -37,34 +38,43 @@ using namespace tc;
 constexpr int kRawBytes = 128 * 128;  // one ring slot of weight codes
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Narrow tiles are bound by the stream of weights: long units (fewer waits a
-// byte) and a long ring.  Wide ones are bound by the MMA: 192 positions are
-// the most of which two accumulators and four units fit tensor memory.
-template <int kCap_>
+// Narrow tiles are bound by the stream of weights: a long ring, one CTA a tile.
+// Wide ones are bound by the MMA and by the turning of codes: a pair of CTAs (a
+// cluster of two on one MMA, cta_group::2) takes 256 channels x 256 positions; each
+// turns its own 128 channels and one half of the positions, half of what a CTA
+// alone would turn for the same products.
+template <bool kPair_>
 struct Cfg {
-    static constexpr int kCap = kCap_;
-    static constexpr bool kWide = kCap > 64;
-    static constexpr int kUnit = kWide ? 64 : 128;         // K of one unit
-    static constexpr int kSlots = 4;                       // units in flight to the MMA
-    static constexpr int kRaw = kWide ? 4 : 8;             // weight ring
-    static constexpr int kPerRaw = 128 / kUnit;            // units in one of its slots
+    static constexpr bool kPair = kPair_;
+    static constexpr int kCtas = kPair ? 2 : 1;
+    static constexpr int kCap = kPair ? 256 : 64;           // positions of a tile
+    static constexpr int kRows = kCap / kCtas;              // of them in this CTA's shared memory
+    static constexpr int kUnit = 128;                       // K of one unit
+    static constexpr int kSlots = 4;                        // units in flight to the MMA
+    static constexpr int kRaw = kPair ? 4 : 8;              // weight ring
     static constexpr int kAGroups = 2;
     static constexpr int kBGroups = 2;
-    static constexpr int kBWarps = kWide ? 8 : 4;          // warps of one token group
-    static constexpr int kLanes = kUnit / 16;              // lanes that share a token's unit
-    static constexpr int kPass = kBWarps * 32 / kLanes;    // token rows a group moves at once
-    static constexpr int kPasses = kCap / kPass;
-    static constexpr int kAhead = kWide ? 1 : 2;           // units of token codes held in registers
-    static constexpr int kSubBytes = kCap * 128;           // 64 of K of all tokens in fp16
+    static constexpr int kBWarps = 4;                       // warps of one token group
+    static constexpr int kLanes = kUnit / 16;               // lanes that share a token's unit
+    static constexpr int kPass = kBWarps * 32 / kLanes;     // token rows a group moves at once
+    static constexpr int kPasses = kRows / kPass;
+    static constexpr int kAhead = kPair ? 1 : 2;            // units of token codes held in registers
+    static constexpr int kTabs = 4;                         // tiles whose token rows are looked up
+    static constexpr int kSubBytes = kRows * 128;           // 64 of K of all its positions in fp16
     static constexpr int kBBytes = kSubBytes * (kUnit / 64);
-    static constexpr int kACols = kUnit / 2;               // tensor-memory columns of one unit
+    static constexpr int kACols = kUnit / 2;                // tensor-memory columns of one unit
     static constexpr int kACol = 512 - kACols * kSlots;
-    static constexpr int kDCols = kCap;
+    static constexpr int kAccs = kPair ? 1 : 2;             // accumulators
     static constexpr int kBFirst = 4 * kAGroups;
-    static constexpr int kEpi = kBFirst + kBGroups * kBWarps;  // first epilogue warp; then TMA, then MMA
-    static constexpr int kThreads = (kEpi + 6) * 32;
+    static constexpr int kEpi = kBFirst + kBGroups * kBWarps;   // first epilogue warp; then TMA, then MMA
+    static constexpr int kEpiWarps = kPair ? 8 : 4;
+    static constexpr int kTma = kEpi + kEpiWarps, kMma = kTma + 1;
+    static constexpr int kThreads = (kMma + 1) * 32;
     static constexpr int kSmem = 1024 + kSlots * kBBytes + kRaw * kRawBytes;
-    static_assert(kCap % kPass == 0 && kCap % 32 == 0 && 2 * kDCols <= kACol, "tensor memory");
+    // a slot of either ring always belongs to the same group: one that met every other
+    // use of a slot could take the phase before last, of the same parity, for its own
+    static_assert(kRaw % kAGroups == 0 && kSlots % kAGroups == 0 && kSlots % kBGroups == 0, "rings");
+    static_assert(kRows % kPass == 0 && kCap % 32 == 0 && kAccs * kCap <= kACol, "tensor memory");
 };
 
 // One lane of the warp, the same one each time: 1 there, 0 elsewhere.
@@ -77,21 +87,84 @@ __device__ __forceinline__ uint32_t elect_lane() {
 // D[tmem] (+)= A[tmem] B[smem]^T, fp16 operands, fp32 accumulators; called by the
 // whole warp, issued by the lane with `on`.  Under an `if` on the lane instead,
 // the operands are no longer uniform over the warp and an issue takes 147
-// cycles whatever N is; so it takes 60 for N <= 64 and N / 2 above (measured).
+// cycles whatever N is; so it takes 35 to 60 for N <= 64 and N / 2 above (measured).
+template <bool kPair>
 __device__ __forceinline__ void mma_f16_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
-        : "memory");
+    if (kPair)
+        asm volatile(
+            "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}"
+            ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+            ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+            : "memory");
 }
 
+// Arrives on the barrier (of both CTAs of a pair) when the MMAs so far are done.
+template <bool kPair>
 __device__ __forceinline__ void mma_commit_by(uint32_t on, uint32_t bar) {
+    if (kPair)
+        asm volatile(
+            "{\n.reg .pred q;\n.reg .b16 m;\nmov.b16 m, 3;\nsetp.ne.b32 q, %1, 0;\n"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}"
+            ::"r"(bar), "r"(on)
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar), "r"(on)
+            : "memory");
+}
+
+// Arrives on the pair's first CTA's barrier at the same place as `bar` here.
+__device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
     asm volatile(
-        "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar), "r"(on)
-        : "memory");
+        "{\n.reg .b32 r;\nmapa.shared::cluster.u32 r, %0, 0;\n"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n}" ::"r"(bar) : "memory");
+}
+
+// mbar_wait for a phase that threads of the other CTA complete as well.
+__device__ __forceinline__ bool mbar_try_wait_pair(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+template <bool kPair>
+__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity, volatile int* abort) {
+    if (!kPair) return mbar_wait(bar, parity, kWaitNs, abort);
+    if (mbar_try_wait_pair(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    while (true) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait_pair(bar, parity)) return true;
+        if (*abort || globaltimer() - t0 > kWaitNs) return false;
+    }
+}
+
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_alloc_all(uint32_t slot) {
+    if (!kPair) return tmem_alloc(slot, 512);
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(slot) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_free_all(uint32_t taddr) {
+    if (!kPair) return tmem_dealloc(taddr, 512);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
 }
 
 // 32 columns of this warp's 32 lanes.
@@ -134,17 +207,22 @@ __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y,
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+
 struct Tile {
     int e, n0, p0, count;
 };
 
 __device__ uint32_t g_product_err;
 
-template <int kCap, typename O>
-__global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Product a, const __grid_constant__ CUtensorMap wmap) {
-    using C = Cfg<kCap>;
+template <bool kPair, typename O>
+__global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Product a, const __grid_constant__ CUtensorMap wmap) {
+    using C = Cfg<kPair>;
+    constexpr int kCap = C::kCap;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * C::kRaw + 2 * C::kSlots + 4];
+    __shared__ uint64_t bars[2 * C::kRaw + 3 * C::kSlots + 4 + 2 * C::kTabs];
+    __shared__ uint32_t token_at[C::kTabs][C::kRows];  // where a tile's rows of q start, in 16 bytes
+    __shared__ int token_passes[C::kTabs];
     __shared__ int first[kMaxExperts + 1];  // token tiles before each expert
     __shared__ int begin[kMaxExperts + 1];  // its segment
     __shared__ int scan[32];
@@ -154,6 +232,8 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
     constexpr unsigned kAll = 0xFFFFFFFFu;
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = kPair ? blockIdx.x & 1 : 0;  // in the pair
+    const int first_tile = blockIdx.x / C::kCtas, tile_step = gridDim.x / C::kCtas;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t b_base = base, raw_base = base + C::kSlots * C::kBBytes;
     const uint32_t bar0 = smem_u32(bars);
@@ -161,28 +241,36 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
     auto raw_empty = [&](int i) { return bar0 + 8u * (C::kRaw + i); };
     auto full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + i); };
     auto empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + C::kSlots + i); };
-    auto d_full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kSlots + i); };
-    auto d_empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kSlots + 2 + i); };
+    auto other = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kSlots + i); };  // the other CTA's full
+    auto d_full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 3 * C::kSlots + i); };
+    auto d_empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 3 * C::kSlots + 2 + i); };
+    auto tab_full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 3 * C::kSlots + 4 + i); };
+    auto tab_empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 3 * C::kSlots + 4 + C::kTabs + i); };
     volatile int* abort = &abort_flag;
     if (tid == 0) {
         for (int i = 0; i < C::kRaw; ++i) {
             mbar_init(raw_full(i), 1);
-            mbar_init(raw_empty(i), 4 * C::kPerRaw);
+            mbar_init(raw_empty(i), 4);
         }
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(full(i), 4 + C::kBWarps);
+            mbar_init(other(i), 1);
             mbar_init(empty(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(d_full(i), 1);
-            mbar_init(d_empty(i), 4);
+            mbar_init(d_empty(i), C::kCtas * C::kEpiWarps);
+        }
+        for (int i = 0; i < C::kTabs; ++i) {
+            mbar_init(tab_full(i), 1);
+            mbar_init(tab_empty(i), C::kBGroups * C::kBWarps);
         }
         abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&wmap);
     }
     // all 512 columns: they start at address 0, which the code below relies on
-    if (warp == C::kEpi + 5) tmem_alloc(smem_u32(&tmem_slot), 512);
+    if (warp == C::kMma) tmem_alloc_all<kPair>(smem_u32(&tmem_slot));
     pdl_wait();
 
     // token tiles of every expert: ceil(count / kCap) of nearly equal size
@@ -216,9 +304,10 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
     }
     tc_fence_before();
     __syncthreads();
+    if (kPair) pair_sync();  // the other CTA's barriers are ready
     tc_fence_after();
-    const int m_tiles = (a.N + 127) / 128;
-    const int tiles = first[a.E] * m_tiles;  // below 2^28: R <= 2^20, N <= 2^20 and m_tiles tiles a token tile
+    const int m_tiles = (a.N + 128 * C::kCtas - 1) / (128 * C::kCtas);
+    const int tiles = first[a.E] * m_tiles;  // below 2^28: R <= 2^20, N <= 2^20
     const int units = (a.K + C::kUnit - 1) / C::kUnit;
 
     // Tile t: the channels of one token tile follow each other.
@@ -231,47 +320,84 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
         }
         Tile w;
         w.e = lo;
-        w.n0 = (t - tt * m_tiles) * 128;
+        w.n0 = ((t - tt * m_tiles) * C::kCtas + rank) * 128;
         const int count = begin[lo + 1] - begin[lo], n = first[lo + 1] - first[lo];
         const int step = n < 8 ? ((count + n - 1) / n + 15) / 16 * 16 : kCap;  // at most kCap
         w.p0 = begin[lo] + (tt - first[lo]) * step;
         w.count = min(step, begin[lo + 1] - w.p0);
         return w;
     };
+    // Accumulator columns of so many positions; each CTA of a pair holds one half.
+    auto columns = [&](int count) { return (count + 16 * C::kCtas - 1) / (16 * C::kCtas) * (16 * C::kCtas); };
+    auto release = [&](int b) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if (kPair) mbar_arrive_first(d_empty(b)); else mbar_arrive(d_empty(b));
+        }
+    };
     bool ok = true;
 
-    if (warp == C::kEpi + 4) {
-        // ------------------------------------------------- weight codes (TMA) --
-        if (lane == 0) {
-            int i = 0;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const Tile w = tile_at(t);
-                for (int k0 = 0; k0 < a.K; k0 += 128, ++i) {
-                    const int s = i % C::kRaw;
-                    ok = mbar_wait(raw_empty(s), ((i / C::kRaw) & 1) ^ 1, kWaitNs, abort);
-                    if (!ok) break;
+    if (warp == C::kTma) {
+        // ---------------- token rows of the next tile, weight codes of this one (TMA) --
+        auto look_up = [&](int t, int n) {
+            if (t >= tiles) return;
+            const Tile w = tile_at(t);
+            const int i = n % C::kTabs, half = columns(w.count) / C::kCtas;
+            ok = __all_sync(kAll, mbar_wait(tab_empty(i), ((n / C::kTabs) & 1) ^ 1, kWaitNs, abort));
+            if (!ok) return;
+            for (int row = lane; row < C::kRows; row += 32) {
+                const int at = rank * half + row;
+                const int r = row < half && at < w.count ? source_row(a, w.p0 + at) : -1;
+                token_at[i][row] = r >= 0 ? (uint32_t)(r * (a.qs >> 4)) : kNoRow;
+            }
+            if (lane == 0) token_passes[i] = (half + C::kPass - 1) / C::kPass;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tab_full(i));
+        };
+        int i = 0, n = 0;
+        look_up(first_tile, 0);
+        for (int t = first_tile; t < tiles && ok; t += tile_step) {
+            const Tile w = tile_at(t);
+            look_up(t + tile_step, ++n);
+            for (int k0 = 0; k0 < a.K && ok; k0 += 128, ++i) {
+                const int s = i % C::kRaw;
+                ok = __all_sync(kAll, mbar_wait(raw_empty(s), ((i / C::kRaw) & 1) ^ 1, kWaitNs, abort));
+                if (ok && lane == 0) {
                     mbar_arrive_expect_tx(raw_full(s), kRawBytes);
                     tma_load_2d(raw_base + s * kRawBytes, &wmap, k0, w.e * a.N + w.n0, raw_full(s));
                 }
+                __syncwarp();
             }
         }
-    } else if (warp == C::kEpi + 5) {
+    } else if (warp == C::kMma) {
         // ------------------------------------------------------------- MMA --
+        // The first CTA of a pair issues for both; in the second this warp passes on that a
+        // unit is there, one arrival over the cluster for the eight warps' (each of
+        // them would wait for its own stores to be seen there).
         const uint32_t on = elect_lane();
         int g = 0, n = 0;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
-            const uint32_t cols = (tile_at(t).count + 15) / 16 * 16;
-            const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u >> 4) << 24);
-            const int b = n & 1;
-            const uint32_t d = b * C::kDCols;
-            ok = __all_sync(kAll, mbar_wait(d_empty(b), ((n >> 1) & 1) ^ 1, kWaitNs, abort));
+        for (int t = first_tile; t < tiles && ok && rank == 1; t += tile_step)
+            for (int u = 0; u < units && ok; ++u, ++g) {
+                const int s = g % C::kSlots;
+                ok = __all_sync(kAll, mbar_wait(full(s), (g / C::kSlots) & 1, kWaitNs, abort));
+                tc_fence_after();
+                tc_fence_before();
+                if (ok && on) mbar_arrive_first(other(s));
+                __syncwarp();
+            }
+        for (int t = first_tile; t < tiles && ok && rank == 0; t += tile_step, ++n) {
+            const uint32_t cols = columns(tile_at(t).count);
+            const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u * C::kCtas >> 4) << 24);
+            const int b = n % C::kAccs;
+            const uint32_t d = b * kCap;
+            ok = __all_sync(kAll, mbar_wait_all<kPair>(d_empty(b), ((n / C::kAccs) & 1) ^ 1, abort));
             tc_fence_after();
             for (int u = 0; u < units && ok; ++u, ++g) {
                 const int s = g % C::kSlots;
                 ok = __all_sync(kAll, mbar_wait(full(s), (g / C::kSlots) & 1, kWaitNs, abort));
+                if (kPair && ok) ok = __all_sync(kAll, mbar_wait_all<kPair>(other(s), (g / C::kSlots) & 1, abort));
                 if (!ok) break;
-                // the loaders' stores, seen through the barrier, before the MMA's own reads; the
-                // fence stands here because there it would wait for the loads that run ahead
                 fence_async_shared();
                 tc_fence_after();
                 const uint64_t bd = desc_sw128(b_base + s * C::kBBytes);
@@ -279,28 +405,26 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
                 if (a.K - u * C::kUnit >= C::kUnit) {
 #pragma unroll
                     for (int i = 0; i < C::kUnit / 16; ++i)
-                        mma_f16_ts(on, d, ad + i * 8, bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2), idesc,
-                                   (u | i) != 0);
+                        mma_f16_ts<kPair>(on, d, ad + i * 8, bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2),
+                                          idesc, (u | i) != 0);
                 } else {
                     for (int i = 0; i < (a.K - u * C::kUnit + 15) / 16; ++i)
-                        mma_f16_ts(on, d, ad + i * 8, bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2), idesc,
-                                   (u | i) != 0);
+                        mma_f16_ts<kPair>(on, d, ad + i * 8, bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2),
+                                          idesc, (u | i) != 0);
                 }
-                mma_commit_by(on, empty(s));
+                mma_commit_by<kPair>(on, empty(s));
             }
-            if (ok) mma_commit_by(on, d_full(b));
+            if (ok) mma_commit_by<kPair>(on, d_full(b));
         }
     } else if (warp < C::kBFirst) {
         // --------------------------------------------- weights to tensor memory --
-        // (with two units a ring slot, each of them frees half of it)
         const int lanes = (warp & 3) * 32, r = lanes + lane, group = warp >> 2;
         const uint32_t lane_at = (uint32_t)lanes << 16;
-        int i0 = 0, g0 = 0;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, i0 += (units + C::kPerRaw - 1) / C::kPerRaw, g0 += units) {
+        int g0 = 0;
+        for (int t = first_tile; t < tiles && ok; t += tile_step, g0 += units) {
             for (int u = group; u < units; u += C::kAGroups) {
-                const int i = i0 + u / C::kPerRaw, rs = i % C::kRaw, g = g0 + u, s = g % C::kSlots;
-                const int part = u % C::kPerRaw;
-                ok = __all_sync(kAll, mbar_wait(raw_full(rs), (i / C::kRaw) & 1, kWaitNs, abort));
+                const int g = g0 + u, rs = g % C::kRaw, s = g % C::kSlots;
+                ok = __all_sync(kAll, mbar_wait(raw_full(rs), (g / C::kRaw) & 1, kWaitNs, abort));
                 if (!ok) break;
                 const uint32_t row = raw_base + rs * kRawBytes + r * 128;
                 uint4 v[C::kUnit / 16];
@@ -308,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
                 for (int c = 0; c < C::kUnit / 16; ++c)
                     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                                  : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
-                                 : "r"(row + (((C::kUnit / 16 * part + c) ^ (r & 7)) << 4)));
+                                 : "r"(row + ((c ^ (r & 7)) << 4)) : "memory");
 #pragma unroll
                 for (int h = 0; h < C::kUnit / 64; ++h) {
                     uint32_t f[32];
@@ -319,13 +443,13 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
                         codes_to_f16(v[4 * h + c].z, f[8 * c + 4], f[8 * c + 5]);
                         codes_to_f16(v[4 * h + c].w, f[8 * c + 6], f[8 * c + 7]);
                     }
-                    if (h == 0) {
+                    if (h == C::kUnit / 64 - 1) {
+                        // not before: every code has been read by now
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(raw_empty(rs));
-                            if (C::kPerRaw == 2 && u == units - 1 && part == 0) mbar_arrive(raw_empty(rs));  // no second unit
-                        }
-                        ok = __all_sync(kAll, mbar_wait(empty(s), ((g / C::kSlots) & 1) ^ 1, kWaitNs, abort));
+                        if (lane == 0) mbar_arrive(raw_empty(rs));
+                    }
+                    if (h == 0) {
+                        ok = __all_sync(kAll, mbar_wait_all<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort));
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -341,111 +465,137 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
     } else if (warp < C::kEpi) {
         // ------------------------------------------- tokens to shared memory --
         const int group = (warp - C::kBFirst) / C::kBWarps, bw = (warp - C::kBFirst) % C::kBWarps;
-        const int sub = lane % C::kLanes, row0 = bw * (32 / C::kLanes) + lane / C::kLanes;
-        // where lane's 16 codes of row row0 go: two 16-byte pieces, in an order that
-        // keeps the eight lanes of a store on eight banks
+        // lane: 16 codes of one of four rows; eight neighbouring lanes hold 64 of K of two
+        // rows, whose stores meet all banks once
+        static_assert(C::kLanes == 8, "lanes of a row");
+        const int sub = (lane & 3) + ((lane >> 4) << 2), row0 = bw * 4 + ((lane >> 2) & 3);
         const uint32_t at = b_base + (sub >> 2) * C::kSubBytes + row0 * 128;
         const uint32_t lo = at + (((2 * (sub & 3)) ^ (row0 & 7)) << 4), hi = at + (((2 * (sub & 3) + 1) ^ (row0 & 7)) << 4);
-        const bool odd = sub >= 4;
-        // the stream of this group's units runs kAhead ahead, over the ends of tiles
-        int at_t = blockIdx.x, at_u = group;
-        const int8_t* src[C::kPasses];
-        auto rows_of = [&](int t) {
-            if (t >= tiles) return;
-            const Tile w = tile_at(t);
-#pragma unroll
-            for (int i = 0; i < C::kPasses; ++i) {
-                const int row = i * C::kPass + row0;
-                const int r = row < w.count ? source_row(a, w.p0 + row) : -1;
-                src[i] = r >= 0 ? a.q + (long long)r * a.qs + sub * 16 : nullptr;
-            }
-        };
-        auto load = [&](uint4 (&v)[C::kPasses]) {
+        const int8_t* q = a.q + sub * 16;
+        // the stream of this group's units runs kAhead ahead, over the ends of tiles; a
+        // warp lets go of a tile's table when it has read the next one
+        int at_t = first_tile, at_u = group, at_n = 0, at_passes = 0;
+        uint32_t src[C::kPasses];
+        auto next_rows = [&]() {
             if (at_t >= tiles) return;
-            const int k = at_u * C::kUnit;
+            const int i = at_n % C::kTabs;
+            ok = __all_sync(kAll, mbar_wait(tab_full(i), (at_n / C::kTabs) & 1, kWaitNs, abort));
+            if (!ok) return;
 #pragma unroll
-            for (int i = 0; i < C::kPasses; ++i) ld_ahead(v[i], src[i] + k, src[i] != nullptr && k + sub * 16 < a.K);
+            for (int p = 0; p < C::kPasses; ++p) src[p] = token_at[i][p * C::kPass + row0];
+            at_passes = token_passes[i];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tab_empty(i));
+        };
+        auto load = [&](uint4 (&v)[C::kPasses], int& passes) {
+            if (at_t >= tiles || !ok) return;
+            const int k = at_u * C::kUnit;
+            passes = at_passes;
+#pragma unroll
+            for (int i = 0; i < C::kPasses; ++i)
+                ld_ahead(v[i], q + (uint64_t)src[i] * 16 + k, src[i] != kNoRow && k + sub * 16 < a.K);
             at_u += C::kBGroups;
             if (at_u >= units) {
                 at_u = group;
-                at_t += gridDim.x;
-                rows_of(at_t);
+                at_t += tile_step;
+                ++at_n;
+                next_rows();
             }
         };
-        if (group < units) {
+        // (a group beyond the units still reads the tables, for the counts of their barriers)
+        if (group >= units)
+            for (; at_t < tiles && ok; at_t += tile_step, ++at_n) next_rows();
+        else {
             uint4 buf[C::kAhead][C::kPasses];
-            rows_of(at_t);
+            int passes[C::kAhead];
+            next_rows();
 #pragma unroll
-            for (int j = 0; j < C::kAhead; ++j) load(buf[j]);
-            int t = blockIdx.x, u = group, g0 = 0;
-            int passes = t < tiles ? (tile_at(t).count + C::kPass - 1) / C::kPass : 0;
+            for (int j = 0; j < C::kAhead; ++j) load(buf[j], passes[j]);
+            int t = first_tile, u = group, g0 = 0;
             while (t < tiles && ok) {
 #pragma unroll
                 for (int j = 0; j < C::kAhead; ++j) {
                     if (t >= tiles || !ok) break;
                     const int g = g0 + u, s = g % C::kSlots;
-                    ok = __all_sync(kAll, mbar_wait(empty(s), ((g / C::kSlots) & 1) ^ 1, kWaitNs, abort));
+                    ok = __all_sync(kAll, mbar_wait_all<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort));
                     if (!ok) break;
 #pragma unroll
                     for (int i = 0; i < C::kPasses; ++i) {
-                        if (i >= passes) break;
+                        if (i >= passes[j]) break;
                         uint32_t f[8];
                         codes_to_f16(buf[j][i].x, f[0], f[1]);
                         codes_to_f16(buf[j][i].y, f[2], f[3]);
                         codes_to_f16(buf[j][i].z, f[4], f[5]);
                         codes_to_f16(buf[j][i].w, f[6], f[7]);
                         const uint32_t to = s * C::kBBytes + i * C::kPass * 128;  // kPass % 8 == 0: the swizzle stays
-                        st_shared16((odd ? hi : lo) + to, odd ? f[4] : f[0], odd ? f[5] : f[1], odd ? f[6] : f[2],
-                                    odd ? f[7] : f[3]);
-                        st_shared16((odd ? lo : hi) + to, odd ? f[0] : f[4], odd ? f[1] : f[5], odd ? f[2] : f[6],
-                                    odd ? f[3] : f[7]);
+                        st_shared16(lo + to, f[0], f[1], f[2], f[3]);
+                        st_shared16(hi + to, f[4], f[5], f[6], f[7]);
                     }
+                    fence_async_shared();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full(s));
-                    load(buf[j]);
+                    load(buf[j], passes[j]);
                     u += C::kBGroups;
                     if (u >= units) {
                         u = group;
-                        t += gridDim.x;
+                        t += tile_step;
                         g0 += units;
-                        if (t < tiles) passes = (tile_at(t).count + C::kPass - 1) / C::kPass;
                     }
                 }
             }
         }
     } else {
         // -------------------------------------------------------- epilogue --
-        const int ew = warp - C::kEpi, et = tid - C::kEpi * 32;
+        // warp e of the kEpiWarps: lanes (e % 4) * 32, every (kEpiWarps / 4)-th 32 columns
+        constexpr int kParts = C::kEpiWarps / 4, kMine = kCap / 32 / kParts;
+        const int ew = (warp - C::kEpi) & 3, part = (warp - C::kEpi) >> 2, et = tid - C::kEpi * 32;
         O* out = reinterpret_cast<O*>(a.out);
+        const bool pairs = a.N % 2 == 0 && a.os % 2 == 0 && (uintptr_t)a.out % 4 == 0;
         for (long long p = begin[a.E] + (long long)blockIdx.x; p < a.R; p += gridDim.x)
-            for (int n = et; n < a.N; n += 128) out[p * a.os + n] = from_f32<O>(0.f);
+            for (int n = et; n < a.N; n += 32 * C::kEpiWarps) out[p * a.os + n] = from_f32<O>(0.f);
         int n = 0;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
+        for (int t = first_tile; t < tiles && ok; t += tile_step, ++n) {
             const Tile w = tile_at(t);
-            const int b = n & 1;
-            float rs[kCap / 32];  // lane i: scale of rows i, 32 + i, ...
+            const int b = n % C::kAccs;
+            float rs[kMine];  // lane i: scale of column i of each of its 32 columns
 #pragma unroll
-            for (int i = 0; i < kCap / 32; ++i) {
-                const int c = 32 * i + lane, r = c < w.count ? source_row(a, w.p0 + c) : -1;
+            for (int i = 0; i < kMine; ++i) {
+                const int c = 32 * (i * kParts + part) + lane, r = c < w.count ? source_row(a, w.p0 + c) : -1;
                 rs[i] = r >= 0 ? a.scale[r] : 0.f;
             }
             const int ch = w.n0 + ew * 32 + lane;
             const float cs = ch < a.N ? a.w_scale[(long long)w.e * a.N + ch] : 0.f;
-            ok = __all_sync(kAll, mbar_wait(d_full(b), (n >> 1) & 1, kWaitNs, abort));
+            ok = __all_sync(kAll, mbar_wait_all<kPair>(d_full(b), (n / C::kAccs) & 1, abort));
             if (!ok) break;
             tc_fence_after();
             O* dst = out + (long long)w.p0 * a.os + ch;
+            const int last = (w.count - 1) / 32;  // the accumulator is free when its columns are in registers
+            bool held = true;
 #pragma unroll
-            for (int i = 0; i < kCap / 32; ++i) {
-                const int c0 = 32 * i;
+            for (int i = 0; i < kMine; ++i) {
+                const int c0 = 32 * (i * kParts + part);
                 if (c0 >= w.count) break;
                 uint32_t v[32];
-                tmem_ld32(((uint32_t)(ew * 32) << 16) + b * C::kDCols + c0, v);
+                tmem_ld32(((uint32_t)(ew * 32) << 16) + b * kCap + c0, v);
                 tmem_ld_wait();
-                if (c0 + 32 >= w.count) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(d_empty(b));
+                if (i * kParts + part + kParts > last) {
+                    release(b);
+                    held = false;
+                }
+                if (sizeof(O) == 2 && pairs) {
+                    // neighbouring lanes swap: the even one stores both channels of an even
+                    // position, the odd one those of the next
+                    const bool odd = lane & 1;
+                    O* at = dst + (long long)(c0 + odd) * a.os - odd;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const float x = __uint_as_float(v[c]) * __shfl_sync(kAll, rs[i], c) * cs;
+                        const float y = __uint_as_float(v[c + 1]) * __shfl_sync(kAll, rs[i], c + 1) * cs;
+                        const float z = __shfl_xor_sync(kAll, odd ? x : y, 1);
+                        const float f[2] = {odd ? z : x, odd ? y : z};
+                        if (c0 + c + odd < w.count && ch < a.N) store_chunk<O, 2>(at + c * a.os, f);
+                    }
+                    continue;
                 }
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
@@ -454,6 +604,7 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
                         dst[(long long)(c0 + c) * a.os] = from_f32<O>(__uint_as_float(v[c]) * s * cs);
                 }
             }
+            if (held) release(b);
         }
     }
     if (!ok) {
@@ -463,28 +614,49 @@ __global__ void __launch_bounds__(Cfg<kCap>::kThreads, 1) k_product_tc(const Pro
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == C::kEpi + 5) {
+    if (kPair) pair_sync();  // neither CTA leaves while the other may still reach it
+    if (warp == C::kMma) {
         tc_fence_after();
-        tmem_dealloc(tmem_slot, 512);
+        tmem_free_all<kPair>(tmem_slot);
     }
+    if (kPair) pair_sync();
 }
 
-template <int kCap, typename O>
-cudaError_t launch_cap(const Product& a, int grid, const CUtensorMap& map, cudaStream_t s) {
+// `most`: tiles at most; the grid is no larger than what runs at the same time.
+template <bool kPair, typename O>
+cudaError_t launch_kind(const Product& a, long long most, int dev, const CUtensorMap& map, cudaStream_t s) {
+    using C = Cfg<kPair>;
     static std::mutex lock;
-    static bool ready[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
+    static int fits[64] = {};  // tiles in flight, once looked up
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C::kCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
     {
         std::lock_guard<std::mutex> hold(lock);
-        if (dev >= 64 || !ready[dev]) {
-            e = cudaFuncSetAttribute(k_product_tc<kCap, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kCap>::kSmem);
+        n = dev < 64 ? fits[dev] : 0;
+        if (!n) {
+            cudaError_t e = cudaFuncSetAttribute(k_product_tc<kPair, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+            // (a pair needs two SMs of one cluster of them: not every SM finds a partner)
+            cfg.gridDim = dim3(C::kCtas);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, k_product_tc<kPair, O>, &cfg);
             if (e != cudaSuccess) return e;
-            if (dev < 64) ready[dev] = true;
+            if (n < 1) return cudaErrorInvalidConfiguration;
+            if (dev < 64) fits[dev] = n;
         }
     }
-    return launch_pdl(k_product_tc<kCap, O>, dim3(grid), dim3(Cfg<kCap>::kThreads), Cfg<kCap>::kSmem, s, a, map);
+    cfg.gridDim = dim3((unsigned)(most < n ? most : n) * C::kCtas);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_product_tc<kPair, O>, a, map);
 }
 
 template <typename O>
@@ -493,16 +665,20 @@ cudaError_t launch_o(const Product& a, const CUtensorMap& map, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const long long most = ((long long)a.R / 64 + (a.E < a.R ? a.E : a.R)) * ((a.N + 127) / 128);  // tiles, at most
-    const int grid = (int)(most < sms ? most : sms);
-    // Few rows an expert: short accumulators and a longer ring of weights.
-    return (long long)a.R <= 40LL * a.E ? launch_cap<64, O>(a, grid, map, s) : launch_cap<192, O>(a, grid, map, s);
+    // Tiles at most (one partly filled a segment).
+    const long long spread = a.E < a.R ? a.E : a.R;
+    const long long narrow = (a.R / 64 + spread) * ((a.N + 127) / 128);
+    const long long wide = (a.R / 256 + spread) * ((a.N + 255) / 256);
+    // Pairs where the segments have more than 40 positions on average and there are tiles for all of them.
+    if ((long long)a.R > 40LL * a.E && wide >= sms / 2)
+        return launch_kind<true, O>(a, wide, dev, map, s);
+    return launch_kind<false, O>(a, narrow, dev, map, s);
 }
 
 }  // namespace
 
 bool product_tc_fits(const Product& a) {
-    return a.K % 16 == 0 && a.qs % 16 == 0 && (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.wq % 16 == 0;
+    return a.K % 16 == 0 && a.qs % 16 == 0 && a.rows * (a.qs / 16) < 0xFFFFFFFFLL && (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.wq % 16 == 0;
 }
 
 cudaError_t launch_product_tc(const Product& a, moe_dtype out, cudaStream_t s) {
