@@ -121,11 +121,15 @@ __device__ __forceinline__ void mma_commit_by(uint32_t on, uint32_t bar) {
             : "memory");
 }
 
-// Arrives on the pair's first CTA's barrier at the same place as `bar` here.
+// Arrives on the pair's first CTA's barrier at the same place as `bar` here.  What
+// it orders (this CTA's shared and tensor memory, read by the pair's MMA) is local
+// and fenced for the MMA before; with release.cluster instead every arrival waits
+// for a fence over the cluster, about 2000 cycles a unit (measured: 2260 us where
+// this takes @@ us).
 __device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
     asm volatile(
         "{\n.reg .b32 r;\nmapa.shared::cluster.u32 r, %0, 0;\n"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n}" ::"r"(bar) : "memory");
+        "mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(bar) : "memory");
 }
 
 // mbar_wait for a phase that threads of the other CTA complete as well.
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
     using C = Cfg<kPair>;
     constexpr int kCap = C::kCap;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * C::kRaw + 3 * C::kSlots + 4 + 2 * C::kTabs];
+    __shared__ uint64_t bars[2 * C::kRaw + 2 * C::kSlots + 4 + 2 * C::kTabs];
     __shared__ uint32_t token_at[C::kTabs][C::kRows];  // where a tile's rows of q start, in 16 bytes
     __shared__ int token_passes[C::kTabs];
     __shared__ int first[kMaxExperts + 1];  // token tiles before each expert
@@ -241,11 +245,10 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
     auto raw_empty = [&](int i) { return bar0 + 8u * (C::kRaw + i); };
     auto full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + i); };
     auto empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + C::kSlots + i); };
-    auto other = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kSlots + i); };  // the other CTA's full
-    auto d_full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 3 * C::kSlots + i); };
-    auto d_empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 3 * C::kSlots + 2 + i); };
-    auto tab_full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 3 * C::kSlots + 4 + i); };
-    auto tab_empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 3 * C::kSlots + 4 + C::kTabs + i); };
+    auto d_full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kSlots + i); };
+    auto d_empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kSlots + 2 + i); };
+    auto tab_full = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kSlots + 4 + i); };
+    auto tab_empty = [&](int i) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kSlots + 4 + C::kTabs + i); };
     volatile int* abort = &abort_flag;
     if (tid == 0) {
         for (int i = 0; i < C::kRaw; ++i) {
@@ -253,8 +256,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             mbar_init(raw_empty(i), 4);
         }
         for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(full(i), 4 + C::kBWarps);
-            mbar_init(other(i), 1);
+            mbar_init(full(i), C::kCtas * (4 + C::kBWarps));
             mbar_init(empty(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -329,6 +331,9 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
     };
     // Accumulator columns of so many positions; each CTA of a pair holds one half.
     auto columns = [&](int count) { return (count + 16 * C::kCtas - 1) / (16 * C::kCtas) * (16 * C::kCtas); };
+    auto arrive_full = [&](int i) {
+        if (kPair) mbar_arrive_first(full(i)); else mbar_arrive(full(i));
+    };
     auto release = [&](int b) {
         tc_fence_before();
         __syncwarp();
@@ -372,20 +377,9 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
         }
     } else if (warp == C::kMma) {
         // ------------------------------------------------------------- MMA --
-        // The first CTA of a pair issues for both; in the second this warp passes on that a
-        // unit is there, one arrival over the cluster for the eight warps' (each of
-        // them would wait for its own stores to be seen there).
+        // (the first CTA of a pair issues for both)
         const uint32_t on = elect_lane();
         int g = 0, n = 0;
-        for (int t = first_tile; t < tiles && ok && rank == 1; t += tile_step)
-            for (int u = 0; u < units && ok; ++u, ++g) {
-                const int s = g % C::kSlots;
-                ok = __all_sync(kAll, mbar_wait(full(s), (g / C::kSlots) & 1, kWaitNs, abort));
-                tc_fence_after();
-                tc_fence_before();
-                if (ok && on) mbar_arrive_first(other(s));
-                __syncwarp();
-            }
         for (int t = first_tile; t < tiles && ok && rank == 0; t += tile_step, ++n) {
             const uint32_t cols = columns(tile_at(t).count);
             const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u * C::kCtas >> 4) << 24);
@@ -395,8 +389,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             tc_fence_after();
             for (int u = 0; u < units && ok; ++u, ++g) {
                 const int s = g % C::kSlots;
-                ok = __all_sync(kAll, mbar_wait(full(s), (g / C::kSlots) & 1, kWaitNs, abort));
-                if (kPair && ok) ok = __all_sync(kAll, mbar_wait_all<kPair>(other(s), (g / C::kSlots) & 1, abort));
+                ok = __all_sync(kAll, mbar_wait_all<kPair>(full(s), (g / C::kSlots) & 1, abort));
                 if (!ok) break;
                 fence_async_shared();
                 tc_fence_after();
@@ -459,7 +452,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full(s));
+                if (lane == 0) arrive_full(s);
             }
         }
     } else if (warp < C::kEpi) {
@@ -533,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                     }
                     fence_async_shared();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(full(s));
+                    if (lane == 0) arrive_full(s);
                     load(buf[j], passes[j]);
                     u += C::kBGroups;
                     if (u >= units) {
