@@ -420,26 +420,21 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                 ok = __all_sync(kAll, mbar_wait(raw_full(rs), (g / C::kRaw) & 1, kWaitNs, abort));
                 if (!ok) break;
                 const uint32_t row = raw_base + rs * kRawBytes + r * 128;
-                uint4 v[C::kUnit / 16];
-#pragma unroll
-                for (int c = 0; c < C::kUnit / 16; ++c)
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
-                                 : "r"(row + ((c ^ (r & 7)) << 4)) : "memory");
 #pragma unroll
                 for (int h = 0; h < C::kUnit / 64; ++h) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
+                                     : "r"(row + (((4 * h + c) ^ (r & 7)) << 4)) : "memory");
                     uint32_t f[32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        codes_to_f16(v[4 * h + c].x, f[8 * c], f[8 * c + 1]);
-                        codes_to_f16(v[4 * h + c].y, f[8 * c + 2], f[8 * c + 3]);
-                        codes_to_f16(v[4 * h + c].z, f[8 * c + 4], f[8 * c + 5]);
-                        codes_to_f16(v[4 * h + c].w, f[8 * c + 6], f[8 * c + 7]);
-                    }
-                    if (h == C::kUnit / 64 - 1) {
-                        // not before: every code has been read by now
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(raw_empty(rs));
+                        codes_to_f16(v[c].x, f[8 * c], f[8 * c + 1]);
+                        codes_to_f16(v[c].y, f[8 * c + 2], f[8 * c + 3]);
+                        codes_to_f16(v[c].z, f[8 * c + 4], f[8 * c + 5]);
+                        codes_to_f16(v[c].w, f[8 * c + 6], f[8 * c + 7]);
                     }
                     if (h == 0) {
                         ok = __all_sync(kAll, mbar_wait_all<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort));
@@ -452,7 +447,13 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_full(s);
+                if (lane == 0) {
+                    // the codes are let go of only here, where the stores that need them are
+                    // done: after an arrival right behind the loads, the compiler may still
+                    // sink a load below it, into the slot's next filling (seen)
+                    mbar_arrive(raw_empty(rs));
+                    arrive_full(s);
+                }
             }
         }
     } else if (warp < C::kEpi) {
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             for (int p = 0; p < C::kPasses; ++p) src[p] = token_at[i][p * C::kPass + row0];
             at_passes = token_passes[i];
             __syncwarp();
-            if (lane == 0) mbar_arrive(tab_empty(i));
+            if (lane == 0 && at_n > 0) mbar_arrive(tab_empty((at_n - 1) % C::kTabs));
         };
         auto load = [&](uint4 (&v)[C::kPasses], int& passes) {
             if (at_t >= tiles || !ok) return;
