@@ -70,6 +70,97 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const A* __restrict__ x, 
     }
 }
 
+// ---------------------------------------------------------------- few rows --
+// Single tokens: a warp takes kChan channels of one expert for up to kFew
+// positions of its segment, lane l the bytes 16 l, 16 l + 512, ... of K; products
+// by __dp4a, exact 32-bit integer sums, joined by shuffles.  Bound by the weights,
+// each read once for every kFew positions: T = 1 with six of 256 experts, K = N =
+// 4096: 19 us, 5.3 TB/s.  Block (x, p): channels 16 x .. of the segment of position p, if p
+// is the first of its kFew.
+constexpr int kFew = 4, kChan = 4;
+
+template <typename O>
+__global__ void __launch_bounds__(128) k_product_few(const Product a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ int sm_e, sm_begin, sm_end;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, p = blockIdx.y;
+    if (threadIdx.x == 0) sm_e = -1;
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += 128) {
+        const int b = segment_at(a, e), n = segment_at(a, e + 1);
+        if (b <= p && p < n) {  // (offsets that are not in order may name several: any one)
+            sm_e = e;
+            sm_begin = b;
+            sm_end = n;
+        }
+    }
+    __syncthreads();
+    const int e = sm_e, n0 = (blockIdx.x * 4 + warp) * kChan;
+    if (e < 0) {  // past the last segment: zeros
+        if (p >= segment_at(a, a.E) && lane < kChan && n0 + lane < a.N)
+            reinterpret_cast<O*>(a.out)[(long long)p * a.os + n0 + lane] = from_f32<O>(0.f);
+        return;
+    }
+    if ((p - sm_begin) % kFew != 0 || n0 >= a.N) return;
+    const int rows = min(kFew, sm_end - p);
+    const int8_t* q[kFew];
+    float s[kFew];
+#pragma unroll
+    for (int r = 0; r < kFew; ++r) {
+        const int src = r < rows ? source_row(a, p + r) : -1;
+        q[r] = a.q + (long long)max(src, 0) * a.qs + lane * 16;
+        s[r] = src >= 0 ? a.scale[src] : 0.f;
+    }
+    const int8_t* w[kChan];
+#pragma unroll
+    for (int c = 0; c < kChan; ++c) w[c] = a.wq + ((long long)e * a.N + min(n0 + c, a.N - 1)) * a.K + lane * 16;
+    int acc[kChan][kFew] = {};
+    auto add = [&](const uint4 (&v)[kChan], int k) {
+#pragma unroll
+        for (int r = 0; r < kFew; ++r) {
+            if (r >= rows) break;
+            const uint4 x = *reinterpret_cast<const uint4*>(q[r] + k);
+#pragma unroll
+            for (int c = 0; c < kChan; ++c) {
+                acc[c][r] = __dp4a((int)x.x, (int)v[c].x, acc[c][r]);
+                acc[c][r] = __dp4a((int)x.y, (int)v[c].y, acc[c][r]);
+                acc[c][r] = __dp4a((int)x.z, (int)v[c].z, acc[c][r]);
+                acc[c][r] = __dp4a((int)x.w, (int)v[c].w, acc[c][r]);
+            }
+        }
+    };
+    int k = 0;
+    for (; k + 1024 <= a.K; k += 1024) {  // two steps of every channel on their way
+        uint4 v[2][kChan];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < kChan; ++c) v[h][c] = __ldcs(reinterpret_cast<const uint4*>(w[c] + k + 512 * h));
+        add(v[0], k);
+        add(v[1], k + 512);
+    }
+    for (; k + lane * 16 < a.K; k += 512) {
+        uint4 v[kChan];
+#pragma unroll
+        for (int c = 0; c < kChan; ++c) v[c] = __ldcs(reinterpret_cast<const uint4*>(w[c] + k));
+        add(v, k);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < kChan; ++c) {
+        if (n0 + c >= a.N) break;
+        const float cs = a.w_scale[(long long)e * a.N + n0 + c];
+#pragma unroll
+        for (int r = 0; r < kFew; ++r) {
+            if (r >= rows) break;
+            const int sum = __reduce_add_sync(0xFFFFFFFFu, acc[c][r]);
+            if (lane == 0)
+                reinterpret_cast<O*>(a.out)[(long long)(p + r) * a.os + n0 + c] = from_f32<O>((float)sum * s[r] * cs);
+        }
+    }
+}
+
 // --------------------------------------------------------- any size, simple --
 // One block a tile of 32 positions of one segment x 32 channels: 32-byte steps
 // of K through shared memory, four products an instruction (__dp4a), exact
@@ -173,8 +264,16 @@ cudaError_t quantize_a(bool gated, const void* x, long long xs, long long rows, 
     return quantize_c<A, 1>(gated, x, xs, rows, K, q, qs, scale, s);
 }
 
+// Whether the CUDA cores stream the weights for every kFew positions.  At K = N =
+// 4096 they take 6.5 us for one position and 11 for 8 of one expert where the
+// tensor-core form takes 19; 16 positions of one expert 20 for 19.5, of four 22 for
+// 21, but of 16 experts 47 for 65.
+bool few_rows(const Product& a) { return a.R <= 8 || (a.R <= 16 && a.R <= a.E); }
+
 template <typename O>
 cudaError_t product_o(const Product& a, cudaStream_t s) {
+    if (product_tc_fits(a))
+        return launch_pdl(k_product_few<O>, dim3((a.N + 4 * kChan - 1) / (4 * kChan), a.R), dim3(128), 0, s, a);
     // at most one partly filled tile an expert
     const long long tiles = (long long)a.R / 32 + (a.E < a.R ? a.E : a.R);
     cudaError_t e = cudaSuccess;
@@ -233,7 +332,7 @@ extern "C" moe_status moe_expert_product(const int8_t* q, long long q_stride, in
                     out_stride};
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (product_tc_fits(a)) e = launch_product_tc(a, out_dtype, s);
+    if (product_tc_fits(a) && !few_rows(a)) e = launch_product_tc(a, out_dtype, s);
     else if (out_dtype == MOE_F32) e = product_o<float>(a, s);
     else if (out_dtype == MOE_BF16) e = product_o<__nv_bfloat16>(a, s);
     else e = product_o<__half>(a, s);

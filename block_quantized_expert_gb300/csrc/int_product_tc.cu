@@ -22,6 +22,7 @@
 // The groups of one kind take the units in turn.
 #include <cuda.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "int_product.cuh"
@@ -659,14 +660,24 @@ cudaError_t launch_o(const Product& a, const CUtensorMap& map, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    // Tiles at most (one partly filled a segment).
-    const long long spread = a.E < a.R ? a.E : a.R;
-    const long long narrow = (a.R / 64 + spread) * ((a.N + 127) / 128);
-    const long long wide = (a.R / 256 + spread) * ((a.N + 255) / 256);
-    // Pairs where the segments have more than 40 positions on average and there are tiles for all of them.
-    if ((long long)a.R > 40LL * a.E && wide >= sms / 2)
-        return launch_kind<true, O>(a, wide, dev, map, s);
-    return launch_kind<false, O>(a, narrow, dev, map, s);
+    // Narrow or wide tiles, by rounds over the GPU times what a round takes.  A segment of
+    // m positions has about m / cap + 1/2 tiles (those of the dense product are known) and
+    // at least one.  Rounds measured at K = 4096: narrow 13 us with 12 positions a tile and
+    // 18 with 62; wide 17 with 62, 20 with 100, 23 with 150, 27 with 200.  So 32 experts of
+    // 62 positions take 127 us narrow and 121 wide, of 100 228 and 142, of 300 547 and 296;
+    // one of 256 takes 23 and 31, of 512 39 and 31, of 8192 429 and 184.
+    const double segs = a.E < a.R ? a.E : a.R;
+    auto cost = [&](int cap, int channels, int at_once, double base, double a_row) {
+        const double mean = a.R / segs, each = a.E == 1 ? (a.R + cap - 1) / cap : mean / cap + 0.5;
+        const double n = each > 1 ? each : 1;
+        return std::ceil(segs * n * ((a.N + channels - 1) / channels) / at_once) * (base + a_row * mean / n);
+    };
+    auto most = [&](int cap, int channels) {  // tiles
+        return (a.R / cap + (long long)segs) * ((a.N + channels - 1) / channels);
+    };
+    if (cost(256, 256, sms / 2, 14, 0.065) < cost(64, 128, sms, 12, 0.09))
+        return launch_kind<true, O>(a, most(256, 256), dev, map, s);
+    return launch_kind<false, O>(a, most(64, 128), dev, map, s);
 }
 
 }  // namespace

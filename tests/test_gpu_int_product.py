@@ -141,10 +141,29 @@ def test_dense_product(M, K, N, dtype):
     assert torch.equal(out, again)
 
 
-@pytest.mark.parametrize("M", [1, 3, 40, 300])
+# experts, K, N, positions of each segment: wide tiles (a pair of CTAs), whole and ragged, several rounds of them
+@pytest.mark.parametrize("E,K,N,counts", [(1, 512, 2560, [2560]), (1, 4096, 1000, [4000]), (3, 1040, 4096, [700, 0, 1301]),
+                                          (16, 4096, 2048, [250, 1, 600, 0, 255, 256, 257, 90, 512, 513, 31, 700, 333, 64, 0, 800]),
+                                          (7, 272, 8192, [300, 100, 2000, 33, 1, 0, 257]), (2, 16, 16384, [1500, 900]),
+                                          (64, 1024, 1030, [150 + 3 * i for i in range(64)])])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_long_segments(E, K, N, counts, dtype):
+    ends = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    R, T = int(ends[-1]), int(ends[-1]) // 3 + 1
+    src = np.random.default_rng(N).permutation(R).astype(np.int32)
+    q, wq = codes((T, K), 21, full=True), codes((E, N, K), 22, full=True)
+    scale, w_scale = scales((T,), 23), scales((E, N), 24)
+    out = torch.full((R, N), float("nan"), dtype=dtype, device="cuda")
+    for _ in range(3):
+        bqe.moe_expert_product(q, scale, wq, w_scale, out, dev(ends), dev(src), 3)
+        want, mag, top = product64(q, scale, wq, w_scale, ends, src.astype(np.int64) // 3)
+        check(out, want, mag, top, K, dtype)
+
+
+@pytest.mark.parametrize("M", [1, 3, 40, 300, 3000])
 def test_largest_sums(M):
     """Every product 127^2 or -128 * 127: the sums pass 2^24 and stay within fp32's rounding."""
-    K, N = 4096, 64
+    K, N = 4096, 64 if M < 1000 else 2048
     q = torch.full((M, K), 127, dtype=torch.int8, device="cuda")
     wq = torch.full((1, N, K), 127, dtype=torch.int8, device="cuda")
     wq[:, N // 2:] = -128
