@@ -65,7 +65,8 @@ struct Cfg {
     static constexpr int kBBytes = kSubBytes * (kUnit / 64);
     static constexpr int kACols = kUnit / 2;                // tensor-memory columns of one unit
     static constexpr int kACol = 512 - kACols * kSlots;
-    static constexpr int kAccs = kPair ? 1 : 2;             // accumulators
+    static constexpr int kAccs = kPair ? 1 : 2;             // accumulators of a tile
+    static constexpr int kBufs = kPair ? 1 : 2;             // tiles in tensor memory
     static constexpr int kBFirst = 4 * kAGroups;
     static constexpr int kEpi = kBFirst + kBGroups * kBWarps;   // first epilogue warp; then TMA, then MMA
     static constexpr int kEpiWarps = kPair ? 8 : 4;
@@ -75,7 +76,7 @@ struct Cfg {
     // a slot of either ring always belongs to the same group: one that met every other
     // use of a slot could take the phase before last, of the same parity, for its own
     static_assert(kRaw % kAGroups == 0 && kSlots % kAGroups == 0 && kSlots % kBGroups == 0, "rings");
-    static_assert(kRows % kPass == 0 && kCap % 32 == 0 && kAccs * kCap <= kACol, "tensor memory");
+    static_assert(kRows % kPass == 0 && kCap % 32 == 0 && kBufs * kAccs * kCap <= kACol, "tensor memory");
 };
 
 // One lane of the warp, the same one each time: 1 there, 0 elsewhere.
@@ -133,26 +134,32 @@ __device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
         "mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(bar) : "memory");
 }
 
-// mbar_wait for a phase that threads of the other CTA complete as well.
-__device__ __forceinline__ bool mbar_try_wait_pair(uint32_t bar, uint32_t parity) {
+// mbar_wait for phases that come late as a rule (and, in a pair, from threads of
+// the other CTA as well): the thread is suspended for up to 100 us at a time. The
+// waiting warps' polling took a third of all issue slots.
+template <bool kPair>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if (kPair)
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+            "selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(100000u) : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            "selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(100000u) : "memory");
     return ok != 0;
 }
 
 template <bool kPair>
-__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity, volatile int* abort) {
-    if (!kPair) return mbar_wait(bar, parity, kWaitNs, abort);
-    if (mbar_try_wait_pair(bar, parity)) return true;
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+    if (try_wait<kPair>(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
-    while (true) {
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait_pair(bar, parity)) return true;
+    while (!try_wait<kPair>(bar, parity))
         if (*abort || globaltimer() - t0 > kWaitNs) return false;
-    }
+    return true;
 }
 
 __device__ __forceinline__ void pair_sync() {
@@ -350,7 +357,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             if (t >= tiles) return;
             const Tile w = tile_at(t);
             const int i = n % C::kTabs, half = columns(w.count) / C::kCtas;
-            ok = __all_sync(kAll, mbar_wait(tab_empty(i), ((n / C::kTabs) & 1) ^ 1, kWaitNs, abort));
+            ok = __all_sync(kAll, wait_for<false>(tab_empty(i), ((n / C::kTabs) & 1) ^ 1, abort));
             if (!ok) return;
             for (int row = lane; row < C::kRows; row += 32) {
                 const int at = rank * half + row;
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             look_up(t + tile_step, ++n);
             for (int k0 = 0; k0 < a.K && ok; k0 += 128, ++i) {
                 const int s = i % C::kRaw;
-                ok = __all_sync(kAll, mbar_wait(raw_empty(s), ((i / C::kRaw) & 1) ^ 1, kWaitNs, abort));
+                ok = __all_sync(kAll, wait_for<false>(raw_empty(s), ((i / C::kRaw) & 1) ^ 1, abort));
                 if (ok && lane == 0) {
                     mbar_arrive_expect_tx(raw_full(s), kRawBytes);
                     tma_load_2d(raw_base + s * kRawBytes, &wmap, k0, w.e * a.N + w.n0, raw_full(s));
@@ -379,34 +386,43 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
     } else if (warp == C::kMma) {
         // ------------------------------------------------------------- MMA --
         // (the first CTA of a pair issues for both)
+        // Narrow: N is always kCap, which costs no more than a smaller N and keeps the
+        // instruction's word a constant, and the steps take turns on two accumulators: one
+        // that waits for itself takes 51 cycles a step, two 35 (measured).  The
+        // epilogue adds the two.
         const uint32_t on = elect_lane();
-        int g = 0, n = 0;
+        const uint64_t b0 = desc_sw128(b_base);
+        int s = 0, n = 0;
+        uint32_t phase = 0;
         for (int t = first_tile; t < tiles && ok && rank == 0; t += tile_step, ++n) {
-            const uint32_t cols = columns(tile_at(t).count);
+            const uint32_t cols = kPair ? columns(tile_at(t).count) : kCap;
             const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u * C::kCtas >> 4) << 24);
-            const int b = n % C::kAccs;
-            const uint32_t d = b * kCap;
-            ok = __all_sync(kAll, mbar_wait_all<kPair>(d_empty(b), ((n / C::kAccs) & 1) ^ 1, abort));
+            const int b = n % C::kBufs;
+            const uint32_t d = b * C::kAccs * kCap;
+            ok = __all_sync(kAll, wait_for<kPair>(d_empty(b), ((n / C::kBufs) & 1) ^ 1, abort));
             tc_fence_after();
-            for (int u = 0; u < units && ok; ++u, ++g) {
-                const int s = g % C::kSlots;
-                ok = __all_sync(kAll, mbar_wait_all<kPair>(full(s), (g / C::kSlots) & 1, abort));
+            for (int k = a.K; k > 0 && ok; k -= C::kUnit) {
+                ok = __all_sync(kAll, wait_for<kPair>(full(s), phase, abort));
                 if (!ok) break;
-                fence_async_shared();
                 tc_fence_after();
-                const uint64_t bd = desc_sw128(b_base + s * C::kBBytes);
-                const uint32_t ad = C::kACol + s * C::kACols;
-                if (a.K - u * C::kUnit >= C::kUnit) {
+                const uint64_t bd = b0 + (uint64_t)(s * (C::kBBytes >> 4));
+                const uint32_t ad = C::kACol + s * C::kACols, fresh = k == a.K;
+                auto step = [&](int i) {
+                    mma_f16_ts<kPair>(on, d + (i % C::kAccs) * kCap, ad + i * 8,
+                                      bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2), idesc,
+                                      i >= C::kAccs || !fresh);
+                };
+                if (k >= C::kUnit) {
 #pragma unroll
-                    for (int i = 0; i < C::kUnit / 16; ++i)
-                        mma_f16_ts<kPair>(on, d, ad + i * 8, bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2),
-                                          idesc, (u | i) != 0);
+                    for (int i = 0; i < C::kUnit / 16; ++i) step(i);
                 } else {
-                    for (int i = 0; i < (a.K - u * C::kUnit + 15) / 16; ++i)
-                        mma_f16_ts<kPair>(on, d, ad + i * 8, bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2),
-                                          idesc, (u | i) != 0);
+                    for (int i = 0; i * 16 < k; ++i) step(i);
                 }
                 mma_commit_by<kPair>(on, empty(s));
+                if (++s == C::kSlots) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
             if (ok) mma_commit_by<kPair>(on, d_full(b));
         }
@@ -418,7 +434,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
         for (int t = first_tile; t < tiles && ok; t += tile_step, g0 += units) {
             for (int u = group; u < units; u += C::kAGroups) {
                 const int g = g0 + u, rs = g % C::kRaw, s = g % C::kSlots;
-                ok = __all_sync(kAll, mbar_wait(raw_full(rs), (g / C::kRaw) & 1, kWaitNs, abort));
+                ok = __all_sync(kAll, wait_for<false>(raw_full(rs), (g / C::kRaw) & 1, abort));
                 if (!ok) break;
                 const uint32_t row = raw_base + rs * kRawBytes + r * 128;
 #pragma unroll
@@ -438,7 +454,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                         codes_to_f16(v[c].w, f[8 * c + 6], f[8 * c + 7]);
                     }
                     if (h == 0) {
-                        ok = __all_sync(kAll, mbar_wait_all<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort));
+                        ok = __all_sync(kAll, wait_for<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort));
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -474,7 +490,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
         auto next_rows = [&]() {
             if (at_t >= tiles) return;
             const int i = at_n % C::kTabs;
-            ok = __all_sync(kAll, mbar_wait(tab_full(i), (at_n / C::kTabs) & 1, kWaitNs, abort));
+            ok = __all_sync(kAll, wait_for<false>(tab_full(i), (at_n / C::kTabs) & 1, abort));
             if (!ok) return;
 #pragma unroll
             for (int p = 0; p < C::kPasses; ++p) src[p] = token_at[i][p * C::kPass + row0];
@@ -512,7 +528,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                 for (int j = 0; j < C::kAhead; ++j) {
                     if (t >= tiles || !ok) break;
                     const int g = g0 + u, s = g % C::kSlots;
-                    ok = __all_sync(kAll, mbar_wait_all<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort));
+                    ok = __all_sync(kAll, wait_for<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort));
                     if (!ok) break;
 #pragma unroll
                     for (int i = 0; i < C::kPasses; ++i) {
@@ -551,7 +567,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
         int n = 0;
         for (int t = first_tile; t < tiles && ok; t += tile_step, ++n) {
             const Tile w = tile_at(t);
-            const int b = n % C::kAccs;
+            const int b = n % C::kBufs;
             float rs[kMine];  // lane i: scale of column i of each of its 32 columns
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
@@ -560,7 +576,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             }
             const int ch = w.n0 + ew * 32 + lane;
             const float cs = ch < a.N ? a.w_scale[(long long)w.e * a.N + ch] : 0.f;
-            ok = __all_sync(kAll, mbar_wait_all<kPair>(d_full(b), (n / C::kAccs) & 1, abort));
+            ok = __all_sync(kAll, wait_for<kPair>(d_full(b), (n / C::kBufs) & 1, abort));
             if (!ok) break;
             tc_fence_after();
             O* dst = out + (long long)w.p0 * a.os + ch;
@@ -571,7 +587,19 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                 const int c0 = 32 * (i * kParts + part);
                 if (c0 >= w.count) break;
                 uint32_t v[32];
-                tmem_ld32(((uint32_t)(ew * 32) << 16) + b * kCap + c0, v);
+                const uint32_t at = ((uint32_t)(ew * 32) << 16) + b * C::kAccs * kCap + c0;
+                tmem_ld32(at, v);
+                if (C::kAccs == 2 && a.K > 16) {  // (of one step of K there is one accumulator only)
+#pragma unroll
+                    for (int h = 0; h < 32; h += 16) {
+                        uint32_t v2[16];
+                        tmem_ld16(at + kCap + h, v2);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            v[h + c] = __float_as_uint(__uint_as_float(v[h + c]) + __uint_as_float(v2[c]));
+                    }
+                }
                 tmem_ld_wait();
                 if (i * kParts + part + kParts > last) {
                     release(b);
