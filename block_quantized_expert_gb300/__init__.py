@@ -29,7 +29,7 @@ EXPORTS = ("moe_create", "moe_destroy", "moe_route", "moe_route_hash", "moe_perm
            "moe_set_route_prune", "moe_set_wait_limit", "moe_test_stall_next_decode", "moe_test_decode_split",
            "moe_set_decode_kernel", "moe_decode_info", "moe_dispatch", "moe_dispatch_backward",
            "moe_combine", "moe_combine_backward", "moe_route_backward", "moe_quantize_rows",
-           "moe_expert_product")
+           "moe_expert_product", "moe_check_product", "moe_test_stall_next_product")
 
 
 class MoeError(RuntimeError):
@@ -100,6 +100,8 @@ def load_library(build: bool = True) -> C.CDLL:
         "moe_route_backward": ([vp, vp, vp, i, i, i, f, vp, vp], i),
         "moe_quantize_rows": ([vp, i, ll, i, i, i, vp, ll, vp, vp], i),
         "moe_expert_product": ([vp, ll, i, vp, i, vp, vp, i, i, vp, vp, i, i, vp, i, ll, vp], i),
+        "moe_check_product": ([vp], i),
+        "moe_test_stall_next_product": ([], i),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
@@ -530,3 +532,13 @@ def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, t
         None if offsets is None else _ptr(offsets, torch.int32, (E + 1,), "offsets"),
         None if row_src is None else _ptr(row_src, torch.int32, (R,), "row_src"), int(top_k), R, po, dto, so,
         _stream(stream)))
+
+
+def moe_check_product(stream=None):
+    """Synchronise the stream; raise MoeError if a wait of moe_expert_product ran out."""
+    _check(load_library().moe_check_product(_stream(stream)))
+
+
+def moe_test_stall_next_product():
+    """Test hook: the next tensor-core moe_expert_product runs out its bounded waits."""
+    _check(load_library().moe_test_stall_next_product())

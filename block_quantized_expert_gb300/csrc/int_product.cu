@@ -5,6 +5,7 @@
 //   out[p, n] = scale[r] w_scale[e, n] sum_i q[r, i] wq[e, n, i]
 //
 // for the positions p of expert e's segment, r the row that position p reads.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -270,6 +271,8 @@ cudaError_t quantize_a(bool gated, const void* x, long long xs, long long rows, 
 // 21, but of 16 experts 47 for 65.
 bool few_rows(const Product& a) { return a.R <= 8 || (a.R <= 16 && a.R <= a.E); }
 
+std::atomic<bool> g_stall_next{false};  // moe_test_stall_next_product
+
 template <typename O>
 cudaError_t product_o(const Product& a, cudaStream_t s) {
     if (product_tc_fits(a))
@@ -328,13 +331,33 @@ extern "C" moe_status moe_expert_product(const int8_t* q, long long q_stride, in
     if (!q || !scale || !wq || !w_scale || !out) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
     if ((uintptr_t)out % dtype_size(out_dtype))
         return fail(MOE_ERR_INVALID_ARG, "%s: out is not aligned to its elements", what);
-    const Product a{q, q_stride, q_rows, scale, K, wq, w_scale, n_experts, N, offsets, row_src, top_k, R, out,
-                    out_stride};
+    Product a{q, q_stride, q_rows, scale, K, wq, w_scale, n_experts, N, offsets, row_src, top_k, R, out,
+              out_stride, 2000000000ull, 0};
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (product_tc_fits(a) && !few_rows(a)) e = launch_product_tc(a, out_dtype, s);
+    if (product_tc_fits(a) && !few_rows(a)) {
+        if (g_stall_next.exchange(false)) {
+            a.stall = 1;
+            a.wait_ns = 5000000ull;
+        }
+        e = launch_product_tc(a, out_dtype, s);
+    }
     else if (out_dtype == MOE_F32) e = product_o<float>(a, s);
     else if (out_dtype == MOE_BF16) e = product_o<__nv_bfloat16>(a, s);
     else e = product_o<__half>(a, s);
     return launched(e, what);
+}
+
+extern "C" moe_status moe_check_product(moe_stream_t stream) {
+    const char* what = "moe_check_product";
+    uint32_t flag = 0;
+    const cudaError_t e = product_flag(&flag, (cudaStream_t)stream);
+    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    if (flag) return fail(MOE_ERR_TIMEOUT, "%s: a device-side wait of moe_expert_product ran out", what);
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_test_stall_next_product(void) {
+    g_stall_next = true;
+    return MOE_OK;
 }

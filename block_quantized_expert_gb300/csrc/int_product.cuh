@@ -12,6 +12,8 @@ struct Product {
     const int8_t* wq; const float* w_scale; int E, N;
     const int32_t* offsets; const int32_t* row_src; int k;
     int R; void* out; long long os;
+    unsigned long long wait_ns;  // limit of every wait of the tensor-core form
+    int stall;                   // its copies never arrive (test of that limit)
 };
 
 // Segment bound of expert e, held inside [0, R] whatever the offsets are.
@@ -28,6 +30,8 @@ __device__ __forceinline__ int source_row(const Product& a, int p) {
 // The tensor-core form (int_product_tc.cu): K and qs multiples of 16, q and wq
 // 16-byte aligned.
 bool product_tc_fits(const Product& a);
+// Its sticky error flag (common.cuh), read after the stream's work and cleared.
+cudaError_t product_flag(uint32_t* flag, cudaStream_t s);
 cudaError_t launch_product_tc(const Product& a, moe_dtype out, cudaStream_t s);
 
 }  // namespace moe

@@ -37,7 +37,6 @@ namespace {
 using namespace tc;
 
 constexpr int kRawBytes = 128 * 128;  // one ring slot of weight codes
-constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Narrow tiles are bound by the stream of weights: a long ring, one CTA a tile.
 // Wide ones are bound by the MMA and by the turning of codes: a pair of CTAs (a
@@ -154,11 +153,11 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
 }
 
 template <bool kPair>
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
     if (try_wait<kPair>(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
     while (!try_wait<kPair>(bar, parity))
-        if (*abort || globaltimer() - t0 > kWaitNs) return false;
+        if (*abort || globaltimer() - t0 > limit_ns) return false;
     return true;
 }
 
@@ -225,7 +224,7 @@ struct Tile {
     int e, n0, p0, count;
 };
 
-__device__ uint32_t g_product_err;
+__device__ uint32_t g_product_err;  // sticky, read by moe_check_product
 
 template <bool kPair, typename O>
 __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Product a, const __grid_constant__ CUtensorMap wmap) {
@@ -357,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             if (t >= tiles) return;
             const Tile w = tile_at(t);
             const int i = n % C::kTabs, half = columns(w.count) / C::kCtas;
-            ok = __all_sync(kAll, wait_for<false>(tab_empty(i), ((n / C::kTabs) & 1) ^ 1, abort));
+            ok = __all_sync(kAll, wait_for<false>(tab_empty(i), ((n / C::kTabs) & 1) ^ 1, abort, a.wait_ns));
             if (!ok) return;
             for (int row = lane; row < C::kRows; row += 32) {
                 const int at = rank * half + row;
@@ -375,10 +374,10 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             look_up(t + tile_step, ++n);
             for (int k0 = 0; k0 < a.K && ok; k0 += 128, ++i) {
                 const int s = i % C::kRaw;
-                ok = __all_sync(kAll, wait_for<false>(raw_empty(s), ((i / C::kRaw) & 1) ^ 1, abort));
+                ok = __all_sync(kAll, wait_for<false>(raw_empty(s), ((i / C::kRaw) & 1) ^ 1, abort, a.wait_ns));
                 if (ok && lane == 0) {
                     mbar_arrive_expect_tx(raw_full(s), kRawBytes);
-                    tma_load_2d(raw_base + s * kRawBytes, &wmap, k0, w.e * a.N + w.n0, raw_full(s));
+                    if (!a.stall) tma_load_2d(raw_base + s * kRawBytes, &wmap, k0, w.e * a.N + w.n0, raw_full(s));
                 }
                 __syncwarp();
             }
@@ -399,10 +398,10 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u * C::kCtas >> 4) << 24);
             const int b = n % C::kBufs;
             const uint32_t d = b * C::kAccs * kCap;
-            ok = __all_sync(kAll, wait_for<kPair>(d_empty(b), ((n / C::kBufs) & 1) ^ 1, abort));
+            ok = __all_sync(kAll, wait_for<kPair>(d_empty(b), ((n / C::kBufs) & 1) ^ 1, abort, a.wait_ns));
             tc_fence_after();
             for (int k = a.K; k > 0 && ok; k -= C::kUnit) {
-                ok = __all_sync(kAll, wait_for<kPair>(full(s), phase, abort));
+                ok = __all_sync(kAll, wait_for<kPair>(full(s), phase, abort, a.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t bd = b0 + (uint64_t)(s * (C::kBBytes >> 4));
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
         for (int t = first_tile; t < tiles && ok; t += tile_step, g0 += units) {
             for (int u = group; u < units; u += C::kAGroups) {
                 const int g = g0 + u, rs = g % C::kRaw, s = g % C::kSlots;
-                ok = __all_sync(kAll, wait_for<false>(raw_full(rs), (g / C::kRaw) & 1, abort));
+                ok = __all_sync(kAll, wait_for<false>(raw_full(rs), (g / C::kRaw) & 1, abort, a.wait_ns));
                 if (!ok) break;
                 const uint32_t row = raw_base + rs * kRawBytes + r * 128;
 #pragma unroll
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                         codes_to_f16(v[c].w, f[8 * c + 6], f[8 * c + 7]);
                     }
                     if (h == 0) {
-                        ok = __all_sync(kAll, wait_for<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort));
+                        ok = __all_sync(kAll, wait_for<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort, a.wait_ns));
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -490,7 +489,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
         auto next_rows = [&]() {
             if (at_t >= tiles) return;
             const int i = at_n % C::kTabs;
-            ok = __all_sync(kAll, wait_for<false>(tab_full(i), (at_n / C::kTabs) & 1, abort));
+            ok = __all_sync(kAll, wait_for<false>(tab_full(i), (at_n / C::kTabs) & 1, abort, a.wait_ns));
             if (!ok) return;
 #pragma unroll
             for (int p = 0; p < C::kPasses; ++p) src[p] = token_at[i][p * C::kPass + row0];
@@ -528,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                 for (int j = 0; j < C::kAhead; ++j) {
                     if (t >= tiles || !ok) break;
                     const int g = g0 + u, s = g % C::kSlots;
-                    ok = __all_sync(kAll, wait_for<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort));
+                    ok = __all_sync(kAll, wait_for<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort, a.wait_ns));
                     if (!ok) break;
 #pragma unroll
                     for (int i = 0; i < C::kPasses; ++i) {
@@ -576,7 +575,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             }
             const int ch = w.n0 + ew * 32 + lane;
             const float cs = ch < a.N ? a.w_scale[(long long)w.e * a.N + ch] : 0.f;
-            ok = __all_sync(kAll, wait_for<kPair>(d_full(b), (n / C::kBufs) & 1, abort));
+            ok = __all_sync(kAll, wait_for<kPair>(d_full(b), (n / C::kBufs) & 1, abort, a.wait_ns));
             if (!ok) break;
             tc_fence_after();
             O* dst = out + (long long)w.p0 * a.os + ch;
@@ -709,6 +708,13 @@ cudaError_t launch_o(const Product& a, const CUtensorMap& map, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t product_flag(uint32_t* flag, cudaStream_t s) {
+    const uint32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_product_err, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_product_err, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s);
+    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
+}
 
 bool product_tc_fits(const Product& a) {
     return a.K % 16 == 0 && a.qs % 16 == 0 && a.rows * (a.qs / 16) < 0xFFFFFFFFLL && (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.wq % 16 == 0;

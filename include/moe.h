@@ -372,7 +372,8 @@ moe_status moe_permute_noalloc(const int32_t* ids, int T, int top_k, int n_exper
  *    NULL.  Outputs must not overlap inputs.
  *  - Sums are held in fp32 (integer products in 32-bit integers or exactly
  *    in fp32) and rounded once, in a fixed order: equal calls give equal bits.
- *  - There is no device flag: out-of-range positions are skipped quietly. */
+ *  - Out-of-range positions are skipped quietly; the one device flag is that
+ *    of moe_check_product.                                                 */
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
 
 /* Tokens to sorted positions: xs[row_dst[t][j]] = x[t] for every filled slot.
@@ -453,6 +454,18 @@ moe_status moe_expert_product(const int8_t* q, long long q_stride, int q_rows, c
                               const int8_t* wq, const float* w_scale, int n_experts, int N,
                               const int32_t* offsets, const int32_t* row_src, int top_k, int R, void* out,
                               moe_dtype out_dtype, long long out_stride, moe_stream_t stream);
+
+/* Synchronise `stream` and report (then clear) the current device's sticky
+ * flag of moe_expert_product: MOE_OK, or MOE_ERR_TIMEOUT if a device-side
+ * wait of its tensor-core kernel ran out (2 s; that call's output is
+ * undefined, later calls are not affected).  The guard moe_set_wait_limit
+ * describes, for a call without a layer.                                  */
+moe_status moe_check_product(moe_stream_t stream);
+
+/* Test hook of that guard: in the next moe_expert_product that takes the
+ * tensor-core kernel no weight arrives, and its waits run out after 5 ms.
+ * One-shot, for the process.                                              */
+moe_status moe_test_stall_next_product(void);
 
 #ifdef __cplusplus
 }

@@ -273,3 +273,20 @@ def test_weights_past_32_bits():
     bqe.moe_expert_product(q, scale, wq, w_scale, out, dev(ends))
     want, mag, top = product64(q, scale, wq, w_scale, ends, np.arange(40))
     check(out, want, mag, top, K, F32)
+
+
+@pytest.mark.parametrize("E,M,N", [(1, 100, 256), (1, 2560, 2560)])  # one CTA a tile, a pair of CTAs a tile
+def test_a_wait_that_runs_out_is_reported(E, M, N):
+    K = 512
+    q, wq, scale, w_scale = codes((M, K), 1), codes((E, N, K), 2), scales((M,), 3), scales((E, N), 4)
+    out, want = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    bqe.moe_expert_product(q, scale, wq, w_scale, want)
+    bqe.moe_check_product()
+    bqe.moe_test_stall_next_product()
+    bqe.moe_expert_product(q, scale, wq, w_scale, out)
+    with pytest.raises(bqe.MoeError) as e:
+        bqe.moe_check_product()
+    assert e.value.status == bqe.MOE_ERR_TIMEOUT
+    bqe.moe_expert_product(q, scale, wq, w_scale, out)
+    bqe.moe_check_product()
+    assert torch.equal(out, want)
