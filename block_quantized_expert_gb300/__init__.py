@@ -123,6 +123,9 @@ def _stream(stream) -> int:
 
 
 def _ptr(t, dtype, shape=None, name="tensor"):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t is None:
         raise ValueError(f"{name} is None")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -145,17 +148,18 @@ def _rows(t, name, rows=None, width=None):
     are adjacent; the moe_dtype of int8 rows is None."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or t.dtype not in _ROW_TYPES:
+    shape, code = t.shape, _ROW_TYPES.get(t.dtype, -1)
+    if code == -1 or len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D tensor of rows in float32, bfloat16, float16 or int8, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    n, m = t.shape
+                         f"got {t.dtype} {tuple(shape)}")
+    n, m = shape
     if (rows is not None and n != rows) or (width is not None and m != width):
         raise ValueError(f"{name} must have shape ({n if rows is None else rows}, {m if width is None else width}), "
-                         f"got {tuple(t.shape)}")
+                         f"got {tuple(shape)}")
     step, inner = t.stride()
-    if m > 1 and inner != 1:
+    if inner != 1 and m > 1:
         raise ValueError(f"the elements of a row of {name} must be adjacent")
-    return t.data_ptr(), _ROW_TYPES[t.dtype], (step if n > 1 else m)
+    return t.data_ptr(), code, (step if n > 1 else m)
 
 
 def _hptr(t, dtype, shape, name):

@@ -34,40 +34,124 @@ __device__ __forceinline__ void quant_load(const A* row, int K, int c, float (&v
     }
 }
 
-template <typename A, int C, bool kGated>
-__global__ void __launch_bounds__(256) k_quantize_rows(const A* __restrict__ x, long long xs, long long rows, int K,
+// Codes of C values v, |v| <= m: rint of the quotient 127 v / m as fp32 rounds
+// it.  c = 127 / m has two roundings and v c is taken exactly, within 2^-15 of
+// that quotient, so where it is further than 2^-13 from half way between two
+// integers it rounds the same; a chunk with a value that is not, one chunk in
+// 512, is divided.  Adding 1.5 * 2^23 rounds to an integer and leaves it in the
+// low bits.  `by` is not 1 for rows of extreme size, which are all divided.
+template <int C>
+__device__ __forceinline__ Chunk<int8_t, C> quant_codes(const float (&v)[C], float c, float m, float by) {
+    constexpr float kBig = 12582912.f;
+    float near = by == 1.f ? 0.f : 1.f, n[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        n[i] = __fmaf_rn(v[i], c, kBig);
+        near = fmaxf(near, fabsf(__fmaf_rn(v[i], c, kBig - n[i])));
+    }
+    if (near > 0.5f - 0x1p-13f) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) n[i] = __fadd_rn(__fdiv_rn(__fmul_rn(v[i] * by, 127.f), m), kBig);
+    }
+    Chunk<int8_t, C> out;
+    if constexpr (C % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < C; i += 4) {
+            const uint32_t lo = __byte_perm(__float_as_uint(n[i]), __float_as_uint(n[i + 1]), 0x0040);
+            const uint32_t hi = __byte_perm(__float_as_uint(n[i + 2]), __float_as_uint(n[i + 3]), 0x0040);
+            reinterpret_cast<uint32_t*>(out.v)[i / 4] = __byte_perm(lo, hi, 0x5410);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) out.v[i] = (int8_t)__float_as_int(n[i]);
+    }
+    return out;
+}
+
+// Largest magnitude of a chunk as bits, in which infinities and NaN are above all
+// numbers: 16-bit types two at a time (both halves of the result), fp32 alone.
+template <typename A, int C>
+__device__ __forceinline__ uint32_t top_bits(const Chunk<A, C>& c, uint32_t top) {
+    if constexpr (sizeof(A) == 2 && C % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < C; i += 2)
+            top = __vmaxu2(top, *reinterpret_cast<const uint32_t*>(&c.v[i]) & 0x7FFF7FFFu);
+    } else if constexpr (sizeof(A) == 2) {
+        top = __vmaxu2(top, *reinterpret_cast<const uint16_t*>(&c.v[0]) & 0x7FFFu);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) top = max(top, *reinterpret_cast<const uint32_t*>(&c.v[i]) & 0x7FFFFFFFu);
+    }
+    return top;
+}
+
+// One block a row.  kKeep chunks of C values a thread stay in registers between
+// the maximum and the codes; kKeep = 0: rows of any length, read (and gated)
+// twice.
+template <typename A, int C, bool kGated, int kKeep>
+__global__ void __launch_bounds__(256, kGated ? 4 : 6) k_quantize_rows(const A* __restrict__ x, long long xs, int K,
                                                        int8_t* __restrict__ q, long long qs,
                                                        float* __restrict__ scale) {
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ float part[8];
-    for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
-        const A* row = x + r * xs;
-        float most = 0.f;  // of |v|, infinite where one is not finite
-        for (int c = threadIdx.x * C; c < K; c += blockDim.x * C) {
-            float v[C];
-            quant_load<A, C, kGated>(row, K, c, v);
+    __shared__ uint32_t part[8];
+    const long long row_at = blockIdx.x;
+    const A* row = x + row_at * xs;
+    const int first = threadIdx.x * C, step = blockDim.x * C;
+    // what stays: the row's own words, or the gated values
+    constexpr int kHeld = kKeep ? kKeep : 1;
+    Chunk<A, C> raw[kHeld];
+    float gated[kGated ? kHeld : 1][C];
+    uint32_t top = 0;
+    auto take = [&](int n, int c) {
+        if (kGated) {
+            quant_load<A, C, true>(row, K, c, gated[kGated ? n : 0]);
 #pragma unroll
-            for (int i = 0; i < C; ++i) most = fmaxf(most, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : INFINITY);
+            for (int i = 0; i < C; ++i) top = max(top, __float_as_uint(gated[kGated ? n : 0][i]) & 0x7FFFFFFFu);
+        } else {
+            raw[n] = load_chunk<A, C>(row + c);
+            top = top_bits<A, C>(raw[n], top);
         }
-        most = warp_max(most);
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = most;
-        __syncthreads();
-        most = part[0];
-        for (int a = 1; a < (int)(blockDim.x >> 5); ++a) most = fmaxf(most, part[a]);
-        const bool live = most > 0.f && most < INFINITY;
-        const float down = most > 0x1p119f ? 0x1p-8f : 1.f;
-        if (threadIdx.x == 0) scale[r] = most < INFINITY ? __fdiv_rn(most, 127.f) : NAN;
-        for (int c = threadIdx.x * C; c < K; c += blockDim.x * C) {
-            float v[C];
-            quant_load<A, C, kGated>(row, K, c, v);
-            Chunk<int8_t, C> out;
+    };
+    if (kKeep) {
 #pragma unroll
-            for (int i = 0; i < C; ++i)
-                out.v[i] = live ? (int8_t)__float2int_rn(__fdiv_rn(__fmul_rn(v[i] * down, 127.f), most * down)) : 0;
-            *reinterpret_cast<Chunk<int8_t, C>*>(q + r * qs + c) = out;
+        for (int n = 0; n < kKeep; ++n)
+            if (first + n * step < K) take(n, first + n * step);
+    } else {
+        for (int c = first; c < K; c += step) take(0, c);
+    }
+    if (!kGated && sizeof(A) == 2) {  // to the bits of that magnitude in fp32
+        const uint16_t h = (uint16_t)max(top & 0xFFFFu, top >> 16);
+        top = __float_as_uint(to_f32(*reinterpret_cast<const A*>(&h)));
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+    top = part[0];
+    for (int a = 1; a < (int)(blockDim.x >> 5); ++a) top = max(top, part[a]);
+    const float most = __uint_as_float(top);
+    const bool live = most > 0.f && most < INFINITY;
+    // 127 v must not overflow, nor may 1 / m
+    const float by = most > 0x1p119f ? 0x1p-8f : most < 0x1p-100f ? 0x1p100f : 1.f;
+    const float m = most * by, c127 = __fmul_rn(127.f, __frcp_rn(m));
+    if (threadIdx.x == 0) scale[row_at] = most < INFINITY ? __fdiv_rn(most, 127.f) : NAN;
+    auto put = [&](int n, int c) {
+        float v[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = kGated ? gated[kGated ? n : 0][i] : to_f32(raw[n].v[i]);
+        Chunk<int8_t, C> out = {};
+        if (live) out = quant_codes(v, c127, m, by);
+        *reinterpret_cast<Chunk<int8_t, C>*>(q + row_at * qs + c) = out;
+    };
+    if (kKeep) {
+#pragma unroll
+        for (int n = 0; n < kKeep; ++n)
+            if (first + n * step < K) put(n, first + n * step);
+    } else {
+        for (int c = first; c < K; c += step) {
+            take(0, c);
+            put(0, c);
         }
-        __syncthreads();
     }
 }
 
@@ -249,20 +333,32 @@ moe_status launched(cudaError_t e, const char* what) {
     return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-template <typename A, int C>
+template <typename A, int C, int kKeep>
 cudaError_t quantize_c(bool gated, const void* x, long long xs, long long rows, int K, int8_t* q, long long qs,
                        float* scale, cudaStream_t s) {
-    auto* f = gated ? k_quantize_rows<A, C, true> : k_quantize_rows<A, C, false>;
-    return launch_pdl(f, dim3((unsigned)rows), dim3(256), 0, s, (const A*)x, xs, rows, K, q, qs, scale);
+    const int each = kKeep ? kKeep : 1, chunks = (K + C * each - 1) / (C * each);
+    const int threads = chunks >= 256 ? 256 : (chunks + 31) / 32 * 32;
+    auto* f = gated ? k_quantize_rows<A, C, true, kKeep> : k_quantize_rows<A, C, false, kKeep>;
+    return launch_pdl(f, dim3((unsigned)rows), dim3(threads), 0, s, (const A*)x, xs, K, q, qs, scale);
 }
 
+// The widest chunk that the rows allow.  Many rows: four chunks a thread and so
+// more rows on an SM at once; few rows: more threads for each.
 template <typename A>
 cudaError_t quantize_a(bool gated, const void* x, long long xs, long long rows, int K, int8_t* q, long long qs,
                        float* scale, cudaStream_t s) {
     constexpr int W = 16 / (int)sizeof(A);
-    if (K % W == 0 && row_align(x, xs * (long long)sizeof(A)) >= 16 && row_align(q, qs) >= (unsigned)W)
-        return quantize_c<A, W>(gated, x, xs, rows, K, q, qs, scale, s);
-    return quantize_c<A, 1>(gated, x, xs, rows, K, q, qs, scale, s);
+    const unsigned ax = row_align(x, xs * (long long)sizeof(A)), aq = row_align(q, qs);
+    if (K % W == 0 && ax >= 16 && aq >= (unsigned)W) {
+        if (rows >= 1024 && K <= 1024 * W) return quantize_c<A, W, 4>(gated, x, xs, rows, K, q, qs, scale, s);
+        if (K <= 256 * W) return quantize_c<A, W, 1>(gated, x, xs, rows, K, q, qs, scale, s);
+        if (K <= 512 * W) return quantize_c<A, W, 2>(gated, x, xs, rows, K, q, qs, scale, s);
+        if (K <= 1024 * W) return quantize_c<A, W, 4>(gated, x, xs, rows, K, q, qs, scale, s);
+        return quantize_c<A, W, 0>(gated, x, xs, rows, K, q, qs, scale, s);
+    }
+    if (K % 2 == 0 && ax >= 2 * sizeof(A) && aq >= 2 && K <= 8192)
+        return quantize_c<A, 2, 16>(gated, x, xs, rows, K, q, qs, scale, s);
+    return quantize_c<A, 1, 0>(gated, x, xs, rows, K, q, qs, scale, s);
 }
 
 // Whether the CUDA cores stream the weights for every kFew positions.  At K = N =
