@@ -206,19 +206,14 @@ __device__ __forceinline__ void codes_to_f16(uint32_t v, uint32_t& lo, uint32_t&
     hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// 16 bytes, or zeros; volatile, so that it is issued here and not at its use.
-__device__ __forceinline__ void ld_ahead(uint4& v, const int8_t* p, bool on) {
-    asm volatile(
-        "{\n.reg .pred q;\nsetp.ne.b32 q, %5, 0;\nmov.b32 %0, 0;\nmov.b32 %1, 0;\nmov.b32 %2, 0;\nmov.b32 %3, 0;\n"
-        "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)on));
+// 16 bytes; volatile, so that it is issued here and not at its use.
+__device__ __forceinline__ void ld_ahead(uint4& v, const int8_t* p) {
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-
-constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 struct Tile {
     int e, n0, p0, count;
@@ -361,7 +356,8 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             for (int row = lane; row < C::kRows; row += 32) {
                 const int at = rank * half + row;
                 const int r = row < half && at < w.count ? source_row(a, w.p0 + at) : -1;
-                token_at[i][row] = r >= 0 ? (uint32_t)(r * (a.qs >> 4)) : kNoRow;
+                // positions without a row read any: none of their sums is used but times 0
+                token_at[i][row] = (uint32_t)(max(r, 0) * (a.qs >> 4));
             }
             if (lane == 0) token_passes[i] = (half + C::kPass - 1) / C::kPass;
             __syncwarp();
@@ -501,9 +497,15 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             if (at_t >= tiles || !ok) return;
             const int k = at_u * C::kUnit;
             passes = at_passes;
+            const int8_t* at = q + k;
+            if (k + C::kUnit <= a.K) {
 #pragma unroll
-            for (int i = 0; i < C::kPasses; ++i)
-                ld_ahead(v[i], q + (uint64_t)src[i] * 16 + k, src[i] != kNoRow && k + sub * 16 < a.K);
+                for (int i = 0; i < C::kPasses; ++i) ld_ahead(v[i], at + (uint64_t)src[i] * 16);
+            } else {  // past K the weights are zeros, so the codes may be anything
+#pragma unroll
+                for (int i = 0; i < C::kPasses; ++i)
+                    if (k + sub * 16 < a.K) ld_ahead(v[i], at + (uint64_t)src[i] * 16);
+            }
             at_u += C::kBGroups;
             if (at_u >= units) {
                 at_u = group;
@@ -717,7 +719,7 @@ cudaError_t product_flag(uint32_t* flag, cudaStream_t s) {
 }
 
 bool product_tc_fits(const Product& a) {
-    return a.K % 16 == 0 && a.qs % 16 == 0 && a.rows * (a.qs / 16) < 0xFFFFFFFFLL && (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.wq % 16 == 0;
+    return a.rows > 0 && a.K % 16 == 0 && a.qs % 16 == 0 && a.rows * (a.qs / 16) < 0xFFFFFFFFLL && (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.wq % 16 == 0;
 }
 
 cudaError_t launch_product_tc(const Product& a, moe_dtype out, cudaStream_t s) {
