@@ -16,8 +16,8 @@
 //                        128-byte swizzle; a gather costs nothing here
 //   4 warps              accumulators -> scales -> out, while the next tile is
 //                        summed (two accumulators)
-//   1 warp               TMA of 128 channels x 128 bytes of codes into a ring; looks
-//                        up the token rows of the next tile
+//   1 warp               TMA of 128 channels x 128 bytes of codes into a ring
+//   1 warp               token rows and scales of up to kTabs tiles ahead
 //   1 warp               the MMAs (N = the tile's rows rounded to 16)
 // The groups of one kind take the units in turn.
 #include <cuda.h>
@@ -67,10 +67,10 @@ struct Cfg {
     static constexpr int kAccs = kPair ? 1 : 2;             // accumulators of a tile
     static constexpr int kBufs = kPair ? 1 : 2;             // tiles in tensor memory
     static constexpr int kBFirst = 4 * kAGroups;
-    static constexpr int kEpi = kBFirst + kBGroups * kBWarps;   // first epilogue warp; then TMA, then MMA
+    static constexpr int kEpi = kBFirst + kBGroups * kBWarps;   // first epilogue warp; then TMA, MMA, rows
     static constexpr int kEpiWarps = kPair ? 8 : 4;
-    static constexpr int kTma = kEpi + kEpiWarps, kMma = kTma + 1;
-    static constexpr int kThreads = (kMma + 1) * 32;
+    static constexpr int kTma = kEpi + kEpiWarps, kMma = kTma + 1, kLook = kMma + 1;
+    static constexpr int kThreads = (kLook + 1) * 32;
     static constexpr int kSmem = 1024 + kSlots * kBBytes + kRaw * kRawBytes;
     // a slot of either ring always belongs to the same group: one that met every other
     // use of a slot could take the phase before last, of the same parity, for its own
@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
     __shared__ uint64_t bars[2 * C::kRaw + 2 * C::kSlots + 4 + 2 * C::kTabs];
     __shared__ uint32_t token_at[C::kTabs][C::kRows];  // where a tile's rows of q start, in 16 bytes
     __shared__ int token_passes[C::kTabs];
+    __shared__ __align__(8) float token_scale[C::kTabs][kCap];
     __shared__ int first[kMaxExperts + 1];  // token tiles before each expert
     __shared__ int begin[kMaxExperts + 1];  // its segment
     __shared__ int scan[32];
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
         }
         for (int i = 0; i < C::kTabs; ++i) {
             mbar_init(tab_full(i), 1);
-            mbar_init(tab_empty(i), C::kBGroups * C::kBWarps);
+            mbar_init(tab_empty(i), C::kBGroups * C::kBWarps + C::kEpiWarps);
         }
         abort_flag = 0;
         fence_mbar_init();
@@ -346,28 +347,10 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
     bool ok = true;
 
     if (warp == C::kTma) {
-        // ---------------- token rows of the next tile, weight codes of this one (TMA) --
-        auto look_up = [&](int t, int n) {
-            if (t >= tiles) return;
-            const Tile w = tile_at(t);
-            const int i = n % C::kTabs, half = columns(w.count) / C::kCtas;
-            ok = __all_sync(kAll, wait_for<false>(tab_empty(i), ((n / C::kTabs) & 1) ^ 1, abort, a.wait_ns));
-            if (!ok) return;
-            for (int row = lane; row < C::kRows; row += 32) {
-                const int at = rank * half + row;
-                const int r = row < half && at < w.count ? source_row(a, w.p0 + at) : -1;
-                // positions without a row read any: none of their sums is used but times 0
-                token_at[i][row] = (uint32_t)(max(r, 0) * (a.qs >> 4));
-            }
-            if (lane == 0) token_passes[i] = (half + C::kPass - 1) / C::kPass;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tab_full(i));
-        };
-        int i = 0, n = 0;
-        look_up(first_tile, 0);
+        // ------------------------------------------------- weight codes (TMA) --
+        int i = 0;
         for (int t = first_tile; t < tiles && ok; t += tile_step) {
             const Tile w = tile_at(t);
-            look_up(t + tile_step, ++n);
             for (int k0 = 0; k0 < a.K && ok; k0 += 128, ++i) {
                 const int s = i % C::kRaw;
                 ok = __all_sync(kAll, wait_for<false>(raw_empty(s), ((i / C::kRaw) & 1) ^ 1, abort, a.wait_ns));
@@ -377,6 +360,26 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                 }
                 __syncwarp();
             }
+        }
+    } else if (warp == C::kLook) {
+        // --------------------------------------- rows and scales of the tiles --
+        int n = 0;
+        for (int t = first_tile; t < tiles && ok; t += tile_step, ++n) {
+            const Tile w = tile_at(t);
+            const int i = n % C::kTabs, half = columns(w.count) / C::kCtas;
+            ok = __all_sync(kAll, wait_for<false>(tab_empty(i), ((n / C::kTabs) & 1) ^ 1, abort, a.wait_ns));
+            if (!ok) break;
+            for (int c = lane; c < kCap; c += 32) {
+                const int r = c < w.count ? source_row(a, w.p0 + c) : -1;
+                token_scale[i][c] = r >= 0 ? a.scale[r] : 0.f;
+                // this CTA's half; positions without a row read any: none of their sums is
+                // used but times 0
+                const int row = c - rank * half;
+                if (row >= 0 && row < C::kRows) token_at[i][row] = (uint32_t)(max(r, 0) * (a.qs >> 4));
+            }
+            if (lane == 0) token_passes[i] = (half + C::kPass - 1) / C::kPass;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tab_full(i));
         }
     } else if (warp == C::kMma) {
         // ------------------------------------------------------------- MMA --
@@ -569,14 +572,11 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
         for (int t = first_tile; t < tiles && ok; t += tile_step, ++n) {
             const Tile w = tile_at(t);
             const int b = n % C::kBufs;
-            float rs[kMine];  // lane i: scale of column i of each of its 32 columns
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int c = 32 * (i * kParts + part) + lane, r = c < w.count ? source_row(a, w.p0 + c) : -1;
-                rs[i] = r >= 0 ? a.scale[r] : 0.f;
-            }
+            const float* scale = token_scale[n % C::kTabs];
             const int ch = w.n0 + ew * 32 + lane;
             const float cs = ch < a.N ? a.w_scale[(long long)w.e * a.N + ch] : 0.f;
+            ok = __all_sync(kAll, wait_for<false>(tab_full(n % C::kTabs), (n / C::kTabs) & 1, abort, a.wait_ns));
+            if (!ok) break;
             ok = __all_sync(kAll, wait_for<kPair>(d_full(b), (n / C::kBufs) & 1, abort, a.wait_ns));
             if (!ok) break;
             tc_fence_after();
@@ -588,13 +588,13 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                 const int c0 = 32 * (i * kParts + part);
                 if (c0 >= w.count) break;
                 uint32_t v[32];
-                const uint32_t at = ((uint32_t)(ew * 32) << 16) + b * C::kAccs * kCap + c0;
-                tmem_ld32(at, v);
+                const uint32_t acc = ((uint32_t)(ew * 32) << 16) + b * C::kAccs * kCap + c0;
+                tmem_ld32(acc, v);
                 if (C::kAccs == 2 && a.K > 16) {  // (of one step of K there is one accumulator only)
 #pragma unroll
                     for (int h = 0; h < 32; h += 16) {
                         uint32_t v2[16];
-                        tmem_ld16(at + kCap + h, v2);
+                        tmem_ld16(acc + kCap + h, v2);
                         tmem_ld_wait();
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
@@ -606,28 +606,44 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                     release(b);
                     held = false;
                 }
+                const bool whole = c0 + 32 <= w.count && w.n0 + 128 <= a.N;
                 if (sizeof(O) == 2 && pairs) {
                     // neighbouring lanes swap: the even one stores both channels of an even
                     // position, the odd one those of the next
                     const bool odd = lane & 1;
                     O* at = dst + (long long)(c0 + odd) * a.os - odd;
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const float x = __uint_as_float(v[c]) * __shfl_sync(kAll, rs[i], c) * cs;
-                        const float y = __uint_as_float(v[c + 1]) * __shfl_sync(kAll, rs[i], c + 1) * cs;
+                    auto put = [&](int c, bool on) {
+                        const float2 s = *reinterpret_cast<const float2*>(&scale[c0 + c]);
+                        const float x = __uint_as_float(v[c]) * s.x * cs, y = __uint_as_float(v[c + 1]) * s.y * cs;
                         const float z = __shfl_xor_sync(kAll, odd ? x : y, 1);
                         const float f[2] = {odd ? z : x, odd ? y : z};
-                        if (c0 + c + odd < w.count && ch < a.N) store_chunk<O, 2>(at + c * a.os, f);
+                        if (on) store_chunk<O, 2>(at, f);
+                        at += 2 * a.os;
+                    };
+                    if (whole) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) put(c, true);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) put(c, c0 + c + odd < w.count && ch < a.N);
                     }
                     continue;
                 }
+                O* at = dst + (long long)c0 * a.os;
+                auto put = [&](int c, bool on) {
+                    if (on) *at = from_f32<O>(__uint_as_float(v[c]) * scale[c0 + c] * cs);
+                    at += a.os;
+                };
+                if (whole) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float s = __shfl_sync(kAll, rs[i], c);
-                    if (c0 + c < w.count && ch < a.N)
-                        dst[(long long)(c0 + c) * a.os] = from_f32<O>(__uint_as_float(v[c]) * s * cs);
+                    for (int c = 0; c < 32; ++c) put(c, true);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) put(c, c0 + c < w.count && ch < a.N);
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tab_empty(n % C::kTabs));
             if (held) release(b);
         }
     }
