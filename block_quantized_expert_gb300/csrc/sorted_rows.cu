@@ -84,12 +84,12 @@ __global__ void __launch_bounds__(128) k_dispatch(const char* __restrict__ x, lo
 // ----------------------------------------------------------------- combine --
 // out[t] = sum_j w[t, j] y[row_dst[t, j]] over the filled slots in ascending
 // position, which is ascending expert id, the order of the layer's own
-// combine; w = NULL stands for ones (the gradient of dispatch).  All rows of a
-// chunk are on their way before the first is added; the sum is held in fp32
-// and rounded once.  T = 8192, k = 6, H = 4096, bf16: 88 us to fp32 and 78.5 us
-// to bf16, 6.0 to 6.1 TB/s; with one chunk a thread instead of four, 115 and 101:
-// a block waits for its token's positions first.  Several tokens a block, their
-// positions looked up together, gave the same 88.
+// combine; w = NULL stands for ones (the gradient of dispatch).  Two rows of a
+// chunk are on their way at a time; the sum is held in fp32 and rounded once.
+// T = 8192, k = 6, H = 4096, bf16: 80 us to fp32 and 71.5 us to bf16, 6.6 to 6.7
+// TB/s.  Four rows at a time take 83 and 74 us, all eight 88 and 79 (their
+// registers leave fewer blocks on an SM).  With one chunk a thread instead of four
+// those 88 and 79 were 115 and 101: a block waits for its token's positions first.
 template <typename A, typename O, int C, int U>
 __global__ void __launch_bounds__(128) k_combine_rows(const A* __restrict__ y, long long ys,
                                                       const float* __restrict__ w, int T, int k, int H,
@@ -104,29 +104,33 @@ __global__ void __launch_bounds__(128) k_combine_rows(const A* __restrict__ y, l
     const int m = s.m;
     O* dst = out + t * os;
     for (int c0 = (blockIdx.y * 128 * U + threadIdx.x) * C; c0 < H; c0 += gridDim.y * 128 * U * C) {
-        Chunk<A, C> v[U][kMaxTopK];
-#pragma unroll
-        for (int a = 0; a < kMaxTopK; ++a)
-            if (a < m) {
-                const A* row = y + s.pos[a] * ys + c0;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (c0 + u * 128 * C < H) v[u][a] = load_chunk<A, C>(row + u * 128 * C);
-            }
         float acc[U][C];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < C; ++i) acc[u][i] = 0.f;
 #pragma unroll
-        for (int a = 0; a < kMaxTopK; ++a)
-            if (a < m) {
-                const float wt = s.wt[a];
+        for (int h = 0; h < kMaxTopK; h += 2) {
+            if (h >= m) break;
+            Chunk<A, C> v[2][U];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+            for (int a = 0; a < 2; ++a)
+                if (h + a < m) {
+                    const A* row = y + s.pos[h + a] * ys + c0;
 #pragma unroll
-                    for (int i = 0; i < C; ++i) acc[u][i] += wt * to_f32(v[u][a].v[i]);
-            }
+                    for (int u = 0; u < U; ++u)
+                        if (c0 + u * 128 * C < H) v[a][u] = load_chunk<A, C>(row + u * 128 * C);
+                }
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+                if (h + a < m) {
+                    const float wt = s.wt[h + a];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int i = 0; i < C; ++i) acc[u][i] += wt * to_f32(v[a][u].v[i]);
+                }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (c0 + u * 128 * C < H) store_chunk<O, C>(dst + c0 + u * 128 * C, acc[u]);
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(256) k_combine_backward(const O* __restrict__ 
 //   dl_j = (w_scale / S^2) sum_i s_i (dw_j - dw_i) * sigmoid(l_j) / (2 s_j),
 // the differences taken first, so that one kept slot gives exactly 0.  Below
 // l = -17, sigmoid(l) / (2 s) is exp(l / 2) / 2 to less than fp32's rounding.
-// One warp a token; the row of E gradients is written once, zeros and all.
+// One warp a token: the row of zeros, then the k gradients into it.
 __global__ void __launch_bounds__(128) k_route_backward(const float* __restrict__ logits,
                                                         const int32_t* __restrict__ ids,
                                                         const float* __restrict__ dw, int T, int E, int k,
@@ -236,21 +240,24 @@ __global__ void __launch_bounds__(128) k_route_backward(const float* __restrict_
             const float slope = l < -17.f ? 0.5f * expf(0.5f * l) : 1.f / (1.f + expf(-l)) / (2.f * s);
             d = w_scale / total / total * against * slope;
         }
-        int at[kMaxTopK];
-        float val[kMaxTopK];
+        // an id that stands twice: its first slot writes the sum
+        float sum = 0.f;
+        bool before = false;
 #pragma unroll
         for (int j = 0; j < kMaxTopK; ++j) {
-            at[j] = __shfl_sync(kAll, id, j);
-            val[j] = __shfl_sync(kAll, d, j);
+            const bool same = __shfl_sync(kAll, id, j) == id;
+            const float v = __shfl_sync(kAll, d, j);
+            if (same) sum += v;
+            before |= same && j < lane;
         }
         float* row = dlogits + t * E;
-        for (int e = lane; e < E; e += 32) {
-            float v = 0.f;
-#pragma unroll
-            for (int j = 0; j < kMaxTopK; ++j)
-                if (at[j] == e) v += val[j];
-            row[e] = v;
+        if (E % 4 == 0 && (uintptr_t)dlogits % 16 == 0) {
+            for (int e = 4 * lane; e < E; e += 128) *reinterpret_cast<float4*>(row + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+            for (int e = lane; e < E; e += 32) row[e] = 0.f;
         }
+        __syncwarp();  // the zeros stand before the gradients
+        if (kept && !before) row[id] = sum;
     }
 }
 
