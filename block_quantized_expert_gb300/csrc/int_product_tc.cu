@@ -8,18 +8,23 @@
 // nearly all are extreme and agree in sign; it is then rounded like any fp32 sum.
 //
 // One CTA per SM walks tiles of 128 output channels (A, one tensor-memory lane
-// a channel) x up to kCap positions of one segment (B), K in units:
+// a channel) x up to kCap positions of one segment (B), K in units of 128:
 //   kAGroups warpgroups  codes of one channel a thread -> fp16 -> tensor memory
 //                        (the A operand: it takes no shared-memory bandwidth from B)
-//   kBGroups x 4 or 8    token codes: global -> registers, a few units ahead and
-//   warps                across tiles -> fp16 -> shared memory, rows of 128 bytes,
+//   kBGroups x 4 warps   token codes: global -> registers, a few units ahead and
+//                        across tiles -> fp16 -> shared memory, rows of 128 bytes,
 //                        128-byte swizzle; a gather costs nothing here
-//   4 warps              accumulators -> scales -> out, while the next tile is
-//                        summed (two accumulators)
+//   kEpiWarps warps      accumulators -> scales -> out
 //   1 warp               TMA of 128 channels x 128 bytes of codes into a ring
+//   1 warp               the MMAs
 //   1 warp               token rows and scales of up to kTabs tiles ahead
-//   1 warp               the MMAs (N = the tile's rows rounded to 16)
-// The groups of one kind take the units in turn.
+// The groups of one kind take the units in turn, two units in the making at once.
+//
+// Measured at K = N = 4096 (bf16 out), the copy rate being 6.78 TB/s and cuBLAS's bf16
+// rate 1909 TFLOP/s: 3000 rows over 256 experts 650 us, 6.6 TB/s of weights; 49152
+// rows over 256 experts 1.34 ms, 1.23 PFLOP/s, where a fixed 14 us a round (a
+// tile's 32 units of weights, whatever its rows) weighs on tiles of 150 rows; 8192
+// rows of one expert 155 us, 1.77 PFLOP/s.
 #include <cuda.h>
 
 #include <cmath>
@@ -125,8 +130,8 @@ __device__ __forceinline__ void mma_commit_by(uint32_t on, uint32_t bar) {
 // Arrives on the pair's first CTA's barrier at the same place as `bar` here.  What
 // it orders (this CTA's shared and tensor memory, read by the pair's MMA) is local
 // and fenced for the MMA before; with release.cluster instead every arrival waits
-// for a fence over the cluster, about 2000 cycles a unit (measured: 2260 us where
-// this takes @@ us).
+// for a fence over the cluster, about 2000 cycles a unit (measured, all else equal:
+// 2260 us for the 49152 rows of 256 experts at K = N = 4096, and 1570 without).
 __device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
     asm volatile(
         "{\n.reg .b32 r;\nmapa.shared::cluster.u32 r, %0, 0;\n"
@@ -134,8 +139,8 @@ __device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
 }
 
 // mbar_wait for phases that come late as a rule (and, in a pair, from threads of
-// the other CTA as well): the thread is suspended for up to 100 us at a time. The
-// waiting warps' polling took a third of all issue slots.
+// the other CTA as well): the thread is suspended for up to 100 us at a time, so
+// that polling leaves the issue slots to the others (677 us for 684 at 3000 rows).
 template <bool kPair>
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -707,10 +712,10 @@ cudaError_t launch_o(const Product& a, const CUtensorMap& map, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // Narrow or wide tiles, by rounds over the GPU times what a round takes.  A segment of
     // m positions has about m / cap + 1/2 tiles (those of the dense product are known) and
-    // at least one.  Rounds measured at K = 4096: narrow 13 us with 12 positions a tile and
-    // 18 with 62; wide 17 with 62, 20 with 100, 23 with 150, 27 with 200.  So 32 experts of
-    // 62 positions take 127 us narrow and 121 wide, of 100 228 and 142, of 300 547 and 296;
-    // one of 256 takes 23 and 31, of 512 39 and 31, of 8192 429 and 184.
+    // at least one.  Rounds measured at K = 4096: narrow 14.0 us with 12 positions a tile,
+    // 15.3 with 31, 17.4 with 62; wide 15.6, 15.8 and 16.7, then 18.6 with 100, 20.4 with
+    // 150, 22.6 with 200.  So 32 experts of 31 positions take 107 us narrow and 110 wide, of
+    // 62 122 and 117, of 100 194 and 130; one of 256 19 and 27, of 512 32 and 28.
     const double segs = a.E < a.R ? a.E : a.R;
     auto cost = [&](int cap, int channels, int at_once, double base, double a_row) {
         const double mean = a.R / segs, each = a.E == 1 ? (a.R + cap - 1) / cap : mean / cap + 0.5;
@@ -720,7 +725,7 @@ cudaError_t launch_o(const Product& a, const CUtensorMap& map, cudaStream_t s) {
     auto most = [&](int cap, int channels) {  // tiles
         return (a.R / cap + (long long)segs) * ((a.N + channels - 1) / channels);
     };
-    if (cost(256, 256, sms / 2, 14, 0.065) < cost(64, 128, sms, 12, 0.09))
+    if (cost(256, 256, sms / 2, 14.2, 0.042) < cost(64, 128, sms, 13.1, 0.068))
         return launch_kind<true, O>(a, most(256, 256), dev, map, s);
     return launch_kind<false, O>(a, most(64, 128), dev, map, s);
 }
