@@ -157,6 +157,23 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// One look, without suspension.
+template <bool kPair>
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    if (kPair)
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 template <bool kPair>
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
     if (try_wait<kPair>(bar, parity)) return true;
@@ -393,39 +410,51 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
         // instruction's word a constant, and the steps take turns on two accumulators: one
         // that waits for itself takes 51 cycles a step, two 35 (measured).  The
         // epilogue adds the two.
+        // The next unit is looked for between the steps of this one: a look, its vote and
+        // fence take about 300 cycles, which the MMAs' queue would not cover.
         const uint32_t on = elect_lane();
         const uint64_t b0 = desc_sw128(b_base);
         int s = 0, n = 0;
         uint32_t phase = 0;
+        bool ready = false;  // unit s has been seen
         for (int t = first_tile; t < tiles && ok && rank == 0; t += tile_step, ++n) {
-            const uint32_t cols = kPair ? columns(tile_at(t).count) : kCap;
+            // (the reduction's result is known to be uniform, a value from memory is not)
+            const uint32_t cols = kPair ? __reduce_max_sync(kAll, columns(tile_at(t).count)) : kCap;
             const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u * C::kCtas >> 4) << 24);
             const int b = n % C::kBufs;
             const uint32_t d = b * C::kAccs * kCap;
             ok = __all_sync(kAll, wait_for<kPair>(d_empty(b), ((n / C::kBufs) & 1) ^ 1, abort, a.wait_ns));
             tc_fence_after();
             for (int k = a.K; k > 0 && ok; k -= C::kUnit) {
-                ok = __all_sync(kAll, wait_for<kPair>(full(s), phase, abort, a.wait_ns));
-                if (!ok) break;
-                tc_fence_after();
+                if (!ready) {
+                    ok = __all_sync(kAll, wait_for<kPair>(full(s), phase, abort, a.wait_ns));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 const uint64_t bd = b0 + (uint64_t)(s * (C::kBBytes >> 4));
-                const uint32_t ad = C::kACol + s * C::kACols, fresh = k == a.K;
+                const uint32_t ad = C::kACol + s * C::kACols, fresh = k == a.K, done = empty(s);
                 auto step = [&](int i) {
                     mma_f16_ts<kPair>(on, d + (i % C::kAccs) * kCap, ad + i * 8,
                                       bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2), idesc,
                                       i >= C::kAccs || !fresh);
                 };
-                if (k >= C::kUnit) {
-#pragma unroll
-                    for (int i = 0; i < C::kUnit / 16; ++i) step(i);
-                } else {
-                    for (int i = 0; i * 16 < k; ++i) step(i);
-                }
-                mma_commit_by<kPair>(on, empty(s));
                 if (++s == C::kSlots) {
                     s = 0;
                     phase ^= 1;
                 }
+                if (k >= C::kUnit) {
+                    const bool seen = test_wait<kPair>(full(s), phase);
+#pragma unroll
+                    for (int i = 0; i < C::kUnit / 32; ++i) step(i);
+                    ready = __all_sync(kAll, seen);
+                    if (ready) tc_fence_after();
+#pragma unroll
+                    for (int i = C::kUnit / 32; i < C::kUnit / 16; ++i) step(i);
+                } else {
+                    for (int i = 0; i * 16 < k; ++i) step(i);
+                    ready = false;
+                }
+                mma_commit_by<kPair>(on, done);
             }
             if (ok) mma_commit_by<kPair>(on, d_full(b));
         }
