@@ -21,10 +21,10 @@
 // The groups of one kind take the units in turn, two units in the making at once.
 //
 // Measured at K = N = 4096 (bf16 out), the copy rate being 6.78 TB/s and cuBLAS's bf16
-// rate 1909 TFLOP/s: 3000 rows over 256 experts 650 us, 6.6 TB/s of weights; 49152
-// rows over 256 experts 1.34 ms, 1.23 PFLOP/s, where a fixed 14 us a round (a
-// tile's 32 units of weights, whatever its rows) weighs on tiles of 150 rows; 8192
-// rows of one expert 155 us, 1.77 PFLOP/s.
+// rate 1909 TFLOP/s: 3000 rows over some 231 of 256 experts 625 us, 6.2 TB/s of
+// weights; 49152 rows over 256 experts 1.29 ms, 1.28 PFLOP/s, where a fixed 14 us a
+// round (a tile's 32 units of weights, whatever its rows) weighs on tiles of 150
+// rows; 8192 rows of one expert 155 us, 1.77 PFLOP/s.
 #include <cuda.h>
 
 #include <cmath>
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             const uint32_t cols = kPair ? __reduce_max_sync(kAll, columns(tile_at(t).count)) : kCap;
             const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u * C::kCtas >> 4) << 24);
             const int b = n % C::kBufs;
-            const uint32_t d = b * C::kAccs * kCap;
+            const uint32_t d = __reduce_max_sync(kAll, (uint32_t)(b * C::kAccs * kCap));
             ok = __all_sync(kAll, wait_for<kPair>(d_empty(b), ((n / C::kBufs) & 1) ^ 1, abort, a.wait_ns));
             tc_fence_after();
             for (int k = a.K; k > 0 && ok; k -= C::kUnit) {
@@ -431,8 +431,9 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                     if (!ok) break;
                     tc_fence_after();
                 }
-                const uint64_t bd = b0 + (uint64_t)(s * (C::kBBytes >> 4));
-                const uint32_t ad = C::kACol + s * C::kACols, fresh = k == a.K, done = empty(s);
+                const int su = __reduce_max_sync(kAll, s);  // uniform: 652 to 629 us at 3000 rows
+                const uint64_t bd = b0 + (uint64_t)(su * (C::kBBytes >> 4));
+                const uint32_t ad = C::kACol + su * C::kACols, fresh = k == a.K, done = empty(su);
                 auto step = [&](int i) {
                     mma_f16_ts<kPair>(on, d + (i % C::kAccs) * kCap, ad + i * 8,
                                       bd + (uint64_t)((i >> 2) * (C::kSubBytes >> 4) + (i & 3) * 2), idesc,
