@@ -77,8 +77,9 @@ struct Cfg {
     static constexpr int kTma = kEpi + kEpiWarps, kMma = kTma + 1, kLook = kMma + 1;
     static constexpr int kThreads = (kLook + 1) * 32;
     static constexpr int kSmem = 1024 + kSlots * kBBytes + kRaw * kRawBytes;
-    // a slot of either ring always belongs to the same group: one that met every other
-    // use of a slot could take the phase before last, of the same parity, for its own
+    // Units are counted through all tiles of a CTA and the groups take them in turn, so a
+    // slot of either ring always belongs to the same group: one that met every other use
+    // of a slot could take the phase before last, of the same parity, for its own.
     static_assert(kRaw % kAGroups == 0 && kSlots % kAGroups == 0 && kSlots % kBGroups == 0, "rings");
     static_assert(kRows % kPass == 0 && kCap % 32 == 0 && kBufs * kAccs * kCap <= kACol, "tensor memory");
 };
@@ -336,6 +337,7 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
     const int m_tiles = (a.N + 128 * C::kCtas - 1) / (128 * C::kCtas);
     const int tiles = first[a.E] * m_tiles;  // below 2^28: R <= 2^20, N <= 2^20
     const int units = (a.K + C::kUnit - 1) / C::kUnit;
+    const int my_tiles = first_tile < tiles ? (tiles - first_tile + tile_step - 1) / tile_step : 0;
 
     // Tile t: the channels of one token tile follow each other.
     auto tile_at = [&](int t) {
@@ -463,47 +465,45 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
         // --------------------------------------------- weights to tensor memory --
         const int lanes = (warp & 3) * 32, r = lanes + lane, group = warp >> 2;
         const uint32_t lane_at = (uint32_t)lanes << 16;
-        int g0 = 0;
-        for (int t = first_tile; t < tiles && ok; t += tile_step, g0 += units) {
-            for (int u = group; u < units; u += C::kAGroups) {
-                const int g = g0 + u, rs = g % C::kRaw, s = g % C::kSlots;
-                ok = __all_sync(kAll, wait_for<false>(raw_full(rs), (g / C::kRaw) & 1, abort, a.wait_ns));
-                if (!ok) break;
-                const uint32_t row = raw_base + rs * kRawBytes + r * 128;
+        const int all_units = my_tiles * units;
+        for (int g = group; g < all_units && ok; g += C::kAGroups) {
+            const int rs = g % C::kRaw, s = g % C::kSlots;
+            ok = __all_sync(kAll, wait_for<false>(raw_full(rs), (g / C::kRaw) & 1, abort, a.wait_ns));
+            if (!ok) break;
+            const uint32_t row = raw_base + rs * kRawBytes + r * 128;
 #pragma unroll
-                for (int h = 0; h < C::kUnit / 64; ++h) {
-                    uint4 v[4];
+            for (int h = 0; h < C::kUnit / 64; ++h) {
+                uint4 v[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
-                                     : "r"(row + (((4 * h + c) ^ (r & 7)) << 4)) : "memory");
-                    uint32_t f[32];
+                for (int c = 0; c < 4; ++c)
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
+                                 : "r"(row + (((4 * h + c) ^ (r & 7)) << 4)) : "memory");
+                uint32_t f[32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        codes_to_f16(v[c].x, f[8 * c], f[8 * c + 1]);
-                        codes_to_f16(v[c].y, f[8 * c + 2], f[8 * c + 3]);
-                        codes_to_f16(v[c].z, f[8 * c + 4], f[8 * c + 5]);
-                        codes_to_f16(v[c].w, f[8 * c + 6], f[8 * c + 7]);
-                    }
-                    if (h == 0) {
-                        ok = __all_sync(kAll, wait_for<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort, a.wait_ns));
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
-                    tmem_st32(lane_at + C::kACol + s * C::kACols + 32 * h, f);
+                for (int c = 0; c < 4; ++c) {
+                    codes_to_f16(v[c].x, f[8 * c], f[8 * c + 1]);
+                    codes_to_f16(v[c].y, f[8 * c + 2], f[8 * c + 3]);
+                    codes_to_f16(v[c].z, f[8 * c + 4], f[8 * c + 5]);
+                    codes_to_f16(v[c].w, f[8 * c + 6], f[8 * c + 7]);
                 }
-                if (!ok) break;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    // the codes are let go of only here, where the stores that need them are
-                    // done: after an arrival right behind the loads, the compiler may still
-                    // sink a load below it, into the slot's next filling (seen)
-                    mbar_arrive(raw_empty(rs));
-                    arrive_full(s);
+                if (h == 0) {
+                    ok = __all_sync(kAll, wait_for<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort, a.wait_ns));
+                    if (!ok) break;
+                    tc_fence_after();
                 }
+                tmem_st32(lane_at + C::kACol + s * C::kACols + 32 * h, f);
+            }
+            if (!ok) break;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                // the codes are let go of only here, where the stores that need them are
+                // done: after an arrival right behind the loads, the compiler may still
+                // sink a load below it, into the slot's next filling (seen)
+                mbar_arrive(raw_empty(rs));
+                arrive_full(s);
             }
         }
     } else if (warp < C::kEpi) {
@@ -531,6 +531,14 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
             __syncwarp();
             if (lane == 0 && at_n > 0) mbar_arrive(tab_empty((at_n - 1) % C::kTabs));
         };
+        auto to_tile = [&]() {  // (a tile may be shorter than the groups' turn)
+            while (at_u >= units && at_t < tiles && ok) {
+                at_u -= units;
+                at_t += tile_step;
+                ++at_n;
+                next_rows();
+            }
+        };
         auto load = [&](uint4 (&v)[C::kPasses], int& passes) {
             if (at_t >= tiles || !ok) return;
             const int k = at_u * C::kUnit;
@@ -545,53 +553,40 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
                     if (k + sub * 16 < a.K) ld_ahead(v[i], at + (uint64_t)src[i] * 16);
             }
             at_u += C::kBGroups;
-            if (at_u >= units) {
-                at_u = group;
-                at_t += tile_step;
-                ++at_n;
-                next_rows();
-            }
+            to_tile();
         };
-        // (a group beyond the units still reads the tables, for the counts of their barriers)
-        if (group >= units)
-            for (; at_t < tiles && ok; at_t += tile_step, ++at_n) next_rows();
-        else {
-            uint4 buf[C::kAhead][C::kPasses];
-            int passes[C::kAhead];
-            next_rows();
+        uint4 buf[C::kAhead][C::kPasses];
+        int passes[C::kAhead];
+        next_rows();
+        to_tile();
 #pragma unroll
-            for (int j = 0; j < C::kAhead; ++j) load(buf[j], passes[j]);
-            int t = first_tile, u = group, g0 = 0;
-            while (t < tiles && ok) {
+        for (int j = 0; j < C::kAhead; ++j) load(buf[j], passes[j]);
+        const int all_units = my_tiles * units;
+        int g = group;
+        while (g < all_units && ok) {
 #pragma unroll
-                for (int j = 0; j < C::kAhead; ++j) {
-                    if (t >= tiles || !ok) break;
-                    const int g = g0 + u, s = g % C::kSlots;
-                    ok = __all_sync(kAll, wait_for<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort, a.wait_ns));
-                    if (!ok) break;
+            for (int j = 0; j < C::kAhead; ++j) {
+                if (g >= all_units || !ok) break;
+                const int s = g % C::kSlots;
+                ok = __all_sync(kAll, wait_for<kPair>(empty(s), ((g / C::kSlots) & 1) ^ 1, abort, a.wait_ns));
+                if (!ok) break;
 #pragma unroll
-                    for (int i = 0; i < C::kPasses; ++i) {
-                        if (i >= passes[j]) break;
-                        uint32_t f[8];
-                        codes_to_f16(buf[j][i].x, f[0], f[1]);
-                        codes_to_f16(buf[j][i].y, f[2], f[3]);
-                        codes_to_f16(buf[j][i].z, f[4], f[5]);
-                        codes_to_f16(buf[j][i].w, f[6], f[7]);
-                        const uint32_t to = s * C::kBBytes + i * C::kPass * 128;  // kPass % 8 == 0: the swizzle stays
-                        st_shared16(lo + to, f[0], f[1], f[2], f[3]);
-                        st_shared16(hi + to, f[4], f[5], f[6], f[7]);
-                    }
-                    fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) arrive_full(s);
-                    load(buf[j], passes[j]);
-                    u += C::kBGroups;
-                    if (u >= units) {
-                        u = group;
-                        t += tile_step;
-                        g0 += units;
-                    }
+                for (int i = 0; i < C::kPasses; ++i) {
+                    if (i >= passes[j]) break;
+                    uint32_t f[8];
+                    codes_to_f16(buf[j][i].x, f[0], f[1]);
+                    codes_to_f16(buf[j][i].y, f[2], f[3]);
+                    codes_to_f16(buf[j][i].z, f[4], f[5]);
+                    codes_to_f16(buf[j][i].w, f[6], f[7]);
+                    const uint32_t to = s * C::kBBytes + i * C::kPass * 128;  // kPass % 8 == 0: the swizzle stays
+                    st_shared16(lo + to, f[0], f[1], f[2], f[3]);
+                    st_shared16(hi + to, f[4], f[5], f[6], f[7]);
                 }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) arrive_full(s);
+                load(buf[j], passes[j]);
+                g += C::kBGroups;
             }
         }
     } else {

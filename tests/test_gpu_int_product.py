@@ -290,3 +290,20 @@ def test_a_wait_that_runs_out_is_reported(E, M, N):
     bqe.moe_expert_product(q, scale, wq, w_scale, out)
     bqe.moe_check_product()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("K,M,N", [(128, 20000, 4096), (384, 12000, 4096), (1152, 12000, 4096), (640, 4000, 2048)])
+def test_odd_units_over_many_tiles(K, M, N):
+    """An odd number of K units a tile, many tiles a CTA: every call gives the exact sums."""
+    q, wq = codes((M, K), 31), codes((3, N, K), 32)
+    scale, w_scale = scales((M,), 33), scales((3, N), 34)
+    ends = np.array([0, M // 2, M // 2 + 300, M], np.int32)
+    want, mag, top = product64(q, scale, wq, w_scale, ends, np.arange(M))
+    first = torch.empty(M, N, device="cuda")
+    bqe.moe_expert_product(q, scale, wq, w_scale, first, dev(ends))
+    check(first, want, mag, top, K, F32)
+    out = torch.empty(M, N, device="cuda")
+    for _ in range(10):
+        out.fill_(float("nan"))
+        bqe.moe_expert_product(q, scale, wq, w_scale, out, dev(ends))
+        assert torch.equal(out, first)
