@@ -231,7 +231,7 @@ __device__ __forceinline__ void codes_to_f16(uint32_t v, uint32_t& lo, uint32_t&
 
 // 16 bytes; volatile, so that it is issued here and not at its use.
 __device__ __forceinline__ void ld_ahead(uint4& v, const int8_t* p) {
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {

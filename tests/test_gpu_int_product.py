@@ -307,3 +307,27 @@ def test_odd_units_over_many_tiles(K, M, N):
         out.fill_(float("nan"))
         bqe.moe_expert_product(q, scale, wq, w_scale, out, dev(ends))
         assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("M", [2, 90, 3000])
+def test_calls_in_a_row_read_what_the_last_one_wrote(M):
+    """Codes and scales are written again before every product, into the same buffers."""
+    K, N, n = 512, 2048, 30
+    wq, w_scale = codes((1, N, K), 2), scales((1, N), 3)
+    x = torch.randn(n, M, K, device="cuda")
+    q, scale = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    want, got = torch.empty(n, M, N, device="cuda"), torch.zeros(n, M, N, device="cuda")
+    for i in range(n):
+        bqe.moe_quantize_rows(x[i], q, scale)
+        torch.cuda.synchronize()
+        bqe.moe_expert_product(q, scale, wq, w_scale, want[i])
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(n):
+            bqe.moe_quantize_rows(x[i], q, scale)
+            bqe.moe_expert_product(q, scale, wq, w_scale, got[i])
+    for _ in range(5):
+        got.zero_()
+        graph.replay()
+        assert torch.equal(got, want)

@@ -269,3 +269,24 @@ def test_offsets_past_32_bits():
     bqe.moe_combine_backward(x, xs, torch.full((T, k), 0.25, device="cuda"), offsets, row_dst, xs.clone(), dw)
     norm = x.double().square().sum(1, keepdim=True)
     assert torch.all((dw.double() - norm).abs() <= (H + 1) * EPS * norm)
+
+
+@pytest.mark.parametrize("T,H", [(4, 512), (64, 256), (700, 1024)])
+def test_calls_in_a_row_read_what_the_last_one_wrote(T, H):
+    """Each call's kernel may start before the one in front of it ends: its rows
+    must be the new ones all the same, also where the buffer was read before."""
+    k, E, n = 3, 4, 60
+    _, _, _, offsets, _, row_dst = S.routing(T, k, E, 5)
+    off, dst, w = dev(offsets), dev(row_dst), torch.ones(T, k, device="cuda")
+    xs, outs = torch.zeros(T * k, H, device="cuda"), torch.empty(n, T, H, device="cuda")
+    x = torch.arange(1.0, n + 1, device="cuda")[:, None, None].expand(n, T, H).contiguous()
+    graph = torch.cuda.CUDAGraph()
+    bqe.moe_dispatch(x[0], off, dst, xs)
+    with torch.cuda.graph(graph):
+        for i in range(n):
+            bqe.moe_dispatch(x[i], off, dst, xs)
+            bqe.moe_combine(xs, w, dst, outs[i])
+    for _ in range(5):
+        outs.zero_()
+        graph.replay()
+        assert torch.equal(outs, k * x)
