@@ -420,6 +420,13 @@ def moe_last_error(layer: Optional[Layer] = None) -> str:
     return m.decode() if m else ""
 
 
+def _here(stream) -> int:
+    """_stream for calls that hold a CUDA tensor, so that PyTorch's CUDA is up."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _stream(stream)
+
+
 def _slots(row_dst, T, name="row_dst"):
     """(pointer, top_k) of the slots [T][top_k], also given flat."""
     n = row_dst.numel()
@@ -440,8 +447,11 @@ def moe_dispatch(x, offsets, row_dst, xs, stream=None):
     ps, dts, ss = _rows(xs, "xs", T * k, H)
     if dt is None or dts != dt:
         raise ValueError("x and xs must have one floating dtype")
-    _check(load_library().moe_dispatch(px, dt, sx, T, k, H, _ptr(offsets, torch.int32, None, "offsets"),
-                                       offsets.numel() - 1, dst, ps, ss, _stream(stream)))
+    lib = _lib or load_library()
+    st = lib.moe_dispatch(px, dt, sx, T, k, H, _ptr(offsets, torch.int32, None, "offsets"),
+                          offsets.numel() - 1, dst, ps, ss, _here(stream))
+    if st:
+        _check(st)
 
 
 def moe_dispatch_backward(dxs, row_dst, dx, stream=None):
@@ -454,7 +464,10 @@ def moe_dispatch_backward(dxs, row_dst, dx, stream=None):
     px, dt, sx = _rows(dx, "dx")
     if dt is None or dts is None:
         raise ValueError("dxs and dx must be floating tensors")
-    _check(load_library().moe_dispatch_backward(ps, dts, ss, T, k, H, dst, px, dt, sx, _stream(stream)))
+    lib = _lib or load_library()
+    st = lib.moe_dispatch_backward(ps, dts, ss, T, k, H, dst, px, dt, sx, _here(stream))
+    if st:
+        _check(st)
 
 
 def moe_combine(y, w, row_dst, out, stream=None):
@@ -467,8 +480,11 @@ def moe_combine(y, w, row_dst, out, stream=None):
     po, dto, so = _rows(out, "out")
     if dty is None or dto is None:
         raise ValueError("y and out must be floating tensors")
-    _check(load_library().moe_combine(py, dty, sy, _ptr(w, torch.float32, (T, k), "w"), T, k, H, dst, po, dto, so,
-                                      _stream(stream)))
+    lib = _lib or load_library()
+    st = lib.moe_combine(py, dty, sy, _ptr(w, torch.float32, (T, k), "w"), T, k, H, dst, po, dto, so,
+                         _here(stream))
+    if st:
+        _check(st)
 
 
 def moe_combine_backward(dout, y, w, offsets, row_dst, dy, dw, stream=None):
@@ -483,9 +499,12 @@ def moe_combine_backward(dout, y, w, offsets, row_dst, dy, dw, stream=None):
     pg, dtg, sg = _rows(dy, "dy", T * k, H)
     if dtd is None or dty is None or dtg != dty:
         raise ValueError("y and dy must have one floating dtype, and dout be a floating tensor")
-    _check(load_library().moe_combine_backward(pd, dtd, sd, py, dty, sy, _ptr(w, torch.float32, (T, k), "w"), T, k, H,
-                                               _ptr(offsets, torch.int32, None, "offsets"), offsets.numel() - 1, dst,
-                                               pg, sg, _ptr(dw, torch.float32, (T, k), "dw"), _stream(stream)))
+    lib = _lib or load_library()
+    st = lib.moe_combine_backward(pd, dtd, sd, py, dty, sy, _ptr(w, torch.float32, (T, k), "w"), T, k, H,
+                                  _ptr(offsets, torch.int32, None, "offsets"), offsets.numel() - 1, dst, pg,
+                                  sg, _ptr(dw, torch.float32, (T, k), "dw"), _here(stream))
+    if st:
+        _check(st)
 
 
 def moe_route_backward(logits, ids, dw, dlogits, w_scale: float = 1.5, stream=None):
@@ -494,10 +513,13 @@ def moe_route_backward(logits, ids, dw, dlogits, w_scale: float = 1.5, stream=No
     k = ids.shape[1]
     if T == 0:
         return
-    _check(load_library().moe_route_backward(_ptr(logits, torch.float32, (T, E), "logits"),
-                                             _ptr(ids, torch.int32, (T, k), "ids"),
-                                             _ptr(dw, torch.float32, (T, k), "dw"), T, E, k, float(w_scale),
-                                             _ptr(dlogits, torch.float32, (T, E), "dlogits"), _stream(stream)))
+    lib = _lib or load_library()
+    st = lib.moe_route_backward(_ptr(logits, torch.float32, (T, E), "logits"),
+                                _ptr(ids, torch.int32, (T, k), "ids"), _ptr(dw, torch.float32, (T, k), "dw"),
+                                T, E, k, float(w_scale), _ptr(dlogits, torch.float32, (T, E), "dlogits"),
+                                _here(stream))
+    if st:
+        _check(st)
 
 
 def moe_quantize_rows(x, q, scale, gated: bool = False, stream=None):
@@ -510,8 +532,11 @@ def moe_quantize_rows(x, q, scale, gated: bool = False, stream=None):
     pq, dtq, sq = _rows(q, "q")
     if dt is None or dtq is not None:
         raise ValueError("x must be a floating tensor and q int8")
-    _check(load_library().moe_quantize_rows(px, dt, sx, int(bool(gated)), rows, K, pq, sq,
-                                            _ptr(scale, torch.float32, (rows,), "scale"), _stream(stream)))
+    lib = _lib or load_library()
+    st = lib.moe_quantize_rows(px, dt, sx, int(bool(gated)), rows, K, pq, sq,
+                               _ptr(scale, torch.float32, (rows,), "scale"), _here(stream))
+    if st:
+        _check(st)
 
 
 def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, top_k: int = 1, stream=None):
@@ -530,12 +555,15 @@ def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, t
     if dtq is not None or dto is None:
         raise ValueError("q must be int8 and out a floating tensor")
     rows = q.shape[0]
-    _check(load_library().moe_expert_product(
-        pq, sq, rows, _ptr(scale, torch.float32, (rows,), "scale"), K, _ptr(wq, torch.int8, (E, N, K), "wq"),
-        _ptr(w_scale, torch.float32, (E, N), "w_scale"), E, N,
-        None if offsets is None else _ptr(offsets, torch.int32, (E + 1,), "offsets"),
-        None if row_src is None else _ptr(row_src, torch.int32, (R,), "row_src"), int(top_k), R, po, dto, so,
-        _stream(stream)))
+    lib = _lib or load_library()
+    st = lib.moe_expert_product(pq, sq, rows, _ptr(scale, torch.float32, (rows,), "scale"), K,
+                                _ptr(wq, torch.int8, (E, N, K), "wq"),
+                                _ptr(w_scale, torch.float32, (E, N), "w_scale"), E, N,
+                                None if offsets is None else _ptr(offsets, torch.int32, (E + 1,), "offsets"),
+                                None if row_src is None else _ptr(row_src, torch.int32, (R,), "row_src"),
+                                int(top_k), R, po, dto, so, _here(stream))
+    if st:
+        _check(st)
 
 
 def moe_check_product(stream=None):
