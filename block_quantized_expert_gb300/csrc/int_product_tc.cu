@@ -21,8 +21,8 @@
 // The groups of one kind take the units in turn, two units in the making at once.
 //
 // Measured at K = N = 4096 (bf16 out), the copy rate being 6.78 TB/s and cuBLAS's bf16
-// rate 1909 TFLOP/s: 3000 rows over some 231 of 256 experts 625 us, 6.2 TB/s of
-// weights; 49152 rows over 256 experts 1.29 ms, 1.28 PFLOP/s, where a fixed 14 us a
+// rate 1909 TFLOP/s: 3000 rows over some 231 of 256 experts 630 us, 6.2 TB/s of
+// weights; 49152 rows over 256 experts 1.27 ms, 1.30 PFLOP/s, where a fixed 14 us a
 // round (a tile's 32 units of weights, whatever its rows) weighs on tiles of 150
 // rows; 8192 rows of one expert 155 us, 1.77 PFLOP/s.
 #include <cuda.h>
