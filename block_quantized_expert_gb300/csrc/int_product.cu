@@ -246,23 +246,37 @@ __global__ void __launch_bounds__(128) k_product_few(const Product a) {
     }
 }
 
-// --------------------------------------------------------- any size, simple --
-// One block a tile of 32 positions of one segment x 32 channels: 32-byte steps
-// of K through shared memory, four products an instruction (__dp4a), exact
-// 32-bit integer sums.  Reads K byte by byte, so any K, stride and alignment.
-template <typename O>
+// ---------------------------------------------------------------- any size --
+// Any K, stride and alignment: one block a tile of 64 positions of one segment x
+// 64 channels, 64 bytes of K at a time through shared memory, 4 x 4 sums a thread
+// by __dp4a (exact 32-bit integers): 8192 rows, K = N = 1000, 166 us (bound by the
+// issue of loads and sums, 0.1 PFLOP/s).  kWords: K, stride and bases allow four codes a
+// load, else they come one by one (777 rows, K = 1101, N = 1001: 78 us for 35 at K = 1100).
+template <bool kWords>
+__device__ __forceinline__ int codes4(const int8_t* row, int c, int K) {
+    if (row == nullptr || c >= K) return 0;
+    if (kWords) return *reinterpret_cast<const int*>(row + c);
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (c + i < K) v |= (uint32_t)(uint8_t)row[c + i] << (8 * i);
+    return (int)v;
+}
+
+template <typename O, bool kWords>
 __global__ void __launch_bounds__(256) k_product_any(const Product a) {
     pdl_launch_dependents();
     pdl_wait();
+    constexpr int kTile = 64;
     __shared__ int sm_e, sm_j;
-    __shared__ int8_t xs[32][36], ws[32][36];
-    __shared__ int src[32];
+    __shared__ int xs[kTile][17], ws[kTile][17];  // 16 words of four codes a row
+    __shared__ int src[kTile];
     const int tid = threadIdx.x;
     if (tid == 0) {
         int left = blockIdx.y;
         sm_e = -1;
         for (int e = 0; e < a.E; ++e) {
-            const int n = (max(segment_at(a, e + 1) - segment_at(a, e), 0) + 31) / 32;
+            const int n = (max(segment_at(a, e + 1) - segment_at(a, e), 0) + kTile - 1) / kTile;
             if (left < n) {
                 sm_e = e;
                 sm_j = left;
@@ -272,41 +286,57 @@ __global__ void __launch_bounds__(256) k_product_any(const Product a) {
         }
     }
     __syncthreads();
-    const int e = sm_e, n0 = blockIdx.x * 32;
+    const int e = sm_e, n0 = blockIdx.x * kTile;
     if (e < 0) return;
-    const int p0 = segment_at(a, e) + 32 * sm_j;
-    const int count = min(32, segment_at(a, e + 1) - p0);
-    if (tid < 32) src[tid] = tid < count ? source_row(a, p0 + tid) : -1;
+    const int p0 = segment_at(a, e) + kTile * sm_j;
+    const int count = min(kTile, segment_at(a, e + 1) - p0);
+    if (tid < kTile) src[tid] = tid < count ? source_row(a, p0 + tid) : -1;
     __syncthreads();
-    const int tx = tid & 15, ty = tid >> 4;  // channels tx, tx + 16; positions ty, ty + 16
-    int acc[2][2] = {{0, 0}, {0, 0}};
-    for (int k0 = 0; k0 < a.K; k0 += 32) {
-        for (int i = tid; i < 32 * 32; i += 256) {
-            const int r = i >> 5, c = k0 + (i & 31);
-            xs[r][i & 31] = c < a.K && src[r] >= 0 ? a.q[src[r] * a.qs + c] : 0;
-            ws[r][i & 31] = c < a.K && n0 + r < a.N ? a.wq[((long long)e * a.N + n0 + r) * a.K + c] : 0;
+    // this thread brings word lw of rows lr, lr + 16, ... and sums channels tx + 16 j, positions ty + 16 i
+    const int lw = tid & 15, lr = tid >> 4, tx = tid & 15, ty = tid >> 4;
+    const int8_t *xrow[4], *wrow[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = lr + 16 * i;
+        xrow[i] = src[r] >= 0 ? a.q + src[r] * a.qs : nullptr;
+        wrow[i] = n0 + r < a.N ? a.wq + ((long long)e * a.N + n0 + r) * a.K : nullptr;
+    }
+    int acc[4][4] = {};
+    for (int k0 = 0; k0 < a.K; k0 += 64) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            xs[lr + 16 * i][lw] = codes4<kWords>(xrow[i], k0 + 4 * lw, a.K);
+            ws[lr + 16 * i][lw] = codes4<kWords>(wrow[i], k0 + 4 * lw, a.K);
         }
         __syncthreads();
 #pragma unroll
-        for (int c = 0; c < 32; c += 4)
+        for (int c = 0; c < 16; ++c) {
+            int x[4], w[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i) {
+                x[i] = xs[ty + 16 * i][c];
+                w[i] = ws[tx + 16 * i][c];
+            }
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __dp4a(*reinterpret_cast<const int*>(&xs[ty + 16 * i][c]),
-                                       *reinterpret_cast<const int*>(&ws[tx + 16 * j][c]), acc[i][j]);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(x[i], w[j], acc[i][j]);
+        }
         __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i) {
+        const int p = ty + 16 * i;
+        if (p >= count) continue;
+        const float s = src[p] >= 0 ? a.scale[src[p]] : 0.f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int p = ty + 16 * i, n = n0 + tx + 16 * j;
-            if (p >= count || n >= a.N) continue;
-            const float s = src[p] >= 0 ? a.scale[src[p]] : 0.f;
-            reinterpret_cast<O*>(a.out)[(long long)(p0 + p) * a.os + n] =
-                from_f32<O>((float)acc[i][j] * s * a.w_scale[(long long)e * a.N + n]);
+        for (int j = 0; j < 4; ++j) {
+            const int n = n0 + tx + 16 * j;
+            if (n < a.N)
+                reinterpret_cast<O*>(a.out)[(long long)(p0 + p) * a.os + n] =
+                    from_f32<O>((float)acc[i][j] * s * a.w_scale[(long long)e * a.N + n]);
         }
+    }
 }
 
 // Positions past the last segment are written as zeros.
@@ -374,10 +404,11 @@ cudaError_t product_o(const Product& a, cudaStream_t s) {
     if (product_tc_fits(a))
         return launch_pdl(k_product_few<O>, dim3((a.N + 4 * kChan - 1) / (4 * kChan), a.R), dim3(128), 0, s, a);
     // at most one partly filled tile an expert
-    const long long tiles = (long long)a.R / 32 + (a.E < a.R ? a.E : a.R);
-    cudaError_t e = cudaSuccess;
+    const long long tiles = (long long)a.R / 64 + (a.E < a.R ? a.E : a.R);
     if (tiles > 65535) return cudaErrorInvalidConfiguration;
-    e = launch_pdl(k_product_any<O>, dim3((a.N + 31) / 32, (unsigned)tiles), dim3(256), 0, s, a);
+    const bool words = a.K % 4 == 0 && a.qs % 4 == 0 && (uintptr_t)a.q % 4 == 0 && (uintptr_t)a.wq % 4 == 0;
+    auto* f = words ? k_product_any<O, true> : k_product_any<O, false>;
+    cudaError_t e = launch_pdl(f, dim3((a.N + 63) / 64, (unsigned)tiles), dim3(256), 0, s, a);
     if (e == cudaSuccess && a.offsets) e = launch_pdl(k_product_tail<O>, dim3(a.R < 152 ? a.R : 152), dim3(256), 0, s, a);
     return e;
 }

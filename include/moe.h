@@ -448,8 +448,11 @@ moe_status moe_quantize_rows(const void* x, moe_dtype dtype, long long x_stride,
  *   row_src device i32 [R]: position p reads row r = row_src[p] / top_k (the
  *   tokens quantised once, read by each of their experts; an r outside
  *   [0, q_rows) reads as zeros); NULL: r = p.
- * The integer sum is exact while |sum| <= 2^24 and else accurate to fp32's
- * rounding.  1 <= K <= 131072, 1 <= N <= 2^20, R <= 2^20.                 */
+ * The integer sum is exact while the sum of |q * wq| is at most 2^24, and
+ * else accurate to fp32's rounding.  1 <= K <= 131072, 1 <= N <= 2^20,
+ * R <= 2^20.  The tensor cores take K and q_stride in multiples of 16 and q
+ * and wq on 16-byte boundaries; anything else runs on the CUDA cores, an
+ * order of magnitude slower.                                              */
 moe_status moe_expert_product(const int8_t* q, long long q_stride, int q_rows, const float* scale, int K,
                               const int8_t* wq, const float* w_scale, int n_experts, int N,
                               const int32_t* offsets, const int32_t* row_src, int top_k, int R, void* out,
