@@ -1368,10 +1368,6 @@ static bool make_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t r
     return r == CUDA_SUCCESS;
 }
 
-bool make_byte_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
-    return make_map(m, base, cols, rows, box_rows, false);
-}
-
 static bool make_act_maps(ActMaps* m, const void* base, uint64_t cols, uint64_t rows) {
     return make_map(&m->b32, base, cols, rows, 32, false) && make_map(&m->b64, base, cols, rows, 64, false) &&
            make_map(&m->b128, base, cols, rows, 128, false);

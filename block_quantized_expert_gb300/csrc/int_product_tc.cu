@@ -35,8 +35,6 @@
 
 namespace moe {
 
-bool make_byte_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows);
-
 namespace {
 
 using namespace tc;
@@ -692,6 +690,24 @@ __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Pr
     if (kPair) pair_sync();
 }
 
+// Map over the codes of all experts, [rows][K]: boxes of 128 bytes x 128 rows, 128-byte swizzle.
+bool map_weights(CUtensorMap* m, const int8_t* wq, uint64_t K, uint64_t rows) {
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static const Encode encode = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(p) : nullptr;
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {K, rows}, strides[1] = {K};
+    const cuuint32_t box[2] = {128, 128}, step[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(wq), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // `most`: tiles at most; the grid is no larger than what runs at the same time.
 template <bool kPair, typename O>
 cudaError_t launch_kind(const Product& a, long long most, int dev, const CUtensorMap& map, cudaStream_t s) {
@@ -770,7 +786,7 @@ bool product_tc_fits(const Product& a) {
 
 cudaError_t launch_product_tc(const Product& a, moe_dtype out, cudaStream_t s) {
     CUtensorMap map;
-    if (!make_byte_map(&map, a.wq, (uint64_t)a.K, (uint64_t)a.E * a.N, 128)) return cudaErrorInvalidValue;
+    if (!map_weights(&map, a.wq, (uint64_t)a.K, (uint64_t)a.E * a.N)) return cudaErrorInvalidValue;
     if (out == MOE_F32) return launch_o<float>(a, map, s);
     if (out == MOE_BF16) return launch_o<__nv_bfloat16>(a, map, s);
     return launch_o<__half>(a, map, s);
