@@ -87,9 +87,10 @@ __device__ __forceinline__ uint32_t top_bits(const Chunk<A, C>& c, uint32_t top)
 
 // One block a row.  kKeep chunks of C values a thread stay in registers between
 // the maximum and the codes; kKeep = 0: rows of any length, read (and gated)
-// twice.
+// twice.  x is not __restrict__: the kernel in front may still write it when this one
+// starts (sorted_rows.cu).
 template <typename A, int C, bool kGated, int kKeep>
-__global__ void __launch_bounds__(256, kGated ? 4 : 6) k_quantize_rows(const A* __restrict__ x, long long xs, int K,
+__global__ void __launch_bounds__(256, kGated ? 4 : 6) k_quantize_rows(const A* x, long long xs, int K,
                                                        int8_t* __restrict__ q, long long qs,
                                                        float* __restrict__ scale) {
     pdl_launch_dependents();

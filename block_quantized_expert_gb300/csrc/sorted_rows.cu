@@ -8,6 +8,11 @@
 // rows are joined without atomics in a fixed order (combine), and one pass
 // over y gives both dy and dw (combine_backward).  A position outside [0, R)
 // counts as an empty slot.  All of it is bound by HBM; offsets are 64 bits.
+//
+// No input is `const __restrict__`: a kernel starts while the one in front of it
+// may still be writing that input, and the qualifier would promise data that stays
+// as it is for the whole kernel, which allows loads before the wait or by the
+// read-only path.  The outputs keep __restrict__, so loads still pass stores.
 #include <climits>
 #include <cmath>
 #include <cstdarg>
@@ -57,9 +62,9 @@ __device__ __forceinline__ void find_slots(Slots& s, const int32_t* row_dst, con
 // word a thread.  Reads T H, writes R H elements; at T = 8192, k = 6, H = 4096,
 // bf16: 71.7 us, 6.6 TB/s (four words a thread: 73.6).
 template <typename V>
-__global__ void __launch_bounds__(128) k_dispatch(const char* __restrict__ x, long long x_pitch, int T, int k,
-                                                  int words, const int32_t* __restrict__ placed,
-                                                  const int32_t* __restrict__ row_dst, char* __restrict__ xs,
+__global__ void __launch_bounds__(128) k_dispatch(const char* x, long long x_pitch, int T, int k,
+                                                  int words, const int32_t* placed,
+                                                  const int32_t* row_dst, char* __restrict__ xs,
                                                   long long xs_pitch) {
     pdl_launch_dependents();
     pdl_wait();
@@ -91,9 +96,9 @@ __global__ void __launch_bounds__(128) k_dispatch(const char* __restrict__ x, lo
 // registers leave fewer blocks on an SM).  With one chunk a thread instead of four
 // those 88 and 79 were 115 and 101: a block waits for its token's positions first.
 template <typename A, typename O, int C, int U>
-__global__ void __launch_bounds__(128) k_combine_rows(const A* __restrict__ y, long long ys,
-                                                      const float* __restrict__ w, int T, int k, int H,
-                                                      const int32_t* __restrict__ row_dst, O* __restrict__ out,
+__global__ void __launch_bounds__(128) k_combine_rows(const A* y, long long ys,
+                                                      const float* w, int T, int k, int H,
+                                                      const int32_t* row_dst, O* __restrict__ out,
                                                       long long os) {
     pdl_launch_dependents();
     pdl_wait();
@@ -142,30 +147,31 @@ __global__ void __launch_bounds__(128) k_combine_rows(const A* __restrict__ y, l
 // (0 for an empty slot).  kGroup warps a slot walk its row of y once, U chunks on
 // their way at a time; the slots of a token stand next to each other, so that
 // dout[t] comes from L1 but once.  The dot product is a fp32 sum a lane, joined
-// by shuffles, then in warp order.  T = 8192, k = 6, H = 4096, bf16, with the
-// router's gradient: 133 us, 6.6 TB/s (one block a token with the k rows of a chunk
-// in flight: 154 to 270).
+// by shuffles, then in warp order.  T = 8192, k = 6, H = 4096, bf16: 131 us, with the
+// router's gradient 136, 6.5 TB/s (one block a token with the k rows of a chunk in
+// flight: 154 to 270).
 template <typename A, typename O, int C, int U, int kGroup>
-__global__ void __launch_bounds__(256) k_combine_backward(const O* __restrict__ dout, long long ds,
-                                                          const A* __restrict__ y, long long ys,
-                                                          const float* __restrict__ w, int T, int k, int H,
-                                                          const int32_t* __restrict__ placed,
-                                                          const int32_t* __restrict__ row_dst, A* __restrict__ dy,
+__global__ void __launch_bounds__(kGroup == 8 ? 256 : 128) k_combine_backward(const O* dout, long long ds,
+                                                          const A* y, long long ys,
+                                                          const float* w, int T, int k, int H,
+                                                          const int32_t* placed,
+                                                          const int32_t* row_dst, A* __restrict__ dy,
                                                           long long dys, float* __restrict__ dw) {
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ float part[8];
+    constexpr int kWarps = kGroup == 8 ? 8 : 4;  // of a block
+    __shared__ float part[kWarps];
     constexpr int kStep = 32 * kGroup * C;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int first = (threadIdx.x % (32 * kGroup)) * C;
     const int R = T * k;
-    const long long r = (long long)blockIdx.x * (8 / kGroup) + warp / kGroup;  // slot
+    const long long r = (long long)blockIdx.x * (kWarps / kGroup) + warp / kGroup;  // slot
     const int p = r < R ? row_dst[r] : -1;
     const bool on = p >= 0 && p < R;
     float dot = 0.f;
     if (on) {
         const float wt = w[r];
-        const O* drow = dout + r / k * ds;
+        const O* drow = dout + (long long)((int)r / k) * ds;
         const A* yrow = y + p * ys;
         A* grow = dy + p * dys;
         for (int c0 = first; c0 < H; c0 += U * kStep) {
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__(256) k_combine_backward(const O* __restrict__ 
     float zero[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) zero[i] = 0.f;
-    for (long long q = max(*placed, 0) + r; q < R; q += (long long)gridDim.x * (8 / kGroup))
+    for (long long q = max(*placed, 0) + r; q < R; q += (long long)gridDim.x * (kWarps / kGroup))
         for (int c = first; c < H; c += kStep) store_chunk<A, C>(dy + q * dys + c, zero);
 }
 
@@ -212,9 +218,9 @@ __global__ void __launch_bounds__(256) k_combine_backward(const O* __restrict__ 
 // the differences taken first, so that one kept slot gives exactly 0.  Below
 // l = -17, sigmoid(l) / (2 s) is exp(l / 2) / 2 to less than fp32's rounding.
 // One warp a token: the row of zeros, then the k gradients into it.
-__global__ void __launch_bounds__(128) k_route_backward(const float* __restrict__ logits,
-                                                        const int32_t* __restrict__ ids,
-                                                        const float* __restrict__ dw, int T, int E, int k,
+__global__ void __launch_bounds__(128) k_route_backward(const float* logits,
+                                                        const int32_t* ids,
+                                                        const float* dw, int T, int E, int k,
                                                         float w_scale, float* __restrict__ dlogits) {
     pdl_launch_dependents();
     pdl_wait();
@@ -350,16 +356,17 @@ struct CombineBackwardLaunch {
     const int32_t *placed, *row_dst; void* dy; long long dys; float* dw; cudaStream_t s;
     template <typename A, typename O, int C, int U>
     cudaError_t operator()() const {
-        // a whole block a slot where there are slots too few to fill the GPU with half blocks
-        // (150 SMs of 16); with two slots a block and one chunk in flight a thread the long
-        // batch takes 133 us, with a warp a slot 142, with two chunks 162, with four 209
+        // eight warps a slot where there are slots too few to fill the GPU with fewer (150 SMs
+        // of 16 slots); with two warps and one chunk in flight a thread the long batch takes
+        // 131 us, with one or four 136 (two in blocks of 256: 132), with fewer warps on an SM
+        // 165 and more
         const long long R = (long long)T * k;
-        return R < 2400 ? launch<A, O, C, 2 * U, 8>((unsigned)R) : launch<A, O, C, U, 4>((unsigned)((R + 1) / 2));
+        return R < 2400 ? launch<A, O, C, 2 * U, 8>((unsigned)R) : launch<A, O, C, U, 2>((unsigned)((R + 1) / 2));
     }
     template <typename A, typename O, int C, int U, int kGroup>
     cudaError_t launch(unsigned blocks) const {
-        return launch_pdl(k_combine_backward<A, O, C, U, kGroup>, dim3(blocks), dim3(256), 0, s, (const O*)dout, ds,
-                          (const A*)y, ys, w, T, k, H, placed, row_dst, (A*)dy, dys, dw);
+        return launch_pdl(k_combine_backward<A, O, C, U, kGroup>, dim3(blocks), dim3(kGroup == 8 ? 256 : 128), 0, s,
+                          (const O*)dout, ds, (const A*)y, ys, w, T, k, H, placed, row_dst, (A*)dy, dys, dw);
     }
 };
 
