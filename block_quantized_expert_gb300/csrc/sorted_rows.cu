@@ -215,8 +215,13 @@ __global__ void __launch_bounds__(kGroup == 8 ? 256 : 128) k_combine_backward(co
 // ---------------------------------------------------------- route_backward --
 // w_j = w_scale s_j / S, S = sum of s over the kept slots, s = sqrt(softplus(l)):
 //   dl_j = (w_scale / S^2) sum_i s_i (dw_j - dw_i) * sigmoid(l_j) / (2 s_j),
-// the differences taken first, so that one kept slot gives exactly 0.  Below
-// l = -17, sigmoid(l) / (2 s) is exp(l / 2) / 2 to less than fp32's rounding.
+// the differences taken first, so that one kept slot gives exactly 0.  S may be as
+// small as 1e-38 and S^2 is then 0 in fp32, so the shares p_i = s_i / S stand for
+// s_i and the slope is divided by S once: all factors stay near 1.
+//   dl_j = w_scale sum_i p_i (dw_j - dw_i) * sigmoid(l_j) / (2 s_j S)
+// Below l = -17, s is exp(l / 2) and sigmoid(l) / (2 s) half of that, to less than
+// fp32's rounding (its square, exp(l), is subnormal below -87).  Below -174 exp(l / 2)
+// itself is, and s counts as 0.
 // One warp a token: the row of zeros, then the k gradients into it.
 __global__ void __launch_bounds__(128) k_route_backward(const float* logits,
                                                         const int32_t* ids,
@@ -232,20 +237,16 @@ __global__ void __launch_bounds__(128) k_route_backward(const float* logits,
         const bool kept = id >= 0 && id < E;
         const float l = kept ? logits[t * E + id] : 0.f;
         const float g = kept ? dw[t * k + lane] : 0.f;
-        const float s = kept ? sqrt_softplus(l) : 0.f;
+        const float s = !kept || l < -174.f ? 0.f : l < -17.f ? expf(0.5f * l) : sqrt_softplus(l);
         float total = 0.f, against = 0.f;
+        for (int i = 0; i < k; ++i) total += __shfl_sync(kAll, s, i);
+        const float p = total != 0.f ? s / total : 0.f;  // (NaN stays NaN)
         for (int i = 0; i < k; ++i) {
-            const float si = __shfl_sync(kAll, s, i), gi = __shfl_sync(kAll, g, i);
-            if (__shfl_sync(kAll, (int)kept, i)) {
-                total += si;
-                against += si * (g - gi);
-            }
+            const float pi = __shfl_sync(kAll, p, i), gi = __shfl_sync(kAll, g, i);
+            if (__shfl_sync(kAll, (int)kept, i)) against += pi * (g - gi);
         }
         float d = 0.f;
-        if (kept && total > 0.f) {
-            const float slope = l < -17.f ? 0.5f * expf(0.5f * l) : 1.f / (1.f + expf(-l)) / (2.f * s);
-            d = w_scale / total / total * against * slope;
-        }
+        if (kept && s != 0.f) d = w_scale * against * (l < -17.f ? 0.5f * p : 1.f / (1.f + expf(-l)) / (2.f * s) / total);
         // an id that stands twice: its first slot writes the sum
         float sum = 0.f;
         bool before = false;

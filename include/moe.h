@@ -417,9 +417,11 @@ moe_status moe_combine_backward(const void* dout, moe_dtype dout_dtype, long lon
  *   w_j = w_scale * s_j / S,
  *   dlogits[t][ids_j] = (w_scale / S^2) * sum_i s_i (dw_j - dw_i)
  *                       * sigmoid(logit_j) / (2 s_j), all others 0.
- * The selection itself has no gradient.  Slots whose id is outside
- * [0, n_experts) are not kept; with tail pruning this is the gradient of
- * the linear rescaling (rho = 1), whose kept weights sum to w_scale.
+ * The selection itself has no gradient.  One kept expert's is exactly 0.  A
+ * logit below -174, where s leaves fp32's normal numbers, counts as s = 0.
+ * Slots whose id is outside [0, n_experts) are not kept; with tail pruning
+ * this is the gradient of the linear rescaling (rho = 1), whose kept weights
+ * sum to w_scale.
  *   logits device f32 [T][n_experts]; ids device i32 [T][top_k]; dw device
  *   f32 [T][top_k]; dlogits device f32 [T][n_experts], overwritten.       */
 moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* dw, int T,
