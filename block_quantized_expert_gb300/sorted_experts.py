@@ -120,8 +120,9 @@ class _RouterWeights(torch.autograd.Function):
     def forward(ctx, logits, ids, w_scale):
         ctx.save_for_backward(logits, ids)
         ctx.w_scale = w_scale
-        kept = ids >= 0
-        s = torch.nn.functional.softplus(logits.gather(1, ids.long().clamp(min=0)), threshold=1e9).sqrt() * kept
+        kept = (ids >= 0) & (ids < logits.shape[1])  # the others are empty slots, whose logits are not read
+        l = logits.gather(1, torch.where(kept, ids, 0).long())
+        s = torch.where(kept, torch.nn.functional.softplus(l, threshold=1e9).sqrt(), 0.0)
         return w_scale * s / s.sum(1, keepdim=True).clamp(min=1e-30)
 
     @staticmethod
@@ -143,7 +144,8 @@ def combine(y: torch.Tensor, w: torch.Tensor, s: Sorted) -> torch.Tensor:
 
 
 def router_weights(logits: torch.Tensor, ids: torch.Tensor, w_scale: float = W_SCALE) -> torch.Tensor:
-    """The weights of moe_route for given ids; differentiable in the logits."""
+    """The weights of moe_route for given ids; differentiable in the logits.  Ids
+    outside [0, E) are empty slots with weight 0."""
     return _RouterWeights.apply(logits, ids, w_scale)
 
 
