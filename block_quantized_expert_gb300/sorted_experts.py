@@ -122,8 +122,11 @@ class _RouterWeights(torch.autograd.Function):
         ctx.w_scale = w_scale
         kept = (ids >= 0) & (ids < logits.shape[1])  # the others are empty slots, whose logits are not read
         l = logits.gather(1, torch.where(kept, ids, 0).long())
-        s = torch.where(kept, torch.nn.functional.softplus(l, threshold=1e9).sqrt(), 0.0)
-        return w_scale * s / s.sum(1, keepdim=True).clamp(min=1e-30)
+        # as in moe_route_backward: below -17 s is exp(l / 2) to fp32's rounding, and 0 below -174
+        s = torch.where(l < -17.0, torch.exp(0.5 * l), (l.clamp(min=0) + torch.log1p(torch.exp(-l.abs()))).sqrt())
+        s = torch.where(kept & ~(l < -174.0), s, 0.0)
+        total = s.sum(1, keepdim=True)
+        return w_scale * (s / torch.where(total == 0, 1.0, total))
 
     @staticmethod
     def backward(ctx, dw):
@@ -145,7 +148,9 @@ def combine(y: torch.Tensor, w: torch.Tensor, s: Sorted) -> torch.Tensor:
 
 def router_weights(logits: torch.Tensor, ids: torch.Tensor, w_scale: float = W_SCALE) -> torch.Tensor:
     """The weights of moe_route for given ids; differentiable in the logits.  Ids
-    outside [0, E) are empty slots with weight 0."""
+    outside [0, E) are empty slots with weight 0.  A logit below -174 counts as
+    weight 0.  (moe_route itself takes exp(l), which loses bits below l = -87 and
+    is 0 below -104.)"""
     return _RouterWeights.apply(logits, ids, w_scale)
 
 

@@ -23,3 +23,16 @@ def test_slots_that_are_not_kept_are_not_read(device):
     want = S.route_weights64(l, np.where(kept, ids.cpu().numpy(), -1))
     # two transcendentals of 2 units, a root, k sums, a product and a quotient
     assert np.all(np.abs(w - want) <= 16 * EPS * want)
+
+
+@pytest.mark.parametrize("device", ["cpu", pytest.param("cuda", marks=pytest.mark.gpu)])
+@pytest.mark.parametrize("base", [3e38, 1000.0, 300.0, 89.0, 88.0, 20.0, 0.0, -17.0, -60.0, -88.0, -95.0, -103.0, -110.0, -170.0])
+def test_weights_over_the_range_of_logits(base, device):
+    """The same bound wherever s = sqrt(softplus(logit)) is a normal number: a
+    logit's half is exact, so exp(l / 2) has no more than its own two units."""
+    T, k, E = 6, 4, 5
+    logits = (np.float32(base) + np.random.default_rng(1).uniform(-2, 2, (T, E))).astype(np.float32)
+    ids = np.tile(np.arange(k, dtype=np.int32), (T, 1))
+    w = se.router_weights(torch.from_numpy(logits).to(device), torch.from_numpy(ids).to(device)).cpu().numpy()
+    want = S.route_weights64(logits.astype(np.float64), ids)
+    assert np.all(np.abs(w - want) <= 16 * EPS * want), (w, want)
