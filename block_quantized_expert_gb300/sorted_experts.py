@@ -147,11 +147,20 @@ def combine(y: torch.Tensor, w: torch.Tensor, s: Sorted) -> torch.Tensor:
 
 
 def router_weights(logits: torch.Tensor, ids: torch.Tensor, w_scale: float = W_SCALE) -> torch.Tensor:
-    """The weights of moe_route for given ids; differentiable in the logits.  Ids
-    outside [0, E) are empty slots with weight 0.  A logit below -174 counts as
+    """The weights [T][k] of moe_route, in fp32, for logits [T][E] of any floating type
+    and whole-number ids [T][k]; differentiable in the logits.  Ids outside [0, E)
+    are empty slots with weight 0.  A logit below -174 counts as
     weight 0.  (moe_route itself takes exp(l), which loses bits below l = -87 and
     is 0 below -104.)"""
-    return _RouterWeights.apply(logits, ids, w_scale)
+    if logits.dim() != 2 or not logits.is_floating_point():
+        raise ValueError(f"logits must be a 2-D floating tensor, got {logits.dtype} {tuple(logits.shape)}")
+    if ids.dim() != 2 or ids.shape[0] != logits.shape[0] or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64 of shape ({logits.shape[0]}, top_k), got {ids.dtype} {tuple(ids.shape)}")
+    if not 1 <= ids.shape[1] <= min(8, logits.shape[1]):
+        raise ValueError(f"top_k must be in [1, 8] and at most the number of experts, got {ids.shape[1]}")
+    if ids.dtype == torch.int64:  # an id past 32 bits is an empty slot, not what its low bits say
+        ids = torch.where((ids >= 0) & (ids < logits.shape[1]), ids, -1).int()
+    return _RouterWeights.apply(logits.float().contiguous(), ids.contiguous(), w_scale)
 
 
 def _example() -> None:

@@ -36,3 +36,39 @@ def test_weights_over_the_range_of_logits(base, device):
     w = se.router_weights(torch.from_numpy(logits).to(device), torch.from_numpy(ids).to(device)).cpu().numpy()
     want = S.route_weights64(logits.astype(np.float64), ids)
     assert np.all(np.abs(w - want) <= 16 * EPS * want), (w, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16, torch.float64])
+@pytest.mark.parametrize("id_dtype", [torch.int32, torch.int64])
+def test_the_gradient_takes_what_the_forward_takes(dtype, id_dtype):
+    """Ids as topk returns them, logits of other types and orders: the gradient is
+    that of contiguous fp32 logits, in the type of the logits."""
+    T, k, E = 7, 3, 9
+    base = torch.randn(E, T, generator=torch.Generator("cuda").manual_seed(2), device="cuda").to(dtype)
+    logits = base.t().requires_grad_()
+    ids = logits.detach().topk(k, dim=1).indices.to(id_dtype)
+    up = torch.randn(k, T, device="cuda").t()
+    w = se.router_weights(logits, ids)
+    assert w.dtype == torch.float32
+    (got,) = torch.autograd.grad(w, logits, up)
+    plain = base.t().float().contiguous().requires_grad_()
+    (want,) = torch.autograd.grad(se.router_weights(plain, ids.int().contiguous()), plain, up.contiguous())
+    assert got.dtype == dtype and torch.equal(got, want.to(dtype))
+
+
+def test_ids_must_be_whole_numbers():
+    with pytest.raises(ValueError, match="ids"):
+        se.router_weights(torch.zeros(2, 4), torch.zeros(2, 2))
+    with pytest.raises(ValueError, match="logits"):
+        se.router_weights(torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, 2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="ids"):
+        se.router_weights(torch.zeros(2, 4), torch.zeros(3, 2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="top_k"):
+        se.router_weights(torch.zeros(2, 16), torch.zeros(2, 9, dtype=torch.int32))
+
+
+def test_64_bit_ids_do_not_wrap():
+    """2^32 + 1 is no expert."""
+    w = se.router_weights(torch.zeros(1, 4), torch.tensor([[2, 2 ** 32 + 1, -2 ** 32]]))
+    assert w.tolist() == [[1.5, 0.0, 0.0]]
