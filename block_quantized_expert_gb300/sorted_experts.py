@@ -11,7 +11,8 @@ hold:
   up in one, each sorted position gathering its token), moe_quantize_rows with the
   gate, moe_expert_product (down), moe_combine.
 * dispatch, combine and router_weights: differentiable forms of moe_dispatch,
-  moe_combine and the router's weights, for products that run in between.
+  moe_combine and the router's weights, for products that run in between.  They
+  are differentiable once: a gradient of their gradient raises.
 
     python -m block_quantized_expert_gb300.sorted_experts
 
@@ -22,6 +23,7 @@ from __future__ import annotations
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 import block_quantized_expert_gb300 as bqe
 
@@ -92,6 +94,7 @@ class _Dispatch(torch.autograd.Function):
         return xs
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dxs):
         (row_dst,) = ctx.saved_tensors
         dx = torch.empty((ctx.T, dxs.shape[1]), dtype=dxs.dtype, device=dxs.device)
@@ -108,6 +111,7 @@ class _Combine(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         y, w, offsets, row_dst = ctx.saved_tensors
         dy, dw = torch.empty_like(y), torch.empty_like(w)
@@ -129,6 +133,7 @@ class _RouterWeights(torch.autograd.Function):
         return w_scale * (s / torch.where(total == 0, 1.0, total))
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dw):
         logits, ids = ctx.saved_tensors
         dlogits = torch.empty_like(logits)
