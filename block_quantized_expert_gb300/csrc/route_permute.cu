@@ -2,6 +2,11 @@
 // learned and hash routing, the token -> expert counting sort, MXFP8
 // quantisation of activations (scattered into the permuted row space), the
 // fixed-order combine, and the one-time block-scale repack of the weights.
+//
+// What a kernel in front may still write when one of these starts (ids, positions,
+// rows) is not `const __restrict__`, which would promise data that stays as it is for
+// the whole kernel.  The router's logits come from outside of this library, whose
+// kernels alone let the next one start early.
 #include <climits>
 #include <cmath>
 
@@ -39,7 +44,7 @@ cudaError_t launch_route(moe_layer* L, const float* logits, int T, int32_t* ids,
 
 // Hash-routed layers (guide, section 1: tid2eid maps a token id to its k
 // experts; flat weights w_scale / k).
-__global__ void k_route_hash(const int32_t* __restrict__ tok, const int32_t* __restrict__ tab,
+__global__ void k_route_hash(const int32_t* tok, const int32_t* tab,
                              int V, int T, int k, int E, float w_each, int32_t* __restrict__ ids,
                              float* __restrict__ w, uint32_t* err) {
     pdl_launch_dependents();
@@ -101,7 +106,7 @@ __device__ Int4Scan block_exclusive_scan4(Int4Scan v, Int4Scan* warp_tot, Int4Sc
 // earlier chunks) + rows of e in earlier warps of this chunk (per-warp counts
 // wc) + in earlier lanes (match_any); cursor then advances by this chunk's
 // counts.  Rows without a valid expert get row_dst = row_pos = -1.
-__device__ void place_chunk(const int32_t* __restrict__ ids, int R, int E, int base, int* cursor,
+__device__ void place_chunk(const int32_t* ids, int R, int E, int base, int* cursor,
                             const int* s_off, const int* s_poff, uint8_t* wc, int32_t* __restrict__ row_src,
                             int32_t* __restrict__ row_dst, int32_t* __restrict__ row_pos,
                             int32_t* __restrict__ pos_row) {
@@ -157,7 +162,7 @@ __device__ void place_chunk(const int32_t* __restrict__ ids, int R, int E, int b
 // Besides the ABI outputs it fills the padded bookkeeping of the GEMMs:
 // every expert segment starts at a multiple of 128 rows.
 __device__ void permute_body(
-    const int32_t* __restrict__ ids, int R, int E, int32_t* __restrict__ offsets,
+    const int32_t* ids, int R, int E, int32_t* __restrict__ offsets,
     int32_t* __restrict__ row_src, int32_t* __restrict__ row_dst, int32_t* __restrict__ counts,
     int32_t* __restrict__ poff, int32_t* __restrict__ tile_scan, int32_t* __restrict__ chunk_scan,
     int32_t* __restrict__ row_pos, int32_t* __restrict__ pos_row, int32_t* __restrict__ sh_desc,
@@ -225,7 +230,7 @@ __device__ void permute_body(
 }
 
 __global__ void __launch_bounds__(1024) k_permute(
-    const int32_t* __restrict__ ids, int R, int E, int32_t* __restrict__ offsets,
+    const int32_t* ids, int R, int E, int32_t* __restrict__ offsets,
     int32_t* __restrict__ row_src, int32_t* __restrict__ row_dst, int32_t* __restrict__ counts,
     int32_t* __restrict__ poff, int32_t* __restrict__ tile_scan, int32_t* __restrict__ chunk_scan,
     int32_t* __restrict__ row_pos, int32_t* __restrict__ pos_row, int32_t* __restrict__ sh_desc,
@@ -237,8 +242,8 @@ __global__ void __launch_bounds__(1024) k_permute(
                  pos_row, sh_desc, T, err, zero, n_zero, dyn);
 }
 
-__global__ void k_perm_count(const int32_t* __restrict__ ids, int R, int E, int32_t* __restrict__ chunk_cnt);
-__global__ void k_perm_place(const int32_t* __restrict__ ids, int R, int E, const int32_t* __restrict__ chunk_cnt,
+__global__ void k_perm_count(const int32_t* ids, int R, int E, int32_t* __restrict__ chunk_cnt);
+__global__ void k_perm_place(const int32_t* ids, int R, int E, const int32_t* chunk_cnt,
                              int32_t* __restrict__ offsets, int32_t* __restrict__ row_src,
                              int32_t* __restrict__ row_dst, int32_t* __restrict__ counts,
                              int32_t* __restrict__ poff, int32_t* __restrict__ tile_scan,
@@ -288,7 +293,7 @@ cudaError_t launch_permute_raw(const int32_t* ids, int T, int k, int E, int32_t*
 // kernels: the chunks' expert counts, then every CTA scans them (its chunk's
 // rows of expert e start after the rows of e in earlier chunks) and places
 // its own rows with place_chunk.  The result is the one-CTA sort's.
-__global__ void __launch_bounds__(1024) k_perm_count(const int32_t* __restrict__ ids, int R, int E,
+__global__ void __launch_bounds__(1024) k_perm_count(const int32_t* ids, int R, int E,
                                                       int32_t* __restrict__ chunk_cnt) {
     extern __shared__ int sc[];  // [E]
     pdl_launch_dependents();
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(1024) k_perm_count(const int32_t* __restrict__
 }
 
 __global__ void __launch_bounds__(1024) k_perm_place(
-    const int32_t* __restrict__ ids, int R, int E, const int32_t* __restrict__ chunk_cnt,
+    const int32_t* ids, int R, int E, const int32_t* chunk_cnt,
     int32_t* __restrict__ offsets, int32_t* __restrict__ row_src, int32_t* __restrict__ row_dst,
     int32_t* __restrict__ counts, int32_t* __restrict__ poff, int32_t* __restrict__ tile_scan,
     int32_t* __restrict__ chunk_scan, int32_t* __restrict__ row_pos, int32_t* __restrict__ pos_row,
@@ -418,7 +423,7 @@ __device__ __forceinline__ QTask q_task(int H, int task, int lane) {
     return q;
 }
 
-__device__ __forceinline__ uint4 q_load(const uint16_t* __restrict__ x, int H, const QTask& q) {
+__device__ __forceinline__ uint4 q_load(const uint16_t* x, int H, const QTask& q) {
     return q.active ? *reinterpret_cast<const uint4*>(x + (size_t)q.t * H + q.h) : make_uint4(0, 0, 0, 0);
 }
 
@@ -470,14 +475,14 @@ __device__ __forceinline__ void q_store(int H, const QuantDst& d, const QTask& q
 }
 
 template <int kMode>
-__device__ __forceinline__ void quantize_task(const uint16_t* __restrict__ x, int H, const QuantDst& d,
+__device__ __forceinline__ void quantize_task(const uint16_t* x, int H, const QuantDst& d,
                                               int task, int lane) {
     const QTask q = q_task(H, task, lane);
     q_store<kMode>(H, d, q, q_load(x, H, q), lane);
 }
 
 template <int kMode>
-__global__ void __launch_bounds__(256) k_quantize(const uint16_t* __restrict__ x, int T, int H,
+__global__ void __launch_bounds__(256) k_quantize(const uint16_t* x, int T, int H,
                                                   QuantDst d) {
     pdl_launch_dependents();
     pdl_wait();
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(256) k_quantize(const uint16_t* __restrict__ x
 __global__ void __launch_bounds__(1024) k_front(
     const float* __restrict__ logits, float w_scale, RoutePrune prune, int32_t* __restrict__ ids,
     float* __restrict__ wts,
-    const uint16_t* __restrict__ x, int T, int k, int E, int H, QuantDst qd, int32_t* __restrict__ offsets,
+    const uint16_t* x, int T, int k, int E, int H, QuantDst qd, int32_t* __restrict__ offsets,
     int32_t* __restrict__ row_src, int32_t* __restrict__ row_dst, int32_t* __restrict__ counts,
     int32_t* __restrict__ poff, int32_t* __restrict__ tile_scan, int32_t* __restrict__ chunk_scan,
     int32_t* __restrict__ row_pos, int32_t* __restrict__ pos_row, int32_t* __restrict__ sh_desc,
@@ -609,11 +614,11 @@ cudaError_t launch_quantize_scatter(moe_layer* L, const uint16_t* x, int T, cuda
 // 128 kCmbQ features, so H must be a multiple of that): the token's ids, row
 // positions and weights are read once for them all.
 template <int kCmbQ>
-__global__ void __launch_bounds__(256) k_combine(const int32_t* __restrict__ ids,
-                                                 const float* __restrict__ w,
-                                                 const int32_t* __restrict__ row_pos,
-                                                 const float* __restrict__ y,
-                                                 const float* __restrict__ y_sh, int T, int H,
+__global__ void __launch_bounds__(256) k_combine(const int32_t* ids,
+                                                 const float* w,
+                                                 const int32_t* row_pos,
+                                                 const float* y,
+                                                 const float* y_sh, int T, int H,
                                                  int k, float* __restrict__ out) {
     pdl_launch_dependents();
     pdl_wait();
@@ -690,8 +695,8 @@ cudaError_t launch_combine(moe_layer* L, const int32_t* ids, const float* w, int
 }
 
 // ----------------------------------------------------------- test helpers --
-__global__ void k_hidden_gather(const int32_t* __restrict__ row_pos, const uint8_t* __restrict__ hq,
-                                const uint8_t* __restrict__ hs, int R, int I, uint8_t* __restrict__ oq,
+__global__ void k_hidden_gather(const int32_t* row_pos, const uint8_t* hq,
+                                const uint8_t* hs, int R, int I, uint8_t* __restrict__ oq,
                                 uint8_t* __restrict__ os) {
     pdl_launch_dependents();
     pdl_wait();

@@ -115,3 +115,35 @@ def test_sort_then_dispatch_and_product(T, k, E, H):
         done()
 
     compare(step, lambda: [torch.empty(N, R, H, device="cuda"), torch.empty(N, R, 64, device="cuda")])
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 300, 5000])
+def test_the_layer_step_by_step(tokens):
+    """Route, sort, quantisation and layer over the same ids, weights and positions;
+    the layer's own buffers are written again by every call."""
+    from tests import _gpu as G
+
+    cfg = G.CONFIGS[0]
+    layer = G.make_layer(cfg, G.weights_np(0), tokens)
+    R = tokens * cfg.k
+    g = torch.Generator("cuda").manual_seed(tokens)
+    logits = torch.randn(N, tokens, cfg.E, generator=g, device="cuda")
+    x = torch.randn(N, tokens, cfg.H, generator=g, device="cuda").to(BF16).view(torch.int16)
+    ids, w = torch.empty(tokens, cfg.k, dtype=torch.int32, device="cuda"), torch.empty(tokens, cfg.k, device="cuda")
+    off = torch.empty(cfg.E + 1, dtype=torch.int32, device="cuda")
+    src, dst = (torch.empty(R, dtype=torch.int32, device="cuda") for _ in range(2))
+
+    def step(i, out, done):
+        bqe.moe_route(layer, logits[i], ids, w)
+        done()
+        bqe.moe_permute(layer, ids, off, src, dst)
+        done()
+        bqe.moe_dispatch(x[i].view(BF16), off, dst, out[0])
+        done()
+        bqe.moe_forward(layer, x[i], ids, w, out[1])
+        done()
+
+    compare(step, lambda: [torch.empty(N, R, cfg.H, dtype=BF16, device="cuda"),
+                           torch.empty(N, tokens, cfg.H, device="cuda")])
+    bqe.moe_check(layer)
+    layer.close()
