@@ -29,7 +29,8 @@ EXPORTS = ("moe_create", "moe_destroy", "moe_route", "moe_route_hash", "moe_perm
            "moe_set_route_prune", "moe_set_wait_limit", "moe_test_stall_next_decode", "moe_test_decode_split",
            "moe_set_decode_kernel", "moe_decode_info", "moe_dispatch", "moe_dispatch_backward",
            "moe_combine", "moe_combine_backward", "moe_route_backward", "moe_quantize_rows",
-           "moe_expert_product", "moe_check_product", "moe_test_stall_next_product")
+           "moe_expert_product", "moe_check_product", "moe_test_stall_next_product", "moe_permute_scratch",
+           "moe_permute_scratch_bytes")
 
 
 class MoeError(RuntimeError):
@@ -85,6 +86,8 @@ def load_library(build: bool = True) -> C.CDLL:
         "moe_set_stage_events": ([vp, C.POINTER(vp), i], i),
         "moe_kernel_launches": ([vp], C.c_ulonglong),
         "moe_permute_noalloc": ([vp, i, i, i, vp, vp, vp, vp], i),
+        "moe_permute_scratch": ([vp, i, i, i, vp, vp, vp, vp, C.c_size_t, vp], i),
+        "moe_permute_scratch_bytes": ([i, i, i], C.c_size_t),
         "moe_set_trace": ([vp, vp, C.c_size_t], i),
         "moe_route_forward": ([vp, vp, vp, i, vp, vp, vp, vp], i),
         "moe_set_route_prune": ([vp, i, f, f], i),
@@ -337,6 +340,24 @@ def moe_permute_noalloc(ids, n_experts: int, offsets, row_src, row_dst, stream=N
         _ptr(offsets, torch.int32, (n_experts + 1,), "offsets"),
         _ptr(row_src, torch.int32, (R,), "row_src"), _ptr(row_dst, torch.int32, (R,), "row_dst"),
         _stream(stream))
+    _check(st)
+
+
+def moe_permute_scratch_bytes(T: int, top_k: int, n_experts: int) -> int:
+    """Bytes of scratch of moe_permute_scratch; 0 for sizes that it does not take."""
+    return load_library().moe_permute_scratch_bytes(T, top_k, n_experts)
+
+
+def moe_permute_scratch(ids, n_experts: int, offsets, row_src, row_dst, scratch, stream=None):
+    """The grouping of moe_permute without a layer, in the caller's scratch (a CUDA
+    uint8 tensor of moe_permute_scratch_bytes); calls share nothing."""
+    T, k = ids.shape
+    R = T * k
+    st = load_library().moe_permute_scratch(
+        _ptr(ids, torch.int32, (T, k), "ids"), T, k, n_experts,
+        _ptr(offsets, torch.int32, (n_experts + 1,), "offsets"),
+        _ptr(row_src, torch.int32, (R,), "row_src"), _ptr(row_dst, torch.int32, (R,), "row_dst"),
+        _ptr(scratch, torch.uint8, None, "scratch"), scratch.numel(), _stream(stream))
     _check(st)
 
 

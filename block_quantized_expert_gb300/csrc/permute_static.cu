@@ -11,11 +11,15 @@
 // bookkeeping (per-expert counts, padded segment starts, tile scans, the
 // padded row maps) lives in one file-scope __device__ array of fixed size
 // that every GPU loading the library keeps until the process exits.
+//
+// moe_permute_scratch is the same sort in scratch that the caller brings: calls
+// on several streams share nothing, and a call may have 2^20 rows.
 #include <cstdio>
 #include <mutex>
 
 #include "common.cuh"
 #include "layer.h"
+#include "permute.h"
 
 namespace moe {
 
@@ -92,4 +96,69 @@ extern "C" moe_status moe_permute_noalloc(const int32_t* ids, int T, int top_k, 
                            tile_scan, chunk_scan, row_pos, pos_row, (cudaStream_t)stream);
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, cudaGetErrorString(e));
     return MOE_OK;
+}
+
+namespace moe {
+namespace {
+
+constexpr int kScratchMaxRows = 1 << 20;
+
+bool scratch_sizes_ok(int T, int top_k, int n_experts) {
+    return T >= 0 && top_k >= 1 && top_k <= kMaxTopK && n_experts >= 1 && n_experts <= kMaxExperts &&
+           (long long)T * top_k <= kScratchMaxRows;
+}
+
+// counts [E] + poff, tile_scan, chunk_scan [E + 1] + row_pos [R] + pos_row [padded
+// rows] + the chunks' counts
+size_t scratch_words(int R, int E) {
+    return (size_t)E + 3 * ((size_t)E + 1) + R + ((size_t)R + (size_t)E * (kRowTile - 1)) + (size_t)perm_ctas(R) * E;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" size_t moe_permute_scratch_bytes(int T, int top_k, int n_experts) {
+    return moe::scratch_sizes_ok(T, top_k, n_experts) ? 4 * moe::scratch_words(T * top_k, n_experts) : 0;
+}
+
+extern "C" moe_status moe_permute_scratch(const int32_t* ids, int T, int top_k, int n_experts, int32_t* offsets,
+                                          int32_t* row_src, int32_t* row_dst, void* scratch, size_t scratch_bytes,
+                                          moe_stream_t stream) {
+    using namespace moe;
+    auto fail = [](moe_status st, const char* msg) {
+        char buf[200];
+        snprintf(buf, sizeof(buf), "moe_permute_scratch: %s", msg);
+        set_thread_error(buf);
+        return st;
+    };
+    if (!scratch_sizes_ok(T, top_k, n_experts))
+        return fail(MOE_ERR_INVALID_ARG,
+                    "T * top_k must be in [0, 2^20], top_k in [1, 8] and n_experts in [1, 1024]");
+    if (!offsets) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL");
+    const int R = T * top_k, E = n_experts;
+    if (R == 0) {
+        const cudaError_t e = cudaMemsetAsync(offsets, 0, ((size_t)E + 1) * 4, (cudaStream_t)stream);
+        return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, cudaGetErrorString(e));
+    }
+    if (!ids || !row_src || !row_dst || !scratch) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
+    if ((uintptr_t)scratch % 4) return fail(MOE_ERR_INVALID_ARG, "scratch is not aligned to 4 bytes");
+    if (scratch_bytes < 4 * scratch_words(R, E))
+        return fail(MOE_ERR_INVALID_ARG, "scratch is smaller than moe_permute_scratch_bytes says");
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, cudaGetErrorString(e));
+    if (dev < 0 || dev >= kMaxDevices) return fail(MOE_ERR_UNSUPPORTED, "device ordinal above 63");
+    int32_t* unused = nullptr;
+    e = setup(dev, &unused);  // the kernels' shared-memory limits
+    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, cudaGetErrorString(e));
+    int32_t* counts = static_cast<int32_t*>(scratch);
+    int32_t* poff = counts + E;
+    int32_t* tile_scan = poff + (E + 1);
+    int32_t* chunk_scan = tile_scan + (E + 1);
+    int32_t* row_pos = chunk_scan + (E + 1);
+    int32_t* pos_row = row_pos + R;
+    int32_t* perm_cnt = pos_row + ((size_t)R + (size_t)E * (kRowTile - 1));
+    e = launch_permute_rows(ids, T, top_k, E, offsets, row_src, row_dst, counts, poff, tile_scan, chunk_scan, row_pos,
+                            pos_row, perm_cnt, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, cudaGetErrorString(e));
 }

@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "layer.h"
+#include "permute.h"
 #include "route.cuh"
 
 namespace moe {
@@ -287,7 +288,24 @@ cudaError_t launch_permute_raw(const int32_t* ids, int T, int k, int E, int32_t*
     return cudaGetLastError();
 }
 
-
+// The same for any number of rows: over one CTA per 1024-row chunk where launch_permute
+// would (perm_cnt then holds their counts).
+cudaError_t launch_permute_rows(const int32_t* ids, int T, int k, int E, int32_t* offsets, int32_t* row_src,
+                                int32_t* row_dst, int32_t* counts, int32_t* poff, int32_t* tile_scan,
+                                int32_t* chunk_scan, int32_t* row_pos, int32_t* pos_row, int32_t* perm_cnt,
+                                cudaStream_t s) {
+    const int R = T * k, C = perm_ctas(R);
+    const size_t smem = (size_t)48 * E;
+    if (C == 0)
+        return launch_pdl(k_permute, dim3(1), dim3(1024), smem, s, ids, R, E, offsets, row_src, row_dst, counts, poff,
+                          tile_scan, chunk_scan, row_pos, pos_row, (int32_t*)nullptr, T, (uint32_t*)nullptr,
+                          (int32_t*)nullptr, 0);
+    cudaError_t e = launch_pdl(k_perm_count, dim3(C), dim3(1024), (size_t)4 * E, s, ids, R, E, perm_cnt);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_perm_place, dim3(C), dim3(1024), smem, s, ids, R, E, (const int32_t*)perm_cnt, offsets, row_src,
+                      row_dst, counts, poff, tile_scan, chunk_scan, row_pos, pos_row, (int32_t*)nullptr, T,
+                      (uint32_t*)nullptr, (int32_t*)nullptr, 0);
+}
 
 // The same sort over one CTA per 1024-row chunk (large batches), in two
 // kernels: the chunks' expert counts, then every CTA scans them (its chunk's

@@ -35,16 +35,18 @@ class Sorted:
     """A routing in the experts' order: what moe_permute gives, with the ids."""
     ids: torch.Tensor       # int32 [T][k], -1: empty slot
     offsets: torch.Tensor   # int32 [E + 1]
-    row_src: torch.Tensor   # int32 [T * k]
+    row_src: torch.Tensor   # int32 [T * k], unset from offsets[E] on
     row_dst: torch.Tensor   # int32 [T * k]
 
 
 def sort_tokens(ids: torch.Tensor, n_experts: int) -> Sorted:
-    """The stable sort of the (token, expert) rows (at most 65536 of them)."""
+    """The stable sort of the (token, expert) rows, at most 2^20 of them, on the
+    current stream.  Each call has its own scratch."""
     T, k = ids.shape
     new = lambda n: torch.empty(n, dtype=torch.int32, device=ids.device)  # noqa: E731
     s = Sorted(ids, new(n_experts + 1), new(T * k), new(T * k))
-    bqe.moe_permute_noalloc(ids, n_experts, s.offsets, s.row_src, s.row_dst)
+    scratch = torch.empty(bqe.moe_permute_scratch_bytes(T, k, n_experts), dtype=torch.uint8, device=ids.device)
+    bqe.moe_permute_scratch(ids, n_experts, s.offsets, s.row_src, s.row_dst, scratch)
     return s
 
 

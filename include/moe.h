@@ -351,6 +351,17 @@ moe_status moe_permute_noalloc(const int32_t* ids, int T, int top_k, int n_exper
                                int32_t* offsets, int32_t* row_src, int32_t* row_dst,
                                moe_stream_t stream);
 
+/* The same sort in scratch of the caller's: nothing is shared between calls,
+ * so they may run on several streams and threads at once, each in its own
+ * scratch.  0 <= T*top_k <= 2^20; T = 0 sets offsets to 0 and the other
+ * pointers may be NULL.  Nothing is allocated; capturable.
+ *   scratch device, 4-byte aligned, at least moe_permute_scratch_bytes (0 for
+ *   sizes out of range); it may be reused when the call's work is done.    */
+size_t moe_permute_scratch_bytes(int T, int top_k, int n_experts);
+moe_status moe_permute_scratch(const int32_t* ids, int T, int top_k, int n_experts,
+                               int32_t* offsets, int32_t* row_src, int32_t* row_dst,
+                               void* scratch, size_t scratch_bytes, moe_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Rows in the experts' order: moving tokens to their sorted positions and
  * back, the gradients of both, and the product of the sorted rows with
