@@ -357,7 +357,8 @@ def moe_permute_scratch(ids, n_experts: int, offsets, row_src, row_dst, scratch,
         _ptr(ids, torch.int32, (T, k), "ids"), T, k, n_experts,
         _ptr(offsets, torch.int32, (n_experts + 1,), "offsets"),
         _ptr(row_src, torch.int32, (R,), "row_src"), _ptr(row_dst, torch.int32, (R,), "row_dst"),
-        _ptr(scratch, torch.uint8, None, "scratch"), scratch.numel(), _stream(stream))
+        _ptr(scratch, torch.uint8, None, "scratch"), scratch.numel(),
+        _here(stream, ids, offsets, row_src, row_dst, scratch))
     _check(st)
 
 
@@ -441,10 +442,18 @@ def moe_last_error(layer: Optional[Layer] = None) -> str:
     return m.decode() if m else ""
 
 
-def _here(stream) -> int:
-    """_stream for calls that hold a CUDA tensor, so that PyTorch's CUDA is up."""
+def _here(stream, *tensors) -> int:
+    """_stream for calls without a layer, on CUDA tensors: all of them, and the
+    stream, must belong to the current device, on which the call launches."""
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor of this call is on cuda:{t.get_device()}, the current device is cuda:{dev}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(dev)
+    on = getattr(getattr(stream, "device", None), "index", None)
+    if on is not None and on != dev:
+        raise ValueError(f"the stream is of cuda:{on}, the current device is cuda:{dev}")
     return _stream(stream)
 
 
@@ -470,7 +479,7 @@ def moe_dispatch(x, offsets, row_dst, xs, stream=None):
         raise ValueError("x and xs must have one floating dtype")
     lib = _lib or load_library()
     st = lib.moe_dispatch(px, dt, sx, T, k, H, _ptr(offsets, torch.int32, None, "offsets"),
-                          offsets.numel() - 1, dst, ps, ss, _here(stream))
+                          offsets.numel() - 1, dst, ps, ss, _here(stream, x, offsets, row_dst, xs))
     if st:
         _check(st)
 
@@ -486,7 +495,7 @@ def moe_dispatch_backward(dxs, row_dst, dx, stream=None):
     if dt is None or dts is None:
         raise ValueError("dxs and dx must be floating tensors")
     lib = _lib or load_library()
-    st = lib.moe_dispatch_backward(ps, dts, ss, T, k, H, dst, px, dt, sx, _here(stream))
+    st = lib.moe_dispatch_backward(ps, dts, ss, T, k, H, dst, px, dt, sx, _here(stream, dxs, row_dst, dx))
     if st:
         _check(st)
 
@@ -503,7 +512,7 @@ def moe_combine(y, w, row_dst, out, stream=None):
         raise ValueError("y and out must be floating tensors")
     lib = _lib or load_library()
     st = lib.moe_combine(py, dty, sy, _ptr(w, torch.float32, (T, k), "w"), T, k, H, dst, po, dto, so,
-                         _here(stream))
+                         _here(stream, y, w, row_dst, out))
     if st:
         _check(st)
 
@@ -523,7 +532,8 @@ def moe_combine_backward(dout, y, w, offsets, row_dst, dy, dw, stream=None):
     lib = _lib or load_library()
     st = lib.moe_combine_backward(pd, dtd, sd, py, dty, sy, _ptr(w, torch.float32, (T, k), "w"), T, k, H,
                                   _ptr(offsets, torch.int32, None, "offsets"), offsets.numel() - 1, dst, pg,
-                                  sg, _ptr(dw, torch.float32, (T, k), "dw"), _here(stream))
+                                  sg, _ptr(dw, torch.float32, (T, k), "dw"),
+                                  _here(stream, dout, y, w, offsets, row_dst, dy, dw))
     if st:
         _check(st)
 
@@ -538,7 +548,7 @@ def moe_route_backward(logits, ids, dw, dlogits, w_scale: float = 1.5, stream=No
     st = lib.moe_route_backward(_ptr(logits, torch.float32, (T, E), "logits"),
                                 _ptr(ids, torch.int32, (T, k), "ids"), _ptr(dw, torch.float32, (T, k), "dw"),
                                 T, E, k, float(w_scale), _ptr(dlogits, torch.float32, (T, E), "dlogits"),
-                                _here(stream))
+                                _here(stream, logits, ids, dw, dlogits))
     if st:
         _check(st)
 
@@ -555,7 +565,7 @@ def moe_quantize_rows(x, q, scale, gated: bool = False, stream=None):
         raise ValueError("x must be a floating tensor and q int8")
     lib = _lib or load_library()
     st = lib.moe_quantize_rows(px, dt, sx, int(bool(gated)), rows, K, pq, sq,
-                               _ptr(scale, torch.float32, (rows,), "scale"), _here(stream))
+                               _ptr(scale, torch.float32, (rows,), "scale"), _here(stream, x, q, scale))
     if st:
         _check(st)
 
@@ -582,7 +592,7 @@ def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, t
                                 _ptr(w_scale, torch.float32, (E, N), "w_scale"), E, N,
                                 None if offsets is None else _ptr(offsets, torch.int32, (E + 1,), "offsets"),
                                 None if row_src is None else _ptr(row_src, torch.int32, (R,), "row_src"),
-                                int(top_k), R, po, dto, so, _here(stream))
+                                int(top_k), R, po, dto, so, _here(stream, q, scale, wq, w_scale, out, offsets, row_src))
     if st:
         _check(st)
 
