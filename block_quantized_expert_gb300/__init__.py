@@ -13,7 +13,18 @@ import ctypes as C
 from dataclasses import dataclass
 from typing import Optional
 
-import torch
+_HAS_TORCH = True
+try:
+    import torch
+except ModuleNotFoundError as _missing:  # the library, its C entries and sizes do without
+    if _missing.name != "torch":
+        raise
+
+    class _NoTorch:
+        def __getattr__(self, name):
+            raise ModuleNotFoundError("calls on tensors need PyTorch (torch)", name="torch")
+
+    torch, _HAS_TORCH = _NoTorch(), False
 
 from . import _build
 
@@ -143,7 +154,9 @@ def _ptr(t, dtype, shape=None, name="tensor"):
 
 
 MOE_F32, MOE_BF16, MOE_F16 = range(3)
-_ROW_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.int8: None}
+_ROW_TYPES = {}
+if _HAS_TORCH:
+    _ROW_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.int8: None}
 
 
 def _rows(t, name, rows=None, width=None):
