@@ -6,6 +6,7 @@
 //
 // for the positions p of expert e's segment, r the row that position p reads.
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -159,11 +160,16 @@ __global__ void __launch_bounds__(256, kGated ? 4 : 6) k_quantize_rows(const A* 
 // ---------------------------------------------------------------- few rows --
 // Single tokens: a warp takes kChan channels of one expert for up to kFew
 // positions of its segment, lane l the bytes 16 l, 16 l + 512, ... of K; products
-// by __dp4a, exact 32-bit integer sums, joined by shuffles.  Bound by the weights,
+// by __dp4a, exact 32-bit integer sums (sum_to_f32), joined by shuffles.  Bound by the weights,
 // each read once for every kFew positions: T = 1 with six of 256 experts, K = N =
 // 4096: 19 us, 5.3 TB/s.  Block (x, p): channels 16 x .. of the segment of position p, if p
 // is the first of its kFew.
 constexpr int kFew = 4, kChan = 4;
+
+// A sum of up to 131072 products of codes in fp32.  They lie in [-2^31 + 2^24, 2^31]:
+// the least 32-bit integer is not among them, and stands for 2^31, which only K =
+// 131072 with every code -128 reaches.
+__device__ __forceinline__ float sum_to_f32(int sum) { return sum == INT_MIN ? 0x1p31f : (float)sum; }
 
 template <typename O>
 __global__ void __launch_bounds__(128) k_product_few(const Product a) {
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(128) k_product_few(const Product a) {
             if (r >= rows) break;
             const int sum = __reduce_add_sync(0xFFFFFFFFu, acc[c][r]);
             if (lane == 0)
-                reinterpret_cast<O*>(a.out)[(long long)(p + r) * a.os + n0 + c] = from_f32<O>((float)sum * s[r] * cs);
+                reinterpret_cast<O*>(a.out)[(long long)(p + r) * a.os + n0 + c] = from_f32<O>(sum_to_f32(sum) * s[r] * cs);
         }
     }
 }
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(256) k_product_any(const Product a) {
             const int n = n0 + tx + 16 * j;
             if (n < a.N)
                 reinterpret_cast<O*>(a.out)[(long long)(p0 + p) * a.os + n] =
-                    from_f32<O>((float)acc[i][j] * s * a.w_scale[(long long)e * a.N + n]);
+                    from_f32<O>(sum_to_f32(acc[i][j]) * s * a.w_scale[(long long)e * a.N + n]);
         }
     }
 }
