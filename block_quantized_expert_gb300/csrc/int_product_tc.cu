@@ -4,8 +4,9 @@
 // This part's tensor cores have no fast 8-bit integer form, but an 8-bit integer is
 // exact in fp16, a product of two is exact in fp32 and so is a sum of them up
 // to 2^24: the codes are turned into fp16 on the way to tcgen05.mma.kind::f16
-// with fp32 accumulators.  A sum passes 2^24 only for K > 1024 and codes that
-// nearly all are extreme and agree in sign; it is then rounded like any fp32 sum.
+// with fp32 accumulators.  For K up to 1024 no sum passes 2^24, at K = 16384 a mean
+// |q wq| of 1024 with signs that agree is enough.  Past it the accumulator rounds once
+// in every 16 products, in all within 2^-23 (2 + K / 16) of the sum of |q wq|.
 //
 // One CTA per SM walks tiles of 128 output channels (A, one tensor-memory lane
 // a channel) x up to kCap positions of one segment (B), K in units of 128:

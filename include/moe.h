@@ -381,8 +381,8 @@ moe_status moe_permute_scratch(const int32_t* ids, int T, int top_k, int n_exper
  *    that writes sorted rows writes zeros there.
  *  - T = 0 (or no rows) is allowed: nothing is enqueued, and pointers may be
  *    NULL.  Outputs must not overlap inputs.
- *  - Sums are held in fp32 (integer products in 32-bit integers or exactly
- *    in fp32) and rounded once, in a fixed order: equal calls give equal bits.
+ *  - Sums are held in fp32 (integer products: see moe_expert_product) and
+ *    rounded once, in a fixed order: equal calls give equal bits.
  *  - Out-of-range positions are skipped quietly; the one device flag is that
  *    of moe_check_product.                                                 */
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
@@ -461,11 +461,18 @@ moe_status moe_quantize_rows(const void* x, moe_dtype dtype, long long x_stride,
  *   row_src device i32 [R]: position p reads row r = row_src[p] / top_k (the
  *   tokens quantised once, read by each of their experts; an r outside
  *   [0, q_rows) reads as zeros); NULL: r = p.
- * The integer sum is exact while the sum of |q * wq| is at most 2^24, and
- * else accurate to fp32's rounding.  1 <= K <= 131072, 1 <= N <= 2^20,
- * R <= 2^20.  The tensor cores take K and q_stride in multiples of 16 and q
- * and wq on 16-byte boundaries; anything else runs on the CUDA cores, an
- * order of magnitude slower.                                              */
+ * Codes may be -128.  The integer sum is exact while the sum of |q * wq| is
+ * at most 2^24: for every K up to 1024, and for codes of ordinary rows (a
+ * mean |q * wq| of some 600) up to K of some 28000.  Past that it is exact on
+ * the CUDA cores, and on the tensor cores, which hold it in fp32, within
+ * 2^-23 (2 + K / 16) of the sum of |q * wq|: at worst 3e-5 of it at K = 4096
+ * and 1e-3 at K = 131072.  It is then multiplied by scale and by w_scale, in
+ * this order, in fp32, and rounded to out_dtype; sum * scale must be finite.
+ * 1 <= K <= 131072, 1 <= N <= 2^20, R <= 2^20, offsets[0] = 0.
+ * The tensor cores take K and q_stride in multiples of 16, q and wq on
+ * 16-byte boundaries and more than a few rows (R > 8, and R > 16 unless there
+ * are more rows than experts); anything else runs on the CUDA cores, with
+ * other K or alignment an order of magnitude slower.                      */
 moe_status moe_expert_product(const int8_t* q, long long q_stride, int q_rows, const float* scale, int K,
                               const int8_t* wq, const float* w_scale, int n_experts, int N,
                               const int32_t* offsets, const int32_t* row_src, int top_k, int R, void* out,
