@@ -611,7 +611,8 @@ def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, t
 
 
 def moe_check_product(stream=None):
-    """Synchronise the stream; raise MoeError if a wait of moe_expert_product ran out."""
+    """Synchronise the stream; raise MoeError if a wait of moe_expert_product ran out,
+    on any stream of the current device, since the last check on any."""
     _check(load_library().moe_check_product(_stream(stream)))
 
 

@@ -30,7 +30,8 @@ __device__ __forceinline__ int source_row(const Product& a, int p) {
 // The tensor-core form (int_product_tc.cu): K and qs multiples of 16, q and wq
 // 16-byte aligned.
 bool product_tc_fits(const Product& a);
-// Its sticky error flag (common.cuh), read after the stream's work and cleared.
+// Its sticky error flag (common.cuh), taken (read and cleared in one step) after the
+// stream's work.
 cudaError_t product_flag(uint32_t* flag, cudaStream_t s);
 cudaError_t launch_product_tc(const Product& a, moe_dtype out, cudaStream_t s);
 

@@ -241,7 +241,11 @@ struct Tile {
     int e, n0, p0, count;
 };
 
-__device__ uint32_t g_product_err;  // sticky, read by moe_check_product
+__device__ uint32_t g_product_err;   // sticky, taken by moe_check_product
+__device__ uint32_t g_product_seen;  // what the check under way has taken
+
+// Reads and clears the flag in one step: what is raised after it stays for the next.
+__global__ void k_take_flag() { g_product_seen = atomicExch(&g_product_err, 0u); }
 
 template <bool kPair, typename O>
 __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Product a, const __grid_constant__ CUtensorMap wmap) {
@@ -775,10 +779,13 @@ cudaError_t launch_o(const Product& a, const CUtensorMap& map, cudaStream_t s) {
 }  // namespace
 
 cudaError_t product_flag(uint32_t* flag, cudaStream_t s) {
-    const uint32_t zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_product_err, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_product_err, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s);
-    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
+    static std::mutex lock;  // one check at a time: they share g_product_seen
+    std::lock_guard<std::mutex> hold(lock);
+    k_take_flag<<<1, 1, 0, s>>>();
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(flag, g_product_seen, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
+    const cudaError_t done = cudaStreamSynchronize(s);
+    return e == cudaSuccess ? done : e;
 }
 
 bool product_tc_fits(const Product& a) {

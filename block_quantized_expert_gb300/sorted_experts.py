@@ -68,7 +68,10 @@ class Int8Experts:
         self.down, self.down_scale = quantize_weights(down)
 
     def __call__(self, x: torch.Tensor, s: Sorted, w: torch.Tensor) -> torch.Tensor:
-        """x [T][H] in bf16, fp16 or fp32; w [T][k] the routing weights; fp32 [T][H]."""
+        """x [T][H] in bf16, fp16 or fp32; w [T][k] the routing weights; fp32 [T][H].
+
+        Asynchronous: whether a device-side wait of the products ran out, which leaves
+        the output undefined, is what moe_check_product tells, and the caller asks it."""
         T, k = w.shape
         R, dev = T * k, x.device
         q = torch.empty((T, self.H), dtype=torch.int8, device=dev)

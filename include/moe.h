@@ -478,11 +478,15 @@ moe_status moe_expert_product(const int8_t* q, long long q_stride, int q_rows, c
                               const int32_t* offsets, const int32_t* row_src, int top_k, int R, void* out,
                               moe_dtype out_dtype, long long out_stride, moe_stream_t stream);
 
-/* Synchronise `stream` and report (then clear) the current device's sticky
- * flag of moe_expert_product: MOE_OK, or MOE_ERR_TIMEOUT if a device-side
- * wait of its tensor-core kernel ran out (2 s; that call's output is
- * undefined, later calls are not affected).  The guard moe_set_wait_limit
- * describes, for a call without a layer.                                  */
+/* Synchronise `stream` and take (report and clear in one step) the current
+ * device's sticky flag of moe_expert_product: MOE_OK, or MOE_ERR_TIMEOUT if
+ * a device-side wait of its tensor-core kernel ran out (2 s; that call's
+ * output is undefined, later calls are not affected).  There is one flag a
+ * device: MOE_ERR_TIMEOUT may be that of a product on any of its streams,
+ * and only the first check after it reports it, so all products since the
+ * last check are in doubt, and one caller checks for all of a device's
+ * streams.  The guard moe_set_wait_limit describes, for a call without a
+ * layer.  Not capturable.                                                 */
 moe_status moe_check_product(moe_stream_t stream);
 
 /* Test hook of that guard: in the next moe_expert_product that takes the
