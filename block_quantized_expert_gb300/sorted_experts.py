@@ -60,9 +60,18 @@ def quantize_weights(w: torch.Tensor):
 
 
 class Int8Experts:
-    """SwiGLU experts with 8-bit integer weights: gate and up [E][I][H], down [E][H][I]."""
+    """SwiGLU experts with 8-bit integer weights: gate and up [E][I][H], down [E][H][I].
 
-    def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor):
+    `rows` is the type of the rows between the products (gate and up, and the experts'
+    outputs before they are combined).  bf16, the default, halves their traffic against
+    fp32, and its rounding (2^-9 of a value) is below a code's half step (1/254 of a
+    row's maximum); fp32 leaves the codes as the only rounding.
+    """
+
+    def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, rows: torch.dtype = torch.bfloat16):
+        if rows not in (torch.float32, torch.bfloat16, torch.float16):
+            raise ValueError(f"rows must be float32, bfloat16 or float16, got {rows}")
+        self.rows = rows
         self.E, self.I, self.H = gate.shape
         self.gate_up, self.gate_up_scale = quantize_weights(torch.cat([gate, up], dim=1))
         self.down, self.down_scale = quantize_weights(down)
@@ -76,10 +85,10 @@ class Int8Experts:
         R, dev = T * k, x.device
         q = torch.empty((T, self.H), dtype=torch.int8, device=dev)
         scale = torch.empty(T, dtype=torch.float32, device=dev)
-        gu = torch.empty((R, 2 * self.I), dtype=torch.bfloat16, device=dev)
+        gu = torch.empty((R, 2 * self.I), dtype=self.rows, device=dev)
         h = torch.empty((R, self.I), dtype=torch.int8, device=dev)
         h_scale = torch.empty(R, dtype=torch.float32, device=dev)
-        y = torch.empty((R, self.H), dtype=torch.bfloat16, device=dev)
+        y = torch.empty((R, self.H), dtype=self.rows, device=dev)
         out = torch.empty((T, self.H), dtype=torch.float32, device=dev)
         bqe.moe_quantize_rows(x, q, scale)
         bqe.moe_expert_product(q, scale, self.gate_up, self.gate_up_scale, gu, s.offsets, s.row_src, k)
