@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(128) k_combine_rows(const A* y, long long ys,
 // (0 for an empty slot).  kGroup warps a slot walk its row of y once, U chunks on
 // their way at a time; the slots of a token stand next to each other, so that
 // dout[t] comes from L1 but once.  The dot product is a fp32 sum a lane, joined
-// by shuffles, then in warp order.  T = 8192, k = 6, H = 4096, bf16: 131 us, with the
-// router's gradient 136, 6.5 TB/s (one block a token with the k rows of a chunk in
+// by shuffles, then in warp order.  T = 8192, k = 6, H = 4096, bf16: 130 us, with the
+// router's gradient 135, 6.5 TB/s (one block a token with the k rows of a chunk in
 // flight: 154 to 270).
 template <typename A, typename O, int C, int U, int kGroup>
 __global__ void __launch_bounds__(kGroup == 8 ? 256 : 128) k_combine_backward(const O* dout, long long ds,
@@ -241,12 +241,13 @@ __global__ void __launch_bounds__(128) k_route_backward(const float* logits,
         float total = 0.f, against = 0.f;
         for (int i = 0; i < k; ++i) total += __shfl_sync(kAll, s, i);
         const float p = total != 0.f ? s / total : 0.f;  // (NaN stays NaN)
+        const unsigned on = __ballot_sync(kAll, kept);
         for (int i = 0; i < k; ++i) {
             const float pi = __shfl_sync(kAll, p, i), gi = __shfl_sync(kAll, g, i);
-            if (__shfl_sync(kAll, (int)kept, i)) against += pi * (g - gi);
+            if ((on >> i) & 1u) against += pi * (g - gi);
         }
         float d = 0.f;
-        if (kept && s != 0.f) d = w_scale * against * (l < -17.f ? 0.5f * p : 1.f / (1.f + expf(-l)) / (2.f * s) / total);
+        if (kept && s != 0.f) d = w_scale * against * (l < -17.f ? 0.5f * p : 0.5f / ((1.f + expf(-l)) * s * total));
         // an id that stands twice: its first slot writes the sum
         float sum = 0.f;
         bool before = false;
@@ -359,8 +360,8 @@ struct CombineBackwardLaunch {
     cudaError_t operator()() const {
         // eight warps a slot where there are slots too few to fill the GPU with fewer (150 SMs
         // of 16 slots); with two warps and one chunk in flight a thread the long batch takes
-        // 131 us, with one or four 136 (two in blocks of 256: 132), with fewer warps on an SM
-        // 165 and more
+        // 130 us, with one or four 134 (one slot a block of 64: 130, but 6.7 for 5.1 us at 1024
+        // tokens of 1024), with fewer warps on an SM 165 and more
         const long long R = (long long)T * k;
         return R < 2400 ? launch<A, O, C, 2 * U, 8>((unsigned)R) : launch<A, O, C, U, 2>((unsigned)((R + 1) / 2));
     }
