@@ -23,7 +23,7 @@
 //
 // Measured at K = N = 4096 (bf16 out), the copy rate being 6.78 TB/s and cuBLAS's bf16
 // rate 1909 TFLOP/s: 3000 rows over some 231 of 256 experts 630 us, 6.2 TB/s of
-// weights; 49152 rows over 256 experts 1.27 ms, 1.30 PFLOP/s, where a fixed 14 us a
+// weights; 49152 rows over 256 experts 1.29 ms, 1.28 PFLOP/s, where a fixed 14 us a
 // round (a tile's 32 units of weights, whatever its rows) weighs on tiles of 150
 // rows; 8192 rows of one expert 155 us, 1.77 PFLOP/s.
 #include <cuda.h>
@@ -762,6 +762,8 @@ cudaError_t launch_o(const Product& a, const CUtensorMap& map, cudaStream_t s) {
     // 15.3 with 31, 17.4 with 62; wide 15.6, 15.8 and 16.7, then 18.6 with 100, 20.4 with
     // 150, 22.6 with 200.  So 32 experts of 31 positions take 107 us narrow and 110 wide, of
     // 62 122 and 117, of 100 194 and 130; one of 256 19 and 27, of 512 32 and 28.
+    // The segments themselves are on the device, and are taken as equal here: 3000 rows on 8
+    // of 256 experts run narrow, at 146 us where the wide form takes 83.
     const double segs = a.E < a.R ? a.E : a.R;
     auto cost = [&](int cap, int channels, int at_once, double base, double a_row) {
         const double mean = a.R / segs, each = a.E == 1 ? (a.R + cap - 1) / cap : mean / cap + 0.5;
