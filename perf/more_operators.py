@@ -20,7 +20,8 @@ Blocks: e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two codes 
 byte, the even element low, times a scale for each
   mxfp4      32 elements, 2^(floor(log2 max) - 2)
   nvfp4      16 elements, e4m3 of max / 6 / scale; element = value * e4m3 * scale
-             with scale = (the row's max) / 2688 in 32 bits
+             with scale the least power of two from (the row's max) / 2688 up, so that
+             no e4m3 passes 448 and dividing by it rounds nothing
 both rounded to nearest, half to even, up to 6.
 """
 import math
@@ -215,17 +216,14 @@ def _blocks(x, form):
         e = torch.where(most > 0, torch.frexp(most).exponent - 3, -127).clamp(min=-127)
         s, scale, y = _power(e), None, b * _power(-e)[:, :, None]
     else:
-        top = most.amax(1)
-        scale = top / torch.full_like(top, 2688.0)  # a quotient, not a product with a rounded 1 / 2688
-        # rows in 16 bits have values half way between two codes, which 32 bits would take to either side
-        wide = scale.double()[:, None]
-        t = torch.where(wide > 0, most.double() / (6.0 * wide), 0.0).clamp(max=448.0)
-        step = torch.exp2((torch.frexp(t).exponent - 4).clamp(min=-9).double())
-        s = torch.round(t / step) * step
-        d = (s * wide)[:, :, None]
-        y = torch.where(d > 0, b.double() / d, 0.0)
-        s = s.float()
-    return torch.where(torch.signbit(y), -_e2m1(y.abs()), _e2m1(y.abs())).float().view_as(x), s, scale
+        m, e = torch.frexp(most.amax(1))
+        scale = torch.where(m > 0, _power((e - torch.where(m <= 0.65625, 12, 11)).clamp(min=-126)), 0.0)
+        # (tensors of sixes: a product with a rounded 1 / 6 is not a quotient)
+        t = torch.where(scale[:, None] > 0, most / torch.full_like(most, 6.0) / scale[:, None], 0.0)
+        s = t.clamp(max=448.0).to(torch.float8_e4m3fn).float()
+        d = (s * scale[:, None])[:, :, None]
+        y = torch.where(d > 0, b / d, 0.0)
+    return torch.where(torch.signbit(y), -_e2m1(y.abs()), _e2m1(y.abs())).view_as(x), s, scale
 
 
 def _codes(v):
@@ -357,6 +355,12 @@ def run(state):
 
 # --------------------------------------------------------- definition, 64 bits --
 _GRID = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+_FINE = [b * 2.0 ** -9 if b < 8 else (8 + b % 8) * 2.0 ** (b // 8 - 10) for b in range(127)]  # e4m3 values
+
+
+def _two(e):
+    """2^e in 64 bits, for whole e (pow of a tensor is off by a rounding on some devices)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
 
 
 def _nearest(a, grid):
@@ -367,19 +371,19 @@ def _nearest(a, grid):
 
 
 def _exact_rows(x, form):
-    """(block values, row scales) of rows in 64 bits; the row scale is held in 32."""
+    """(block values, row scales) of rows in 64 bits."""
     grid = torch.tensor(_GRID, dtype=torch.float64, device="cuda")
     n = BLOCK[form]
     values, scales = torch.empty_like(x), torch.ones(x.shape[0], dtype=torch.float64, device="cuda")
     if form == "nvfp4":
-        byte = torch.arange(127, device="cuda")
-        fine = torch.where(byte < 8, byte * 2.0 ** -9, (8 + byte % 8) * 2.0 ** (byte // 8 - 10.0)).double()
-        scales = (x.abs().amax(1) / 2688).float().double()
+        fine = torch.tensor(_FINE, dtype=torch.float64, device="cuda")
+        m, e = torch.frexp(x.abs().amax(1) / 2688)
+        scales = _two(torch.where(m == 0.5, e - 1, e).clamp(min=-126))
     for k in range(0, x.shape[1], n):
         b = x[:, k:k + n]
         most = b.abs().amax(1)
         if form == "mxfp4":
-            s = torch.where(most > 0, 2.0 ** (torch.frexp(most).exponent - 3).clamp(min=-127).double(), 2.0 ** -127)
+            s = _two(torch.where(most > 0, torch.frexp(most).exponent - 3, -127).clamp(min=-127))
             d = s
         else:
             s = _nearest(most / (6 * scales.clamp(min=1e-300)), fine)
@@ -396,6 +400,7 @@ def _exact_product(st):
     if c["gated"]:
         x = x[:, :K] * torch.sigmoid(x[:, :K]) * x[:, K:]
     rows, scale = _exact_rows(x, form)
+    fine = torch.tensor(_FINE, dtype=torch.float64, device="cuda")
     both = torch.tensor(_GRID + tuple(-v for v in _GRID), dtype=torch.float64, device="cuda")
     ends = st["offsets"].tolist() if E > 1 else [0, c["tokens"]]
     src = st["row_src"].long() // k if E > 1 and not c["gated"] else torch.arange(c["tokens"] * k, device="cuda")
@@ -404,8 +409,8 @@ def _exact_product(st):
         at = src[ends[e]:ends[e + 1]]
         if not len(at):
             continue
-        codes, sb = st["wq"][e].long(), st["ws"][e].double()
-        s = 2.0 ** (sb - 127) if form == "mxfp4" else torch.where(sb < 8, sb * 2.0 ** -9, (8 + sb % 8) * 2.0 ** (torch.floor(sb / 8) - 10))
+        codes, s = st["wq"][e].long(), st["ws"][e].long()
+        s = _two(s - 127) if form == "mxfp4" else fine[s]
         w = torch.empty(c["N"], K, dtype=torch.float64, device="cuda")
         w[:, 0::2], w[:, 1::2] = both[codes % 16], both[codes // 16]
         w *= s.repeat_interleave(BLOCK[form], dim=1)
