@@ -41,7 +41,8 @@ EXPORTS = ("moe_create", "moe_destroy", "moe_route", "moe_route_hash", "moe_perm
            "moe_set_decode_kernel", "moe_decode_info", "moe_dispatch", "moe_dispatch_backward",
            "moe_combine", "moe_combine_backward", "moe_route_backward", "moe_quantize_rows",
            "moe_expert_product", "moe_check_product", "moe_test_stall_next_product", "moe_permute_scratch",
-           "moe_permute_scratch_bytes")
+           "moe_permute_scratch_bytes", "moe_norm_rows", "moe_norm_rows_backward", "moe_norm_scratch_bytes",
+           "moe_quantize_blocks", "moe_dequantize_blocks", "moe_block_product")
 
 
 class MoeError(RuntimeError):
@@ -114,6 +115,12 @@ def load_library(build: bool = True) -> C.CDLL:
         "moe_route_backward": ([vp, vp, vp, i, i, i, f, vp, vp], i),
         "moe_quantize_rows": ([vp, i, ll, i, i, i, vp, ll, vp, vp], i),
         "moe_expert_product": ([vp, ll, i, vp, i, vp, vp, i, i, vp, vp, i, i, vp, i, ll, vp], i),
+        "moe_norm_rows": ([vp, i, ll, vp, ll, vp, i, i, i, f, vp, ll, vp, ll, vp, vp, ll, vp, vp], i),
+        "moe_norm_scratch_bytes": ([i, i], C.c_size_t),
+        "moe_norm_rows_backward": ([vp, i, ll, vp, ll, vp, ll, vp, i, vp, i, i, vp, ll, vp, vp, C.c_size_t, vp], i),
+        "moe_quantize_blocks": ([vp, i, ll, i, i, i, i, vp, ll, vp, vp, i, vp], i),
+        "moe_dequantize_blocks": ([vp, ll, vp, vp, i, i, i, vp, i, ll, vp], i),
+        "moe_block_product": ([vp, ll, i, vp, vp, i, i, vp, vp, vp, i, i, vp, vp, i, i, vp, i, ll, vp], i),
         "moe_check_product": ([vp], i),
         "moe_test_stall_next_product": ([], i),
     }
@@ -606,6 +613,168 @@ def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, t
                                 None if offsets is None else _ptr(offsets, torch.int32, (E + 1,), "offsets"),
                                 None if row_src is None else _ptr(row_src, torch.int32, (R,), "row_src"),
                                 int(top_k), R, po, dto, so, _here(stream, q, scale, wq, w_scale, out, offsets, row_src))
+    if st:
+        _check(st)
+
+
+def _same_rows(t, name, dt, T, H):
+    """_rows of an optional operand: (None, 0) without it."""
+    if t is None:
+        return None, 0
+    p, code, step = _rows(t, name, T, H)
+    if code != dt or dt is None:
+        raise ValueError(f"{name} must have the rows' floating dtype, got {t.dtype}")
+    return p, step
+
+
+def _gamma(gamma, dt, H):
+    code = _ROW_TYPES.get(getattr(gamma, "dtype", None))
+    if code is None or code not in (dt, MOE_F32):
+        raise ValueError("gamma must be a CUDA tensor in the rows' dtype or float32")
+    return _ptr(gamma, gamma.dtype, (H,), "gamma"), code
+
+
+def moe_norm_rows(x, gamma, y, eps: float = 1e-6, residual=None, h=None, rstd=None, q=None, scale=None, stream=None):
+    """h = x + residual, rstd = 1 / sqrt(mean h^2 + eps) [T], y = h * rstd * gamma, and y as int8
+    codes q with one float32 scale a row.  x, residual, h, y [T][H] in one floating dtype, gamma
+    [H] in it or float32; without a residual h = x; y may be None where q is given."""
+    T, H = x.shape
+    if T == 0:
+        return
+    px, dt, sx = _rows(x, "x")
+    pr, sr = _same_rows(residual, "residual", dt, T, H)
+    ph, sh = _same_rows(h, "h", dt, T, H)
+    py, sy = _same_rows(y, "y", dt, T, H)
+    pq, sq = None, 0
+    if dt is None:
+        raise ValueError("x must be a floating tensor")
+    if q is not None:
+        pq, dtq, sq = _rows(q, "q", T, H)
+        if dtq is not None:
+            raise ValueError("q must be int8")
+    pg, dtg = _gamma(gamma, dt, H)
+    lib = _lib or load_library()
+    st = lib.moe_norm_rows(px, dt, sx, pr, sr, pg, dtg, T, H, float(eps), ph, sh, py, sy,
+                           None if rstd is None else _ptr(rstd, torch.float32, (T,), "rstd"), pq, sq,
+                           None if scale is None else _ptr(scale, torch.float32, (T,), "scale"),
+                           _here(stream, x, residual, gamma, h, y, rstd, q, scale))
+    if st:
+        _check(st)
+
+
+def moe_norm_scratch_bytes(T: int, hidden: int) -> int:
+    """Bytes of scratch of moe_norm_rows_backward with dgamma; 0 for sizes that it does not take."""
+    return (_lib or load_library()).moe_norm_scratch_bytes(T, hidden)
+
+
+def moe_norm_rows_backward(dy, h, gamma, rstd, dx, dgamma=None, scratch=None, dh=None, stream=None):
+    """dx [T][H] (of x and of the residual alike) and dgamma [H] in float32 from dy and, where the
+    residual stream goes on, dh; h and rstd as moe_norm_rows gave them.  dgamma needs scratch, a
+    CUDA uint8 tensor of moe_norm_scratch_bytes."""
+    T, H = h.shape
+    ph, dt, sh = _rows(h, "h")
+    if dt is None:
+        raise ValueError("h must be a floating tensor")
+    pd, sd = _same_rows(dy, "dy", dt, T, H)
+    pe, se = _same_rows(dh, "dh", dt, T, H)
+    px, sx = _same_rows(dx, "dx", dt, T, H)
+    pg, dtg = _gamma(gamma, dt, H)
+    lib = _lib or load_library()
+    st = lib.moe_norm_rows_backward(pd, dt, sd, pe, se, ph, sh, pg, dtg, _ptr(rstd, torch.float32, (T,), "rstd"), T, H,
+                                    px, sx, None if dgamma is None else _ptr(dgamma, torch.float32, (H,), "dgamma"),
+                                    None if scratch is None else _ptr(scratch, torch.uint8, None, "scratch"),
+                                    0 if scratch is None else scratch.numel(),
+                                    _here(stream, dy, h, gamma, rstd, dx, dgamma, scratch, dh))
+    if st:
+        _check(st)
+
+
+_BLOCK = {MOE_WEIGHTS_MXFP4: 32, MOE_WEIGHTS_NVFP4: 16}
+
+
+def _codes(q, name, rows=None, K=None):
+    """(pointer, stride in bytes, rows, K) of uint8 rows of two codes a byte."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dtype != torch.uint8 or q.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA uint8 tensor of codes, two a byte")
+    n, half = q.shape
+    if (rows is not None and n != rows) or (K is not None and 2 * half != K):
+        raise ValueError(f"{name} must have shape ({rows}, {K // 2}), got {tuple(q.shape)}")
+    step, inner = q.stride()
+    if inner != 1 and half > 1:
+        raise ValueError(f"the bytes of a row of {name} must be adjacent")
+    return q.data_ptr(), (step if n > 1 else half), n, 2 * half
+
+
+def _block(fmt) -> int:
+    if fmt not in _BLOCK:
+        raise ValueError(f"fmt must be MOE_WEIGHTS_MXFP4 or MOE_WEIGHTS_NVFP4, got {fmt}")
+    return _BLOCK[fmt]
+
+
+def moe_quantize_blocks(x, q, s, scale=None, fmt: int = MOE_WEIGHTS_NVFP4, gated: bool = False, given: bool = False,
+                        stream=None):
+    """x [rows][K] (gated: [rows][2 K], SiLU of the first half times the second) to blocks of
+    4-bit codes q [rows][K / 2], two a byte, with scale bytes s [rows][K / 16] and a float32
+    scale a row (NVFP4; `given`: read, not written) or s [rows][K / 32] and no scale (MXFP4)."""
+    n = _block(fmt)
+    pq, sq, rows, K = _codes(q, "q")
+    if rows == 0:
+        return
+    px, dt, sx = _rows(x, "x", rows, 2 * K if gated else K)
+    if dt is None:
+        raise ValueError("x must be a floating tensor")
+    lib = _lib or load_library()
+    st = lib.moe_quantize_blocks(px, dt, sx, int(bool(gated)), rows, K, fmt, pq, sq,
+                                 _ptr(s, torch.uint8, (rows, K // n), "s"),
+                                 None if scale is None else _ptr(scale, torch.float32, (rows,), "scale"),
+                                 int(bool(given)), _here(stream, x, q, s, scale))
+    if st:
+        _check(st)
+
+
+def moe_dequantize_blocks(q, s, x, scale=None, fmt: int = MOE_WEIGHTS_NVFP4, stream=None):
+    """Blocks of 4-bit codes (moe_quantize_blocks) back to rows x [rows][K]."""
+    n = _block(fmt)
+    pq, sq, rows, K = _codes(q, "q")
+    if rows == 0:
+        return
+    px, dt, sx = _rows(x, "x", rows, K)
+    if dt is None:
+        raise ValueError("x must be a floating tensor")
+    lib = _lib or load_library()
+    st = lib.moe_dequantize_blocks(pq, sq, _ptr(s, torch.uint8, (rows, K // n), "s"),
+                                   None if scale is None else _ptr(scale, torch.float32, (rows,), "scale"), rows, K, fmt,
+                                   px, dt, sx, _here(stream, q, s, x, scale))
+    if st:
+        _check(st)
+
+
+def moe_block_product(q, s, wq, ws, out, offsets=None, row_src=None, top_k: int = 1, scale=None, w_scale=None,
+                      fmt: int = MOE_WEIGHTS_NVFP4, stream=None):
+    """out[p] = scale[r] * w_scale[e] * (w[e] v[r]) for the positions p of expert e's segment, v and w
+    the values of 4-bit blocks; r = row_src[p] // top_k, or p without row_src.  q [rows][K / 2] and
+    s, scale as moe_quantize_blocks makes them; wq [E][N][K / 2], ws [E][N][K / 16 or K / 32],
+    w_scale [E][N]; out [R][N]; offsets [E + 1] may be left out with one expert."""
+    R, N = out.shape
+    n = _block(fmt)
+    if R == 0:
+        return
+    if wq.dim() != 3:
+        raise ValueError(f"wq must have shape (E, N, K / 2), got {tuple(wq.shape)}")
+    E, _, half = wq.shape
+    K = 2 * half
+    pq, sq, rows, _ = _codes(q, "q", q.shape[0], K)
+    po, dto, so = _rows(out, "out")
+    if dto is None:
+        raise ValueError("out must be a floating tensor")
+    lib = _lib or load_library()
+    st = lib.moe_block_product(pq, sq, rows, _ptr(s, torch.uint8, (rows, K // n), "s"),
+                               None if scale is None else _ptr(scale, torch.float32, (rows,), "scale"), K, fmt,
+                               _ptr(wq, torch.uint8, (E, N, half), "wq"), _ptr(ws, torch.uint8, (E, N, K // n), "ws"),
+                               None if w_scale is None else _ptr(w_scale, torch.float32, (E, N), "w_scale"), E, N,
+                               None if offsets is None else _ptr(offsets, torch.int32, (E + 1,), "offsets"),
+                               None if row_src is None else _ptr(row_src, torch.int32, (R,), "row_src"), int(top_k), R,
+                               po, dto, so, _here(stream, q, s, scale, wq, ws, w_scale, out, offsets, row_src))
     if st:
         _check(st)
 

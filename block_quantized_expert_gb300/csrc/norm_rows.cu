@@ -1,0 +1,420 @@
+// norm_rows.cu -- the root-mean-square norm in front of an expert layer, with the
+// residual's addition and 8-bit codes (moe_norm_rows), and its gradient
+// (moe_norm_rows_backward; C entries at the end).
+//
+//   h = x + residual, rounded to the rows' type;  r = 1 / sqrt(mean h^2 + eps)
+//   y = h r gamma, rounded to the rows' type
+//
+// and with g = dy gamma, dh the gradient that reaches h by the residual's way:
+//
+//   dx = dh + r (g - h r^2 mean(g h)),   dgamma = sum_t dy h r
+//
+// The mean is over the h that the stream holds, so that the gradient, which has
+// only that h, is the gradient of what was computed.  Sums are fp32 in a fixed
+// order: equal calls give equal bits.  As in sorted_rows.cu no input is
+// `const __restrict__`; here h may be x or residual itself, too.
+#include <cmath>
+#include <type_traits>
+
+#include "entry.h"
+#include "row_codes.cuh"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+// Sum over the block, the same in every thread; `part` is free again after the
+// next __syncthreads.
+__device__ __forceinline__ float block_sum(float v, float* part) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v += part[i];
+    return v;
+}
+
+template <typename A>
+struct Norm {
+    const A *x, *residual;
+    long long xs, rs;
+    const void* gamma;
+    int H;
+    float eps;
+    A *h, *y;  // either may be NULL
+    long long hs, ys;
+    float* rstd;  // may be NULL
+    int8_t* q;    // NULL: no codes
+    long long qs;
+    float* scale;
+};
+
+// One block a row.  kKeep chunks of C elements a thread stay in registers from the
+// sum to the codes; kKeep = 0: rows of any length, read again for each pass (from h
+// where it is written: it may lie over an input).
+template <typename A, typename G, int C, int kKeep>
+__global__ void __launch_bounds__(1024) k_norm_rows(const Norm<A> a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ float part[32];
+    __shared__ uint32_t tops[32];
+    const long long t = blockIdx.x;
+    const int first = threadIdx.x * C, step = blockDim.x * C, H = a.H;
+    const A* x = a.x + t * a.xs;
+    const G* gamma = reinterpret_cast<const G*>(a.gamma);
+    constexpr int kHeld = kKeep ? kKeep : 1;
+    Chunk<A, C> held[kHeld];
+    auto each = [&](auto&& f) {
+        if (kKeep) {
+#pragma unroll
+            for (int n = 0; n < kHeld; ++n)
+                if (first + n * step < H) f(held[n], first + n * step);
+        } else {
+            for (int c = first; c < H; c += step) f(held[0], c);
+        }
+    };
+    float sum = 0.f;
+    each([&](Chunk<A, C>& v, int c) {
+        v = load_chunk<A, C>(x + c);
+        if (a.residual) {
+            const Chunk<A, C> r = load_chunk<A, C>(a.residual + t * a.rs + c);
+#pragma unroll
+            for (int i = 0; i < C; ++i) v.v[i] = from_f32<A>(to_f32(v.v[i]) + to_f32(r.v[i]));
+        }
+        if (a.h) *reinterpret_cast<Chunk<A, C>*>(a.h + t * a.hs + c) = v;
+#pragma unroll
+        for (int i = 0; i < C; ++i) sum = fmaf(to_f32(v.v[i]), to_f32(v.v[i]), sum);
+    });
+    const float r = 1.f / sqrtf(block_sum(sum, part) / (float)H + a.eps);
+    if (threadIdx.x == 0 && a.rstd) a.rstd[t] = r;
+    // y of a chunk of h, in place
+    auto scaled = [&](Chunk<A, C>& v, int c) {
+        const Chunk<G, C> g = load_chunk<G, C>(gamma + c);
+#pragma unroll
+        for (int i = 0; i < C; ++i) v.v[i] = from_f32<A>(to_f32(v.v[i]) * r * to_f32(g.v[i]));
+    };
+    const A* from = a.h ? a.h + t * a.hs : x;
+    auto again = [&](Chunk<A, C>& v, int c) {  // kKeep = 0: h of the row once more
+        v = load_chunk<A, C>(from + c);
+        if (a.residual && !a.h) {
+            const Chunk<A, C> e = load_chunk<A, C>(a.residual + t * a.rs + c);
+#pragma unroll
+            for (int i = 0; i < C; ++i) v.v[i] = from_f32<A>(to_f32(v.v[i]) + to_f32(e.v[i]));
+        }
+    };
+    uint32_t top = 0;
+    each([&](Chunk<A, C>& v, int c) {
+        if (!kKeep) again(v, c);
+        scaled(v, c);
+        if (a.y) *reinterpret_cast<Chunk<A, C>*>(a.y + t * a.ys + c) = v;
+        if (a.q) top = top_bits<A, C>(v, top);
+    });
+    if (!a.q) return;
+    const float most = block_most<A>(top, tops);
+    const RowScale by = row_scale(most);
+    if (threadIdx.x == 0) a.scale[t] = by.scale;
+    each([&](Chunk<A, C>& v, int c) {
+        if (!kKeep) {
+            if (a.y) {
+                v = load_chunk<A, C>(a.y + t * a.ys + c);
+            } else {
+                again(v, c);
+                scaled(v, c);
+            }
+        }
+        float f[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) f[i] = to_f32(v.v[i]);
+        Chunk<int8_t, C> out = {};
+        if (by.live) out = quant_codes(f, by.c127, by.m, by.by);
+        *reinterpret_cast<Chunk<int8_t, C>*>(a.q + t * a.qs + c) = out;
+    });
+}
+
+// ---------------------------------------------------------------- gradient --
+template <typename A>
+struct NormBack {
+    const A *dy, *dh, *h;  // dh may be NULL
+    long long dys, dhs, hs;
+    const void* gamma;
+    const float* rstd;
+    int T, H;
+    A* dx;
+    long long dxs;
+    float* part;  // [gridDim.x][H] sums of dy h r over a block's rows, or NULL
+};
+
+// A block walks rows t, t + gridDim.x, ... ; a thread's columns stay the same, so
+// its share of dgamma is summed in registers and written once.
+template <typename A, typename G, int C, int kKeep>
+__global__ void __launch_bounds__(1024) k_norm_backward(const NormBack<A> a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ float part[2][32];
+    const int first = threadIdx.x * C, step = blockDim.x * C, H = a.H;
+    float gamma[kKeep][C], dgamma[kKeep][C];
+#pragma unroll
+    for (int n = 0; n < kKeep; ++n) {
+        Chunk<G, C> g = {};
+        if (first + n * step < H) g = load_chunk<G, C>(reinterpret_cast<const G*>(a.gamma) + first + n * step);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            gamma[n][i] = to_f32(g.v[i]);
+            dgamma[n][i] = 0.f;
+        }
+    }
+    int turn = 0;
+    for (long long t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+        Chunk<A, C> dy[kKeep], h[kKeep], dh[kKeep];
+        const float r = a.rstd[t];
+#pragma unroll
+        for (int n = 0; n < kKeep; ++n) {
+            const int c = first + n * step;
+            if (c >= H) continue;
+            dy[n] = load_chunk<A, C>(a.dy + t * a.dys + c);
+            h[n] = load_chunk<A, C>(a.h + t * a.hs + c);
+            if (a.dh) dh[n] = load_chunk<A, C>(a.dh + t * a.dhs + c);
+        }
+        float dot = 0.f;
+#pragma unroll
+        for (int n = 0; n < kKeep; ++n)
+            if (first + n * step < H) {
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    const float v = to_f32(dy[n].v[i]), w = to_f32(h[n].v[i]) * r;
+                    dot = fmaf(v * gamma[n][i], w, dot);
+                    dgamma[n][i] = fmaf(v, w, dgamma[n][i]);
+                }
+            }
+        const float mean = block_sum(dot, part[turn]) / (float)H;  // of g h r
+#pragma unroll
+        for (int n = 0; n < kKeep; ++n) {
+            const int c = first + n * step;
+            if (c >= H) continue;
+            float f[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                f[i] = r * (to_f32(dy[n].v[i]) * gamma[n][i] - to_f32(h[n].v[i]) * r * mean);
+                if (a.dh) f[i] += to_f32(dh[n].v[i]);
+            }
+            store_chunk<A, C>(a.dx + t * a.dxs + c, f);
+        }
+    }
+    if (a.part) {
+#pragma unroll
+        for (int n = 0; n < kKeep; ++n)
+            if (first + n * step < H) store_chunk<float, C>(a.part + (long long)blockIdx.x * H + first + n * step, dgamma[n]);
+    }
+}
+
+// Rows of any length: dx alone, a block a row, read twice.
+template <typename A, typename G>
+__global__ void __launch_bounds__(1024) k_norm_backward_long(const NormBack<A> a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ float part[32];
+    const long long t = blockIdx.x;
+    const A *dy = a.dy + t * a.dys, *h = a.h + t * a.hs;
+    const G* gamma = reinterpret_cast<const G*>(a.gamma);
+    const float r = a.rstd[t];
+    float dot = 0.f;
+    for (int c = threadIdx.x; c < a.H; c += blockDim.x) dot = fmaf(to_f32(dy[c]) * to_f32(gamma[c]), to_f32(h[c]) * r, dot);
+    const float mean = block_sum(dot, part) / (float)a.H;
+    for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
+        float f = r * (to_f32(dy[c]) * to_f32(gamma[c]) - to_f32(h[c]) * r * mean);
+        if (a.dh) f += to_f32(a.dh[t * a.dhs + c]);
+        a.dx[t * a.dxs + c] = from_f32<A>(f);
+    }
+}
+
+// Their dgamma: block (x, y) sums 256 columns over the rows y, y + gridDim.y, ...
+template <typename A>
+__global__ void __launch_bounds__(256) k_dgamma_long(const NormBack<A> a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= a.H) return;
+    float sum = 0.f;
+    for (long long t = blockIdx.y; t < a.T; t += gridDim.y)
+        sum = fmaf(to_f32(a.dy[t * a.dys + c]), to_f32(a.h[t * a.hs + c]) * a.rstd[t], sum);
+    a.part[(long long)blockIdx.y * a.H + c] = sum;
+}
+
+// dgamma[c] = the parts' sum: 32 columns a block, each warp a part in turn.
+__global__ void __launch_bounds__(1024) k_join_parts(const float* part, int parts, int H, float* dgamma) {
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float sum = 0.f;
+    if (c < H)
+        for (int p = warp; p < parts; p += 32) sum += part[(long long)p * H + c];
+    sums[warp][lane] = sum;
+    __syncthreads();
+    sum = warp_sum(sums[lane][warp]);
+    if (lane == 0 && blockIdx.x * 32 + warp < H) dgamma[blockIdx.x * 32 + warp] = sum;
+}
+
+// ----------------------------------------------------------------- launches --
+constexpr int kParts = 608;  // blocks of the gradient at most, four an SM
+
+int threads_for(int chunks) { return chunks >= 1024 ? 1024 : (chunks + 31) / 32 * 32; }
+
+template <typename A, typename G, int C>
+cudaError_t norm_c(const Norm<A>& a, int T, cudaStream_t s) {
+    const int chunks = (a.H + C - 1) / C;
+    if (chunks <= 512) return launch_pdl(k_norm_rows<A, G, C, 1>, dim3(T), dim3(threads_for(chunks)), 0, s, a);
+    if (chunks <= 2048) return launch_pdl(k_norm_rows<A, G, C, 4>, dim3(T), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
+    return launch_pdl(k_norm_rows<A, G, C, 0>, dim3(T), dim3(1024), 0, s, a);
+}
+
+template <typename A, typename G, int C>
+cudaError_t back_c(const NormBack<A>& a, float* dgamma, cudaStream_t s) {
+    const int chunks = (a.H + C - 1) / C;
+    int parts = a.T < kParts ? a.T : kParts;
+    cudaError_t e = cudaSuccess;
+    if (a.T == 0) {
+    } else if (chunks <= 4096) {
+        if (chunks <= 256) e = launch_pdl(k_norm_backward<A, G, C, 1>, dim3(parts), dim3(threads_for(chunks)), 0, s, a);
+        else if (chunks <= 512) e = launch_pdl(k_norm_backward<A, G, C, 2>, dim3(parts), dim3(threads_for((chunks + 1) / 2)), 0, s, a);
+        else e = launch_pdl(k_norm_backward<A, G, C, 4>, dim3(parts), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
+    } else {
+        e = launch_pdl(k_norm_backward_long<A, G>, dim3(a.T), dim3(1024), 0, s, a);
+        parts = parts < 16 ? parts : 16;
+        if (e == cudaSuccess && a.part) e = launch_pdl(k_dgamma_long<A>, dim3((a.H + 255) / 256, parts), dim3(256), 0, s, a);
+    }
+    if (e == cudaSuccess && dgamma)
+        e = launch_pdl(k_join_parts, dim3((a.H + 31) / 32), dim3(1024), 0, s, (const float*)a.part, parts, a.H, dgamma);
+    return e;
+}
+
+// The widest chunk that every row of every operand allows (16 bytes of A; gamma's
+// rows are one row of another type).
+template <typename A, typename G, typename F>
+cudaError_t by_chunk(unsigned align, const void* gamma, int H, F&& f) {
+    constexpr int W = 16 / (int)sizeof(A);
+    const uintptr_t g = (uintptr_t)gamma;
+    if (H % W == 0 && align >= 16 && g % 16 == 0) return f(std::integral_constant<int, W>());
+    if (H % 2 == 0 && align >= 2 * sizeof(A) && g % (2 * sizeof(G)) == 0) return f(std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, 1>());
+}
+
+unsigned least(unsigned a, unsigned b) { return a < b ? a : b; }
+
+template <typename A, typename G>
+cudaError_t norm_ag(Norm<A> a, int T, cudaStream_t s) {
+    constexpr long long z = sizeof(A);
+    unsigned al = row_align(a.x, a.xs * z);
+    if (a.residual) al = least(al, row_align(a.residual, a.rs * z));
+    if (a.h) al = least(al, row_align(a.h, a.hs * z));
+    if (a.y) al = least(al, row_align(a.y, a.ys * z));
+    if (a.q) al = least(al, (unsigned)z * row_align(a.q, a.qs));  // a code for each element
+    return by_chunk<A, G>(al, a.gamma, a.H, [&](auto c) { return norm_c<A, G, decltype(c)::value>(a, T, s); });
+}
+
+template <typename A, typename G>
+cudaError_t back_ag(NormBack<A> a, float* dgamma, cudaStream_t s) {
+    constexpr long long z = sizeof(A);
+    unsigned al = least(row_align(a.dy, a.dys * z), row_align(a.h, a.hs * z));
+    al = least(al, row_align(a.dx, a.dxs * z));
+    if (a.dh) al = least(al, row_align(a.dh, a.dhs * z));
+    return by_chunk<A, G>(al, a.gamma, a.H, [&](auto c) { return back_c<A, G, decltype(c)::value>(a, dgamma, s); });
+}
+
+moe_status check_norm(const char* what, moe_dtype dtype, moe_dtype gamma_dtype, int T, int H) {
+    if (!dtype_ok(dtype)) return refuse(MOE_ERR_INVALID_ARG, "%s: unknown dtype", what);
+    if (gamma_dtype != dtype && gamma_dtype != MOE_F32)
+        return refuse(MOE_ERR_INVALID_ARG, "%s: gamma's dtype must be the rows' or MOE_F32", what);
+    if (T < 0 || T > (1 << 24)) return refuse(MOE_ERR_INVALID_ARG, "%s: T must be in [0, 2^24]", what);
+    if (H < 1 || H > 131072) return refuse(MOE_ERR_INVALID_ARG, "%s: hidden must be in [1, 131072]", what);
+    return MOE_OK;
+}
+
+// A matrix of rows; `needed`: it may not be NULL.
+moe_status check_matrix(const char* what, const char* name, const void* p, long long stride, int H, int size, bool needed) {
+    if (!p) return needed ? refuse(MOE_ERR_INVALID_ARG, "%s: %s is NULL", what, name) : MOE_OK;
+    if (stride < H || stride > kMostStride)
+        return refuse(MOE_ERR_INVALID_ARG, "%s: the row stride of %s is below the row or above 2^40", what, name);
+    if ((uintptr_t)p % size) return refuse(MOE_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", what, name);
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_norm_rows(const void* x, moe_dtype dtype, long long x_stride, const void* residual,
+                                    long long residual_stride, const void* gamma, moe_dtype gamma_dtype, int T, int hidden,
+                                    float eps, void* h, long long h_stride, void* y, long long y_stride, float* rstd,
+                                    int8_t* q, long long q_stride, float* scale, moe_stream_t stream) {
+    const char* what = "moe_norm_rows";
+    moe_status st = check_norm(what, dtype, gamma_dtype, T, hidden);
+    if (st == MOE_OK && !(eps >= 0.f && std::isfinite(eps)))
+        st = refuse(MOE_ERR_INVALID_ARG, "%s: eps must be finite and not negative", what);
+    if (st != MOE_OK || T == 0) return st;
+    const int z = dtype_size(dtype);
+    st = check_matrix(what, "x", x, x_stride, hidden, z, true);
+    if (st == MOE_OK) st = check_matrix(what, "residual", residual, residual_stride, hidden, z, false);
+    if (st == MOE_OK) st = check_matrix(what, "h", h, h_stride, hidden, z, false);
+    if (st == MOE_OK) st = check_matrix(what, "y", y, y_stride, hidden, z, q == nullptr);
+    if (st == MOE_OK) st = check_matrix(what, "q", q, q_stride, hidden, 1, false);
+    if (st == MOE_OK) st = check_matrix(what, "gamma", gamma, hidden, hidden, dtype_size(gamma_dtype), true);
+    if (st == MOE_OK && (q == nullptr) != (scale == nullptr))
+        st = refuse(MOE_ERR_INVALID_ARG, "%s: of q and scale one is NULL", what);
+    if (st != MOE_OK) return st;
+    cudaStream_t s = (cudaStream_t)stream;
+    auto run = [&](auto type) {
+        using A = decltype(type);
+        const Norm<A> a{(const A*)x, (const A*)residual, x_stride, residual_stride, gamma, hidden, eps, (A*)h, (A*)y,
+                        h_stride, y_stride, rstd, q, q_stride, scale};
+        return gamma_dtype == MOE_F32 ? norm_ag<A, float>(a, T, s) : norm_ag<A, A>(a, T, s);
+    };
+    cudaError_t e;
+    if (dtype == MOE_F32) e = run(float());
+    else if (dtype == MOE_BF16) e = run(__nv_bfloat16());
+    else e = run(__half());
+    return status_of(e, what);
+}
+
+extern "C" size_t moe_norm_scratch_bytes(int T, int hidden) {
+    if (T < 0 || T > (1 << 24) || hidden < 1 || hidden > 131072) return 0;
+    return (size_t)(T < 1 ? 1 : T < kParts ? T : kParts) * hidden * sizeof(float);
+}
+
+extern "C" moe_status moe_norm_rows_backward(const void* dy, moe_dtype dtype, long long dy_stride, const void* dh,
+                                             long long dh_stride, const void* h, long long h_stride, const void* gamma,
+                                             moe_dtype gamma_dtype, const float* rstd, int T, int hidden, void* dx,
+                                             long long dx_stride, float* dgamma, void* scratch, size_t scratch_bytes,
+                                             moe_stream_t stream) {
+    const char* what = "moe_norm_rows_backward";
+    moe_status st = check_norm(what, dtype, gamma_dtype, T, hidden);
+    if (st != MOE_OK) return st;
+    if (dgamma && (!scratch || scratch_bytes < moe_norm_scratch_bytes(T, hidden)))
+        return refuse(MOE_ERR_INVALID_ARG, "%s: scratch is NULL or below moe_norm_scratch_bytes", what);
+    if (dgamma && (uintptr_t)scratch % 16) return refuse(MOE_ERR_INVALID_ARG, "%s: scratch is not aligned to 16 bytes", what);
+    if (T == 0 && !dgamma) return MOE_OK;
+    const int z = dtype_size(dtype);
+    if (T > 0) {
+        st = check_matrix(what, "dy", dy, dy_stride, hidden, z, true);
+        if (st == MOE_OK) st = check_matrix(what, "dh", dh, dh_stride, hidden, z, false);
+        if (st == MOE_OK) st = check_matrix(what, "h", h, h_stride, hidden, z, true);
+        if (st == MOE_OK) st = check_matrix(what, "dx", dx, dx_stride, hidden, z, true);
+        if (st == MOE_OK) st = check_matrix(what, "gamma", gamma, hidden, hidden, dtype_size(gamma_dtype), true);
+        if (st == MOE_OK && !rstd) st = refuse(MOE_ERR_INVALID_ARG, "%s: rstd is NULL", what);
+        if (st != MOE_OK) return st;
+    }
+    cudaStream_t s = (cudaStream_t)stream;
+    auto run = [&](auto type) {
+        using A = decltype(type);
+        const NormBack<A> a{(const A*)dy, (const A*)dh, (const A*)h, dy_stride, dh_stride, h_stride, gamma, rstd, T,
+                            hidden, (A*)dx, dx_stride, dgamma ? (float*)scratch : nullptr};
+        return gamma_dtype == MOE_F32 ? back_ag<A, float>(a, dgamma, s) : back_ag<A, A>(a, dgamma, s);
+    };
+    cudaError_t e;
+    if (dtype == MOE_F32) e = run(float());
+    else if (dtype == MOE_BF16) e = run(__nv_bfloat16());
+    else e = run(__half());
+    return status_of(e, what);
+}

@@ -478,6 +478,96 @@ moe_status moe_expert_product(const int8_t* q, long long q_stride, int q_rows, c
                               const int32_t* offsets, const int32_t* row_src, int top_k, int R, void* out,
                               moe_dtype out_dtype, long long out_stride, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The norm in front of an expert layer, and rows in blocks of 4-bit codes.
+ * The conventions of the sorted-row calls above hold here too.
+ *
+ * Root-mean-square norm with the residual's addition: for every row
+ *   h = x + residual   rounded to dtype (h = x where residual is NULL)
+ *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * gamma  rounded to dtype
+ * and, where q is given, y as 8-bit codes with one scale a row: exactly what
+ * moe_quantize_rows makes of y, for moe_expert_product.
+ *   x, residual, h, y  device dtype [T][hidden], each with its row stride; h
+ *          (the residual stream to go on with) and y may be NULL, y only if q
+ *          is not; h may be x or residual itself, other outputs lie apart
+ *   gamma  device gamma_dtype [hidden], gamma_dtype being dtype or MOE_F32
+ *   rstd   device f32 [T] or NULL: moe_norm_rows_backward reads it
+ *   q      device i8 [T][hidden] with its stride, scale device f32 [T]; both
+ *          or neither
+ * eps >= 0; 1 <= hidden <= 131072, T <= 2^24.  The sum of squares is held in
+ * fp32: a row where it overflows (|h| of 1e18 and more) has rstd 0.        */
+moe_status moe_norm_rows(const void* x, moe_dtype dtype, long long x_stride, const void* residual,
+                         long long residual_stride, const void* gamma, moe_dtype gamma_dtype, int T,
+                         int hidden, float eps, void* h, long long h_stride, void* y, long long y_stride,
+                         float* rstd, int8_t* q, long long q_stride, float* scale, moe_stream_t stream);
+
+/* Gradient of moe_norm_rows (of y; the codes have none): with g = dy * gamma
+ *   dx = dh + rstd * (g - h * rstd^2 * mean(g * h)),  rounded to dtype
+ *   dgamma = sum over the rows of dy * h * rstd
+ *   dy, h, dx device dtype [T][hidden]; dh the same or NULL (zeros): the
+ *   gradient that reaches h along the residual stream.  x and residual have
+ *   the same gradient dx.  h and rstd are moe_norm_rows's; dx may be dy or dh
+ *   itself.
+ *   dgamma device f32 [hidden], overwritten, or NULL; with it scratch, device,
+ *   16-byte aligned, of at least moe_norm_scratch_bytes (0 for sizes out of
+ *   range), which may be reused when the call's work is done.  T = 0 sets
+ *   dgamma to 0.                                                            */
+size_t moe_norm_scratch_bytes(int T, int hidden);
+moe_status moe_norm_rows_backward(const void* dy, moe_dtype dtype, long long dy_stride, const void* dh,
+                                  long long dh_stride, const void* h, long long h_stride, const void* gamma,
+                                  moe_dtype gamma_dtype, const float* rstd, int T, int hidden, void* dx,
+                                  long long dx_stride, float* dgamma, void* scratch, size_t scratch_bytes,
+                                  moe_stream_t stream);
+
+/* Rows to blocks of e2m1 codes, in the formats and layouts of moe_weights
+ * (two codes a byte, the even element in the low half):
+ *   format MOE_WEIGHTS_MXFP4: blocks of 32 with the UE8M0 byte of
+ *     2^(floor(log2 amax) - 2), at least 2^-127;
+ *   format MOE_WEIGHTS_NVFP4: blocks of 16 with s = e4m3 of amax / 6 / g, an
+ *     element being code * s * g with g = scale[row]; scale_given = 0: g is
+ *     written, the least power of two from max|row| / 2688 up (at least
+ *     2^-126; 0 for a row of zeros), which makes both quotients exact where
+ *     they are half way between two codes; scale_given = 1: g is read (a
+ *     checkpoint's scale of the whole matrix, say), the quotients amax / 6,
+ *     / g and v / (s * g) each rounded in fp32.
+ * Rounded to nearest, half to even, at most 6.  gated as in moe_quantize_rows.
+ *   x device dtype [rows][K] (gated: [rows][2 K]); q device u8 [rows][K / 2]
+ *   with its stride; s device u8 [rows][K / 32] or [rows][K / 16], dense;
+ *   scale device f32 [rows] for NVFP4, NULL for MXFP4.
+ *   K a multiple of 32 in [32, 131072].
+ * A block with an infinity or a NaN gets the NaN byte (255, or 127 for e4m3)
+ * and codes 0, and its row's g, where it is written, is NaN: the products of
+ * that row are NaN.  A block scale may round up by 1/16 of itself: values that
+ * close to the largest of their type come back as infinities.                    */
+moe_status moe_quantize_blocks(const void* x, moe_dtype dtype, long long x_stride, int gated, int rows, int K,
+                               int format, uint8_t* q, long long q_stride, uint8_t* s, float* scale,
+                               int scale_given, moe_stream_t stream);
+
+/* Such rows back: x[r][i] = code * block scale * scale[r], rounded to dtype;
+ * scale NULL stands for ones.                                              */
+moe_status moe_dequantize_blocks(const uint8_t* q, long long q_stride, const uint8_t* s, const float* scale,
+                                 int rows, int K, int format, void* x, moe_dtype dtype, long long x_stride,
+                                 moe_stream_t stream);
+
+/* Sorted rows times 4-bit experts: for the positions p of expert e's segment
+ *   out[p][n] = scale[r] * w_scale[e][n] * sum_i v[r][i] * w[e][n][i]
+ * v and w being code times block scale, both sides in one format.
+ *   q device u8 [q_rows][K / 2] with q_stride a multiple of 16, s device u8
+ *   [q_rows][K / 32 or K / 16], scale device f32 [q_rows] or NULL (ones);
+ *   wq device u8 [n_experts][N][K / 2], ws device u8 [n_experts][N][K / 32 or
+ *   K / 16], w_scale device f32 [n_experts][N] or NULL (ones), all dense; q
+ *   and wq 16-byte aligned; out device out_dtype [R][N], every row of which
+ *   is written.  offsets, row_src and top_k as in moe_expert_product.
+ * Products of block values (which must stay in fp32's normal range) are exact
+ * and summed in fp32, in a fixed order; the sum is
+ * multiplied by scale and by w_scale, in this order, and rounded to out_dtype.
+ * K a multiple of 32 in [32, 131072], 1 <= N <= 2^20, R <= 2^20.           */
+moe_status moe_block_product(const uint8_t* q, long long q_stride, int q_rows, const uint8_t* s,
+                             const float* scale, int K, int format, const uint8_t* wq, const uint8_t* ws,
+                             const float* w_scale, int n_experts, int N, const int32_t* offsets,
+                             const int32_t* row_src, int top_k, int R, void* out, moe_dtype out_dtype,
+                             long long out_stride, moe_stream_t stream);
+
 /* Synchronise `stream` and take (report and clear in one step) the current
  * device's sticky flag of moe_expert_product: MOE_OK, or MOE_ERR_TIMEOUT if
  * a device-side wait of its tensor-core kernel ran out (2 s; that call's
