@@ -3,6 +3,7 @@
 #pragma once
 
 #include "block_rows.cuh"
+#include "layer.h"
 #include "rows.cuh"
 
 namespace moe {
@@ -26,5 +27,11 @@ __device__ __forceinline__ int source_row(const BlockProduct& a, int p) {
     const int r = a.row_src ? (a.row_src[p] < 0 ? -1 : a.row_src[p] / a.k) : p;
     return r < a.rows ? r : -1;
 }
+
+// The tensor-core form (block_product_tc.cu): q and wq 16-byte aligned, qs a multiple of 16.
+cudaError_t launch_block_product_tc(const BlockProduct& a, bool nv, moe_dtype out, cudaStream_t s);
+// Its sticky error flag (common.cuh), taken (read and cleared in one step) after the
+// stream's work.
+cudaError_t block_product_flag(uint32_t* flag, cudaStream_t s);
 
 }  // namespace moe

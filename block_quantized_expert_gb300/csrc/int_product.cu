@@ -11,6 +11,7 @@
 #include <cstdarg>
 #include <cstdio>
 
+#include "block_product.cuh"
 #include "int_product.cuh"
 #include "row_codes.cuh"
 
@@ -359,6 +360,9 @@ cudaError_t product_o(const Product& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool take_product_stall() { return g_stall_next.exchange(false); }
+
 }  // namespace moe
 
 using namespace moe;
@@ -408,7 +412,7 @@ extern "C" moe_status moe_expert_product(const int8_t* q, long long q_stride, in
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (product_tc_fits(a) && !few_rows(a)) {
-        if (g_stall_next.exchange(false)) {
+        if (take_product_stall()) {
             a.stall = 1;
             a.wait_ns = 5000000ull;
         }
@@ -422,10 +426,12 @@ extern "C" moe_status moe_expert_product(const int8_t* q, long long q_stride, in
 
 extern "C" moe_status moe_check_product(moe_stream_t stream) {
     const char* what = "moe_check_product";
-    uint32_t flag = 0;
-    const cudaError_t e = product_flag(&flag, (cudaStream_t)stream);
+    uint32_t flag = 0, blocks = 0;
+    cudaError_t e = product_flag(&flag, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = block_product_flag(&blocks, (cudaStream_t)stream);
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     if (flag) return fail(MOE_ERR_TIMEOUT, "%s: a device-side wait of moe_expert_product ran out", what);
+    if (blocks) return fail(MOE_ERR_TIMEOUT, "%s: a device-side wait of moe_block_product ran out", what);
     return MOE_OK;
 }
 

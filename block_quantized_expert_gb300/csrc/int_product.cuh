@@ -33,6 +33,8 @@ bool product_tc_fits(const Product& a);
 // Its sticky error flag (common.cuh), taken (read and cleared in one step) after the
 // stream's work.
 cudaError_t product_flag(uint32_t* flag, cudaStream_t s);
+// Whether the next product on the tensor cores, of either kind, is to stall (test of its waits).
+bool take_product_stall();
 cudaError_t launch_product_tc(const Product& a, moe_dtype out, cudaStream_t s);
 
 }  // namespace moe

@@ -569,8 +569,9 @@ moe_status moe_block_product(const uint8_t* q, long long q_stride, int q_rows, c
                              long long out_stride, moe_stream_t stream);
 
 /* Synchronise `stream` and take (report and clear in one step) the current
- * device's sticky flag of moe_expert_product: MOE_OK, or MOE_ERR_TIMEOUT if
- * a device-side wait of its tensor-core kernel ran out (2 s; that call's
+ * device's sticky flag of moe_expert_product and moe_block_product: MOE_OK,
+ * or MOE_ERR_TIMEOUT if a device-side wait of their tensor-core kernels ran
+ * out (2 s; that call's
  * output is undefined, later calls are not affected).  There is one flag a
  * device: MOE_ERR_TIMEOUT may be that of a product on any of its streams,
  * and only the first check after it reports it, so all products since the
@@ -579,8 +580,9 @@ moe_status moe_block_product(const uint8_t* q, long long q_stride, int q_rows, c
  * layer.  Not capturable.                                                 */
 moe_status moe_check_product(moe_stream_t stream);
 
-/* Test hook of that guard: in the next moe_expert_product that takes the
- * tensor-core kernel no weight arrives, and its waits run out after 5 ms.
+/* Test hook of that guard: in the next moe_expert_product or
+ * moe_block_product that takes a tensor-core kernel no weight arrives, and
+ * its waits run out after 5 ms.
  * One-shot, for the process.                                              */
 moe_status moe_test_stall_next_product(void);
 
