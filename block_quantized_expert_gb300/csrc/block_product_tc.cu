@@ -40,14 +40,19 @@ struct Cfg {
     static constexpr int kAtoms = kWords * (1 + kHalves);
     static constexpr int kStage = kABytes + kBBytes + (kAtoms * 512 + 1023) / 1024 * 1024;
     static constexpr int kStages = kPair ? 5 : 7;
-    static constexpr int kTabs = 4;                      // tiles whose rows are looked up
+    static constexpr int kAhead = 4;                     // units of scales held in registers
+    static constexpr int kTabs = 8;                      // tiles whose rows are looked up
     static constexpr int kSfCol = 2 * kCap;              // tensor memory: two accumulators, scales
     static constexpr int kSfA = 4 * kWords, kSfB = 4 * kWords * kHalves;
     static constexpr int kSfWarps = 4, kEpiWarps = 4;
     static constexpr int kEpi = kSfWarps;                // warps: scales, epilogue, TMA, MMA, rows
-    static constexpr int kTma = kEpi + kEpiWarps, kMma = kTma + 1, kLook = kMma + 1;
+    static constexpr int kTmaWarps = 4, kGroups = (kRows / 4 + kTmaWarps - 1) / kTmaWarps;  // copies of a warp
+    static constexpr int kTma = kEpi + kEpiWarps, kMma = kTma + kTmaWarps, kLook = kMma + 1;
     static constexpr int kThreads = (kLook + 1) * 32;
     static constexpr int kSmem = 1024 + kStages * kStage;
+    // The scales' loads are up to kAhead + 1 tiles ahead of their stores where a tile is one unit:
+    // the table they wait for must not be one that waits for those stores.
+    static_assert(kAhead + 1 < kTabs, "tables");
     static_assert(kSfCol + kSfA + kSfB <= 512 && kCap % (16 * kCtas) == 0 && kBBytes % 1024 == 0, "tensor memory");
 };
 
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
         }
         for (int i = 0; i < C::kTabs; ++i) {
             mbar_init(tab_full(i), 1);
-            mbar_init(tab_empty(i), 1 + C::kSfWarps + C::kEpiWarps);
+            mbar_init(tab_empty(i), C::kTmaWarps + C::kSfWarps + C::kEpiWarps);
         }
         abort_flag = 0;
         fence_mbar_init();
@@ -249,8 +254,11 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
     };
     bool ok = true;
 
-    if (warp == C::kTma) {
+    if (warp >= C::kTma && warp < C::kTma + C::kTmaWarps) {
         // ------------------------------------------------------ codes (TMA) --
+        // The first warp brings the weights; the positions' rows, four a copy, are shared
+        // out over the lanes of all of them.
+        const int group = (lane < C::kGroups ? lane * C::kTmaWarps + warp - C::kTma : 0);
         int s = 0, n = 0;
         uint32_t phase = 1;
         for (int t = first_tile; t < tiles && ok; t += tile_step, ++n) {
@@ -258,20 +266,20 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
             const int tab = n % C::kTabs, half = columns(w.count) / C::kCtas;
             ok = __all_sync(kAll, wait_for<false>(tab_full(tab), (n / C::kTabs) & 1, abort, a.wait_ns));
             if (!ok) break;
-            const bool mine = 4 * lane < half;  // lane l: positions 4 l .. 4 l + 3 of this CTA's half
+            const bool mine = lane < C::kGroups && 4 * group < half;
             int4 y = make_int4(none, none, none, none);
-            if (mine) y = *reinterpret_cast<const int4*>(&token_row[tab][rank * half + 4 * lane]);
+            if (mine) y = *reinterpret_cast<const int4*>(&token_row[tab][rank * half + 4 * group]);
             leave_tab(tab);
             for (int k0 = 0; k0 < a.K && ok; k0 += C::kUnit) {
                 ok = __all_sync(kAll, wait_for<kPair>(empty(s), phase, abort, a.wait_ns));
                 if (!ok) break;
                 const uint32_t st = base + s * C::kStage;
-                if (lane == 0) {
+                if (warp == C::kTma && lane == 0) {
                     mbar_arrive_expect_tx(landed(s), C::kABytes + half * 128);
                     if (!a.stall) tma_load_2d(st, &wmap, k0 / 2, w.e * a.N + w.n0, landed(s));
                 }
                 __syncwarp();
-                if (mine) gather_rows(st + C::kABytes + lane * 512, &qmap, k0 / 2, y.x, y.y, y.z, y.w, landed(s));
+                if (mine) gather_rows(st + C::kABytes + group * 512, &qmap, k0 / 2, y.x, y.y, y.z, y.w, landed(s));
                 if (++s == C::kStages) {
                     s = 0;
                     phase ^= 1;
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
         const uint32_t at = base + C::kABytes + C::kBBytes + (r & 31) * 16 + (r >> 5) * 4;
         const int blocks = a.K / kSpan;
         const bool wide = a.K % 256 == 0 && ((uintptr_t)a.s | (uintptr_t)a.ws) % (4 * C::kWords) == 0;
-        // the loads run a unit ahead of the stores, over the ends of tiles
+        // the loads run kAhead units ahead of the stores, over the ends of tiles
         int at_t = first_tile, at_k = 0, at_n = 0;
         const uint8_t* rows[1 + C::kHalves];
         auto next_rows = [&]() {
@@ -366,8 +374,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
             }
             leave_tab(tab);
         };
-        uint32_t v[1 + C::kHalves][C::kWords];
-        auto load = [&]() {
+        auto load = [&](uint32_t (&v)[1 + C::kHalves][C::kWords]) {
             if (at_t >= tiles || !ok) return;
 #pragma unroll
             for (int h = 0; h < 1 + C::kHalves; ++h) load_scales<C::kWords, kSpan>(v[h], rows[h], at_k, a.K, wide);
@@ -379,21 +386,28 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
                 next_rows();
             }
         };
+        uint32_t v[C::kAhead][1 + C::kHalves][C::kWords];
         next_rows();
-        load();
+#pragma unroll
+        for (int i = 0; i < C::kAhead; ++i) load(v[i]);
         int s = 0;
         uint32_t phase = 0;
-        for (int t = first_tile; t < tiles && ok; t += tile_step)
-            for (int k0 = 0; k0 < a.K && ok; k0 += C::kUnit) {
+        const int units = (a.K + C::kUnit - 1) / C::kUnit;
+        int left = first_tile < tiles ? (tiles - first_tile + tile_step - 1) / tile_step * units : 0;
+        while (left > 0 && ok) {
+#pragma unroll
+            for (int i = 0; i < C::kAhead; ++i) {
+                if (left == 0 || !ok) break;
+                --left;
                 ok = __all_sync(kAll, wait_for<kPair>(empty(s), phase ^ 1, abort, a.wait_ns));
                 if (!ok) break;
 #pragma unroll
                 for (int h = 0; h < 1 + C::kHalves; ++h)
 #pragma unroll
                     for (int j = 0; j < C::kWords; ++j)
-                        st_shared4(at + s * C::kStage + 512 * (C::kWords * h + j), v[h][j]);
+                        st_shared4(at + s * C::kStage + 512 * (C::kWords * h + j), v[i][h][j]);
                 fence_async_shared();
-                load();
+                load(v[i]);
                 // the codes have landed, too: one arrival for both
                 ok = ok && __all_sync(kAll, wait_for<false>(landed(s), phase, abort, a.wait_ns));
                 if (!ok) break;
@@ -406,6 +420,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
                     phase ^= 1;
                 }
             }
+        }
     } else {
         // -------------------------------------------------------- epilogue --
         const int ew = warp - C::kEpi, et = tid - C::kEpi * 32;  // ew: lanes 32 ew .. of tensor memory
