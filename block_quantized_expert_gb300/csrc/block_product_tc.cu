@@ -40,7 +40,8 @@ struct Cfg {
     static constexpr int kAtoms = kWords * (1 + kHalves);
     static constexpr int kStage = kABytes + kBBytes + (kAtoms * 512 + 1023) / 1024 * 1024;
     static constexpr int kStages = kPair ? 5 : 7;
-    static constexpr int kAhead = 4;                     // units of scales held in registers
+    static constexpr int kSubs = 8 / kWords;             // units of a sector of scales
+    static constexpr int kAhead = 2;                     // sectors of a row held in registers
     static constexpr int kTabs = 8;                      // tiles whose rows are looked up
     static constexpr int kSfCol = 2 * kCap;              // tensor memory: two accumulators, scales
     static constexpr int kSfA = 4 * kWords, kSfB = 4 * kWords * kHalves;
@@ -50,7 +51,7 @@ struct Cfg {
     static constexpr int kTma = kEpi + kEpiWarps, kMma = kTma + kTmaWarps, kLook = kMma + 1;
     static constexpr int kThreads = (kLook + 1) * 32;
     static constexpr int kSmem = 1024 + kStages * kStage;
-    // The scales' loads are up to kAhead + 1 tiles ahead of their stores where a tile is one unit:
+    // The scales' loads are up to kAhead + 1 tiles ahead of their stores where a tile is one sector:
     // the table they wait for must not be one that waits for those stores.
     static_assert(kAhead + 1 < kTabs, "tables");
     static_assert(kSfCol + kSfA + kSfB <= 512 && kCap % (16 * kCtas) == 0 && kBBytes % 1024 == 0, "tensor memory");
@@ -87,13 +88,42 @@ __device__ __forceinline__ void copy_scales(uint32_t on, uint32_t col, uint64_t 
                      ::"r"(col), "l"(desc), "r"(on) : "memory");
 }
 
-// Rows y0 .. y3 of the map, 128 bytes of each from byte x, to 512 bytes of shared memory;
-// a row past the map reads as zeros.
-__device__ __forceinline__ void gather_rows(uint32_t dst, const void* map, int x, int y0, int y1, int y2, int y3, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-        ::"r"(dst), "l"(map), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar) : "memory");
+// A box of the map, and four rows of one, 128 bytes of each from byte x, into this CTA's
+// shared memory; the bytes count on `bar`, which for a pair is the first CTA's.  A row
+// past the map reads as zeros.
+template <bool kPair>
+__device__ __forceinline__ void load_box(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+    if (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+    else
+        tma_load_2d(dst, map, x, y, bar);
+}
+
+template <bool kPair>
+__device__ __forceinline__ void gather_rows(uint32_t dst, const void* map, int x, int4 y, uint32_t bar) {
+    if (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+            ::"r"(dst), "l"(map), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(bar) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+            ::"r"(dst), "l"(map), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(bar) : "memory");
+}
+
+// The address of the pair's first CTA's shared memory at the same place.
+__device__ __forceinline__ uint32_t in_first(uint32_t at) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(at));
+    return r;
+}
+
+__device__ __forceinline__ void arrive_expect_in(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void st_shared4(uint32_t at, uint32_t v) {
@@ -109,27 +139,30 @@ __device__ uint32_t g_block_seen;  // what the check under way has taken
 
 __global__ void k_take_block_flag() { g_block_seen = atomicExch(&g_block_err, 0u); }
 
-// The scale words of one row from K = k0 on, zeros from K on: no row (nullptr) is all
-// zeros.  `wide`: a unit is whole and its words are aligned to their own size.
-template <int kWords, int kSpan>
-__device__ __forceinline__ void load_scales(uint32_t (&w)[kWords], const uint8_t* row, int k0, int K, bool wide) {
+// 32 scale bytes of one row from byte `at` on, zeros from byte `all` on: no row (nullptr)
+// is all zeros.  A whole sector at a time: in pieces of a unit, 16 or 8 bytes, each piece moves
+// its sector again.  words: 8 where every row's sectors are whole and aligned, 1 where its
+// words are, else 0.
+__device__ __forceinline__ void load_scales(uint32_t (&w)[8], const uint8_t* row, int at, int all, int words) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0;
+    for (int i = 0; i < 8; ++i) w[i] = 0;
     if (row == nullptr) return;
-    row += k0 / kSpan;
-    if (wide) {
-        if (kWords == 4)
-            asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[kWords - 1]) : "l"(row));
-        else
-            asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[kWords - 1]) : "l"(row));
+    row += at;
+    if (words == 8) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(row));
         return;
     }
-    const int n = min(K - k0, 256) / kSpan;
+    const int n = all - at;
+    if (words == 1) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i)
+        for (int i = 0; i < 8; ++i)
+            if (4 * i < n) w[i] = *reinterpret_cast<const uint32_t*>(row + 4 * i);
+        return;
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (4 * i + j < n) w[i] |= (uint32_t)row[4 * i + j] << (8 * j);
+    for (int i = 0; i < 32; ++i)
+        if (i < n) w[i / 4] |= (uint32_t)row[i] << (8 * (i & 3));
 }
 
 template <bool kPair, bool kNv, typename O>
@@ -155,8 +188,9 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
     const int first_tile = blockIdx.x / C::kCtas, tile_step = gridDim.x / C::kCtas;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t bar0 = smem_u32(bars);
-    auto landed = [&](int i) { return bar0 + 8u * i; };                       // codes, in this CTA
-    auto full = [&](int i) { return bar0 + 8u * (C::kStages + i); };          // codes and scales, of the pair
+    // (of a pair the first CTA's are used)
+    auto landed = [&](int i) { return bar0 + 8u * i; };               // codes
+    auto scaled = [&](int i) { return bar0 + 8u * (C::kStages + i); };  // scales
     auto empty = [&](int i) { return bar0 + 8u * (2 * C::kStages + i); };
     auto d_full = [&](int i) { return bar0 + 8u * (3 * C::kStages + i); };
     auto d_empty = [&](int i) { return bar0 + 8u * (3 * C::kStages + 2 + i); };
@@ -165,8 +199,8 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
     volatile int* abort = &abort_flag;
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(landed(i), 1);
-            mbar_init(full(i), C::kCtas * C::kSfWarps);
+            mbar_init(landed(i), C::kCtas);
+            mbar_init(scaled(i), C::kCtas * C::kSfWarps);
             mbar_init(empty(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -257,8 +291,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
     if (warp >= C::kTma && warp < C::kTma + C::kTmaWarps) {
         // ------------------------------------------------------ codes (TMA) --
         // The first warp brings the weights; the positions' rows, four a copy, are shared
-        // out over the lanes of all of them.
-        const int group = (lane < C::kGroups ? lane * C::kTmaWarps + warp - C::kTma : 0);
+        // out over all of them.
         int s = 0, n = 0;
         uint32_t phase = 1;
         for (int t = first_tile; t < tiles && ok; t += tile_step, ++n) {
@@ -266,6 +299,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
             const int tab = n % C::kTabs, half = columns(w.count) / C::kCtas;
             ok = __all_sync(kAll, wait_for<false>(tab_full(tab), (n / C::kTabs) & 1, abort, a.wait_ns));
             if (!ok) break;
+            const int group = lane * C::kTmaWarps + warp - C::kTma;
             const bool mine = lane < C::kGroups && 4 * group < half;
             int4 y = make_int4(none, none, none, none);
             if (mine) y = *reinterpret_cast<const int4*>(&token_row[tab][rank * half + 4 * group]);
@@ -273,13 +307,15 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
             for (int k0 = 0; k0 < a.K && ok; k0 += C::kUnit) {
                 ok = __all_sync(kAll, wait_for<kPair>(empty(s), phase, abort, a.wait_ns));
                 if (!ok) break;
-                const uint32_t st = base + s * C::kStage;
+                const int su = __reduce_max_sync(kAll, s);
+                const uint32_t st = base + su * C::kStage, bar = kPair ? in_first(landed(su)) : landed(su);
                 if (warp == C::kTma && lane == 0) {
-                    mbar_arrive_expect_tx(landed(s), C::kABytes + half * 128);
-                    if (!a.stall) tma_load_2d(st, &wmap, k0 / 2, w.e * a.N + w.n0, landed(s));
+                    if (kPair) arrive_expect_in(bar, C::kABytes + half * 128);
+                    else mbar_arrive_expect_tx(bar, C::kABytes + half * 128);
+                    if (!a.stall) load_box<kPair>(st, &wmap, k0 / 2, w.e * a.N + w.n0, bar);
                 }
                 __syncwarp();
-                if (mine) gather_rows(st + C::kABytes + group * 512, &qmap, k0 / 2, y.x, y.y, y.z, y.w, landed(s));
+                if (mine) gather_rows<kPair>(st + C::kABytes + group * 512, &qmap, k0 / 2, y, bar);
                 if (++s == C::kStages) {
                     s = 0;
                     phase ^= 1;
@@ -318,7 +354,8 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
             ok = __all_sync(kAll, wait_for<kPair>(d_empty(b), ((n >> 1) & 1) ^ 1, abort, a.wait_ns));
             tc_fence_after();
             for (int k = a.K; k > 0 && ok; k -= C::kUnit) {
-                ok = __all_sync(kAll, wait_for<kPair>(full(s), phase, abort, a.wait_ns));
+                ok = __all_sync(kAll, wait_for<kPair>(scaled(s), phase, abort, a.wait_ns) &&
+                                          wait_for<kPair>(landed(s), phase, abort, a.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t st = base + __reduce_max_sync(kAll, (uint32_t)s) * C::kStage, sf = st + C::kABytes + C::kBBytes;
@@ -356,9 +393,10 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
         const int r = (lane & 3) * 32 + (lane >> 2) + 8 * warp;
         const uint32_t at = base + C::kABytes + C::kBBytes + (r & 31) * 16 + (r >> 5) * 4;
         const int blocks = a.K / kSpan;
-        const bool wide = a.K % 256 == 0 && ((uintptr_t)a.s | (uintptr_t)a.ws) % (4 * C::kWords) == 0;
-        // the loads run kAhead units ahead of the stores, over the ends of tiles
-        int at_t = first_tile, at_k = 0, at_n = 0;
+        const uintptr_t low = (uintptr_t)a.s | (uintptr_t)a.ws | (uintptr_t)blocks;
+        const int words = low % 32 == 0 ? 8 : low % 4 == 0 ? 1 : 0;
+        // the loads run kAhead sectors ahead of the stores, over the ends of tiles
+        int at_t = first_tile, at_b = 0, at_n = 0;
         const uint8_t* rows[1 + C::kHalves];
         auto next_rows = [&]() {
             if (at_t >= tiles) return;
@@ -374,51 +412,54 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
             }
             leave_tab(tab);
         };
-        auto load = [&](uint32_t (&v)[1 + C::kHalves][C::kWords]) {
+        auto load = [&](uint32_t (&v)[1 + C::kHalves][8]) {
             if (at_t >= tiles || !ok) return;
 #pragma unroll
-            for (int h = 0; h < 1 + C::kHalves; ++h) load_scales<C::kWords, kSpan>(v[h], rows[h], at_k, a.K, wide);
-            at_k += C::kUnit;
-            if (at_k >= a.K) {
-                at_k = 0;
+            for (int h = 0; h < 1 + C::kHalves; ++h) load_scales(v[h], rows[h], at_b, blocks, words);
+            at_b += 32;
+            if (at_b >= blocks) {
+                at_b = 0;
                 at_t += tile_step;
                 ++at_n;
                 next_rows();
             }
         };
-        uint32_t v[C::kAhead][1 + C::kHalves][C::kWords];
+        uint32_t v[C::kAhead][1 + C::kHalves][8];
         next_rows();
 #pragma unroll
         for (int i = 0; i < C::kAhead; ++i) load(v[i]);
-        int s = 0;
+        int s = 0, left = 0;  // left: K of this tile
         uint32_t phase = 0;
-        const int units = (a.K + C::kUnit - 1) / C::kUnit;
-        int left = first_tile < tiles ? (tiles - first_tile + tile_step - 1) / tile_step * units : 0;
-        while (left > 0 && ok) {
+        const int sectors = (blocks + 31) / 32;
+        int all = first_tile < tiles ? (tiles - first_tile + tile_step - 1) / tile_step * sectors : 0;
+        while (all > 0 && ok) {
 #pragma unroll
             for (int i = 0; i < C::kAhead; ++i) {
-                if (left == 0 || !ok) break;
-                --left;
-                ok = __all_sync(kAll, wait_for<kPair>(empty(s), phase ^ 1, abort, a.wait_ns));
-                if (!ok) break;
+                if (all == 0 || !ok) break;
+                --all;
+                if (left <= 0) left = a.K;
 #pragma unroll
-                for (int h = 0; h < 1 + C::kHalves; ++h)
+                for (int u = 0; u < C::kSubs; ++u) {
+                    if (left <= 0 || !ok) break;
+                    left -= C::kUnit;
+                    ok = __all_sync(kAll, wait_for<kPair>(empty(s), phase ^ 1, abort, a.wait_ns));
+                    if (!ok) break;
 #pragma unroll
-                    for (int j = 0; j < C::kWords; ++j)
-                        st_shared4(at + s * C::kStage + 512 * (C::kWords * h + j), v[i][h][j]);
-                fence_async_shared();
+                    for (int h = 0; h < 1 + C::kHalves; ++h)
+#pragma unroll
+                        for (int j = 0; j < C::kWords; ++j)
+                            st_shared4(at + s * C::kStage + 512 * (C::kWords * h + j), v[i][h][u * C::kWords + j]);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (kPair) mbar_arrive_first(scaled(s)); else mbar_arrive(scaled(s));
+                    }
+                    if (++s == C::kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
                 load(v[i]);
-                // the codes have landed, too: one arrival for both
-                ok = ok && __all_sync(kAll, wait_for<false>(landed(s), phase, abort, a.wait_ns));
-                if (!ok) break;
-                __syncwarp();
-                if (lane == 0) {
-                    if (kPair) mbar_arrive_first(full(s)); else mbar_arrive(full(s));
-                }
-                if (++s == C::kStages) {
-                    s = 0;
-                    phase ^= 1;
-                }
             }
         }
     } else {
