@@ -37,24 +37,24 @@ struct Cfg {
     static constexpr int kBBytes = kRows * 128;
     static constexpr int kWords = kNv ? 4 : 2;           // 4-byte words of a row's scales of a unit: an atom each
     static constexpr int kHalves = (kCap + 127) / 128;   // 128-row parts of the positions' scales
-    static constexpr int kAtoms = kWords * (1 + kHalves);
-    static constexpr int kStage = kABytes + kBBytes + (kAtoms * 512 + 1023) / 1024 * 1024;
+    static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kStages = kPair ? 5 : 7;
-    static constexpr int kSubs = 8 / kWords;             // units of a sector of scales
-    static constexpr int kAhead = 2;                     // sectors of a row held in registers
-    static constexpr int kTabs = 8;                      // tiles whose rows are looked up
+    // Scales come in batches of 64 bytes a row, four units or eight; the units of two batches
+    // lie apart by a few banks more than their atoms, so that the stores of one row's meet
+    // other banks.
+    static constexpr int kBatch = 16 / kWords;
+    static constexpr int kSfStride = kWords * (1 + kHalves) * 512 + 8 * kWords;
+    static constexpr int kTabs = 4;                      // tiles whose rows are looked up
     static constexpr int kSfCol = 2 * kCap;              // tensor memory: two accumulators, scales
     static constexpr int kSfA = 4 * kWords, kSfB = 4 * kWords * kHalves;
     static constexpr int kSfWarps = 4, kEpiWarps = 4;
     static constexpr int kEpi = kSfWarps;                // warps: scales, epilogue, TMA, MMA, rows
-    static constexpr int kTmaWarps = 4, kGroups = (kRows / 4 + kTmaWarps - 1) / kTmaWarps;  // copies of a warp
+    static constexpr int kTmaWarps = kPair ? 6 : 4, kGroups = (kRows / 4 + kTmaWarps - 1) / kTmaWarps;  // copies of a warp
     static constexpr int kTma = kEpi + kEpiWarps, kMma = kTma + kTmaWarps, kLook = kMma + 1;
     static constexpr int kThreads = (kLook + 1) * 32;
-    static constexpr int kSmem = 1024 + kStages * kStage;
-    // The scales' loads are up to kAhead + 1 tiles ahead of their stores where a tile is one sector:
-    // the table they wait for must not be one that waits for those stores.
-    static_assert(kAhead + 1 < kTabs, "tables");
+    static constexpr int kSmem = 1024 + kStages * kStage + 2 * kBatch * kSfStride;
     static_assert(kSfCol + kSfA + kSfB <= 512 && kCap % (16 * kCtas) == 0 && kBBytes % 1024 == 0, "tensor memory");
+    static_assert(kSfWarps == 4, "scales");
 };
 
 // D[tmem] (+)= (A sfa)(B sfb)^T over K = 64, both operands in shared memory; issued
@@ -139,29 +139,25 @@ __device__ uint32_t g_block_seen;  // what the check under way has taken
 
 __global__ void k_take_block_flag() { g_block_seen = atomicExch(&g_block_err, 0u); }
 
-// 32 scale bytes of one row from byte `at` on, zeros from byte `all` on: no row (nullptr)
-// is all zeros.  A whole sector at a time: in pieces of a unit, 16 or 8 bytes, each piece moves
-// its sector again.  words: 8 where every row's sectors are whole and aligned, 1 where its
-// words are, else 0.
-__device__ __forceinline__ void load_scales(uint32_t (&w)[8], const uint8_t* row, int at, int all, int words) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 0;
-    if (row == nullptr) return;
+// 16 scale bytes of one row from byte `at` on, zeros from byte `all` on: no row (nullptr)
+// is all zeros.  bytes: 16 or 4 where every row's pieces of that size are whole and aligned.
+__device__ __forceinline__ void load_scales(uint32_t (&w)[4], const uint8_t* row, int at, int all, int bytes) {
+    w[0] = w[1] = w[2] = w[3] = 0;
+    if (row == nullptr || at >= all) return;
     row += at;
-    if (words == 8) {
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(row));
+    if (bytes == 16) {
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(row));
         return;
     }
     const int n = all - at;
-    if (words == 1) {
+    if (bytes == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
             if (4 * i < n) w[i] = *reinterpret_cast<const uint32_t*>(row + 4 * i);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < 16; ++i)
         if (i < n) w[i / 4] |= (uint32_t)row[i] << (8 * (i & 3));
 }
 
@@ -171,7 +167,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
     using C = Cfg<kPair, kNv>;
     constexpr int kCap = C::kCap, kSpan = kNv ? 16 : 32;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[3 * C::kStages + 4 + 2 * C::kTabs];
+    __shared__ uint64_t bars[2 * C::kStages + 8 + 2 * C::kTabs];
     __shared__ __align__(16) int token_row[C::kTabs][kCap];  // rows of q, or `none`
     __shared__ __align__(8) float token_scale[C::kTabs][kCap];
     __shared__ int first[kMaxExperts + 1];  // token tiles before each expert
@@ -187,23 +183,26 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
     const int none = max(a.rows, 1);              // a row past the map of q: zeros
     const int first_tile = blockIdx.x / C::kCtas, tile_step = gridDim.x / C::kCtas;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sf_base = base + C::kStages * C::kStage;
     const uint32_t bar0 = smem_u32(bars);
     // (of a pair the first CTA's are used)
-    auto landed = [&](int i) { return bar0 + 8u * i; };               // codes
-    auto scaled = [&](int i) { return bar0 + 8u * (C::kStages + i); };  // scales
-    auto empty = [&](int i) { return bar0 + 8u * (2 * C::kStages + i); };
-    auto d_full = [&](int i) { return bar0 + 8u * (3 * C::kStages + i); };
-    auto d_empty = [&](int i) { return bar0 + 8u * (3 * C::kStages + 2 + i); };
-    auto tab_full = [&](int i) { return bar0 + 8u * (3 * C::kStages + 4 + i); };
-    auto tab_empty = [&](int i) { return bar0 + 8u * (3 * C::kStages + 4 + C::kTabs + i); };
+    auto landed = [&](int i) { return bar0 + 8u * i; };                     // codes
+    auto empty = [&](int i) { return bar0 + 8u * (C::kStages + i); };
+    auto scaled = [&](int i) { return bar0 + 8u * (2 * C::kStages + i); };  // a batch of scales
+    auto sf_empty = [&](int i) { return bar0 + 8u * (2 * C::kStages + 2 + i); };
+    auto d_full = [&](int i) { return bar0 + 8u * (2 * C::kStages + 4 + i); };
+    auto d_empty = [&](int i) { return bar0 + 8u * (2 * C::kStages + 6 + i); };
+    auto tab_full = [&](int i) { return bar0 + 8u * (2 * C::kStages + 8 + i); };
+    auto tab_empty = [&](int i) { return bar0 + 8u * (2 * C::kStages + 8 + C::kTabs + i); };
     volatile int* abort = &abort_flag;
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(landed(i), C::kCtas);
-            mbar_init(scaled(i), C::kCtas * C::kSfWarps);
             mbar_init(empty(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(scaled(i), C::kCtas * C::kSfWarps);
+            mbar_init(sf_empty(i), 1);
             mbar_init(d_full(i), 1);
             mbar_init(d_empty(i), C::kCtas * C::kEpiWarps);
         }
@@ -342,7 +341,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
         // ------------------------------------------------------------- MMA --
         // (the first CTA of a pair issues for both)
         const uint32_t on = elect_lane();
-        int s = 0, n = 0;
+        int s = 0, n = 0, batch = 0;  // batch: of all so far
         uint32_t phase = 0;
         for (int t = first_tile; t < tiles && ok && rank == 0; t += tile_step, ++n) {
             // (the reduction's result is known to be uniform, a value from memory is not)
@@ -353,22 +352,24 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
             const uint32_t d = __reduce_max_sync(kAll, (uint32_t)(b * kCap));
             ok = __all_sync(kAll, wait_for<kPair>(d_empty(b), ((n >> 1) & 1) ^ 1, abort, a.wait_ns));
             tc_fence_after();
+            int unit = 0;  // of the batch
             for (int k = a.K; k > 0 && ok; k -= C::kUnit) {
-                ok = __all_sync(kAll, wait_for<kPair>(scaled(s), phase, abort, a.wait_ns) &&
-                                          wait_for<kPair>(landed(s), phase, abort, a.wait_ns));
+                if (unit == 0) ok = __all_sync(kAll, wait_for<kPair>(scaled(batch & 1), (batch >> 1) & 1, abort, a.wait_ns));
+                ok = ok && __all_sync(kAll, wait_for<kPair>(landed(s), phase, abort, a.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t st = base + __reduce_max_sync(kAll, (uint32_t)s) * C::kStage, sf = st + C::kABytes + C::kBBytes;
-                const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + C::kABytes);
+                const uint32_t st = base + __reduce_max_sync(kAll, (uint32_t)s) * C::kStage;
+                const uint32_t sf = sf_base + __reduce_max_sync(kAll, (uint32_t)((batch & 1) * C::kBatch + unit)) * C::kSfStride;
+                const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + C::kABytes), fd = desc_sf(sf);
                 const int steps = min(k + 63, 256) / 64;
 #pragma unroll
                 for (int j = 0; j < C::kWords; ++j) {
-                    copy_scales<kPair>(on, C::kSfCol + 4 * j, desc_sf(sf + 512 * j));
+                    copy_scales<kPair>(on, C::kSfCol + 4 * j, fd + 32 * j);
 #pragma unroll
                     for (int h = 0; h < C::kHalves; ++h)
                         if (h == 0 || cols > 128)
                             copy_scales<kPair>(on, C::kSfCol + C::kSfA + 4 * (j * C::kHalves + h),
-                                               desc_sf(sf + 512 * (C::kWords * (1 + h) + j)));
+                                               fd + 32 * (C::kWords * (1 + h) + j));
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -379,6 +380,11 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
                                         C::kSfCol + C::kSfA + 4 * word * C::kHalves, j > 0 || k != a.K);
                 }
                 mma_commit_by<kPair>(on, empty(s));
+                if (++unit == C::kBatch || k <= C::kUnit) {
+                    mma_commit_by<kPair>(on, sf_empty(batch & 1));
+                    ++batch;
+                    unit = 0;
+                }
                 if (++s == C::kStages) {
                     s = 0;
                     phase ^= 1;
@@ -388,79 +394,69 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
         }
     } else if (warp < C::kSfWarps) {
         // ---------------------------------------------------- block scales --
-        // thread: channel r of the tile and positions r, r + 128; lanes take rows so that the
-        // words of one store are adjacent
-        const int r = (lane & 3) * 32 + (lane >> 2) + 8 * warp;
-        const uint32_t at = base + C::kABytes + C::kBBytes + (r & 31) * 16 + (r >> 5) * 4;
+        // Four neighbouring lanes hold 64 bytes of one row, a batch: whole sectors, and stores
+        // that meet all banks once.  A warp's eight rows are r, r + 32, .. and r + 1, r + 33, ..
+        // of 128, four such eights a warp, of the channels and of each half of the positions.
+        constexpr int kParts = 1 + C::kHalves;
+        const int piece = lane & 3, r0 = ((lane >> 2) & 3) * 32 + (lane >> 4) + 2 * warp;
         const int blocks = a.K / kSpan;
         const uintptr_t low = (uintptr_t)a.s | (uintptr_t)a.ws | (uintptr_t)blocks;
-        const int words = low % 32 == 0 ? 8 : low % 4 == 0 ? 1 : 0;
-        // the loads run kAhead sectors ahead of the stores, over the ends of tiles
+        const int bytes = low % 16 == 0 ? 16 : low % 4 == 0 ? 4 : 1;
+        uint32_t v[kParts][4][4];
+        const uint8_t* rows[kParts][4];
         int at_t = first_tile, at_b = 0, at_n = 0;
-        const uint8_t* rows[1 + C::kHalves];
-        auto next_rows = [&]() {
-            if (at_t >= tiles) return;
-            const Tile w = tile_at(at_t);
-            const int tab = at_n % C::kTabs;
-            ok = __all_sync(kAll, wait_for<false>(tab_full(tab), (at_n / C::kTabs) & 1, abort, a.wait_ns));
-            if (!ok) return;
-            rows[0] = w.n0 + r < a.N ? a.ws + ((long long)w.e * a.N + w.n0 + r) * blocks : nullptr;
-#pragma unroll
-            for (int h = 0; h < C::kHalves; ++h) {
-                const int src = r + 128 * h < kCap ? token_row[tab][r + 128 * h] : none;
-                rows[1 + h] = src != none ? a.s + (long long)src * blocks : nullptr;
-            }
-            leave_tab(tab);
-        };
-        auto load = [&](uint32_t (&v)[1 + C::kHalves][8]) {
+        // the loads run a batch ahead of the stores, over the ends of tiles
+        auto load = [&]() {
             if (at_t >= tiles || !ok) return;
+            if (at_b == 0) {
+                const Tile w = tile_at(at_t);
+                const int tab = at_n % C::kTabs;
+                ok = __all_sync(kAll, wait_for<false>(tab_full(tab), (at_n / C::kTabs) & 1, abort, a.wait_ns));
+                if (!ok) return;
 #pragma unroll
-            for (int h = 0; h < 1 + C::kHalves; ++h) load_scales(v[h], rows[h], at_b, blocks, words);
-            at_b += 32;
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + 8 * i;
+                    rows[0][i] = w.n0 + r < a.N ? a.ws + ((long long)w.e * a.N + w.n0 + r) * blocks : nullptr;
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h) {
+                        const int src = r + 128 * h < kCap ? token_row[tab][r + 128 * h] : none;
+                        rows[1 + h][i] = src != none ? a.s + (long long)src * blocks : nullptr;
+                    }
+                }
+                leave_tab(tab);
+            }
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) load_scales(v[p][i], rows[p][i], at_b + 16 * piece, blocks, bytes);
+            at_b += 64;
             if (at_b >= blocks) {
                 at_b = 0;
                 at_t += tile_step;
                 ++at_n;
-                next_rows();
             }
         };
-        uint32_t v[C::kAhead][1 + C::kHalves][8];
-        next_rows();
+        load();
+        const int all = first_tile < tiles ? (tiles - first_tile + tile_step - 1) / tile_step * ((blocks + 63) / 64) : 0;
+        for (int batch = 0; batch < all && ok; ++batch) {
+            ok = __all_sync(kAll, wait_for<kPair>(sf_empty(batch & 1), ((batch >> 1) & 1) ^ 1, abort, a.wait_ns));
+            if (!ok) break;
+            const uint32_t to = sf_base + (batch & 1) * C::kBatch * C::kSfStride + (r0 & 31) * 16 + (r0 >> 5) * 4;
 #pragma unroll
-        for (int i = 0; i < C::kAhead; ++i) load(v[i]);
-        int s = 0, left = 0;  // left: K of this tile
-        uint32_t phase = 0;
-        const int sectors = (blocks + 31) / 32;
-        int all = first_tile < tiles ? (tiles - first_tile + tile_step - 1) / tile_step * sectors : 0;
-        while (all > 0 && ok) {
+            for (int p = 0; p < kParts; ++p)
 #pragma unroll
-            for (int i = 0; i < C::kAhead; ++i) {
-                if (all == 0 || !ok) break;
-                --all;
-                if (left <= 0) left = a.K;
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int u = 0; u < C::kSubs; ++u) {
-                    if (left <= 0 || !ok) break;
-                    left -= C::kUnit;
-                    ok = __all_sync(kAll, wait_for<kPair>(empty(s), phase ^ 1, abort, a.wait_ns));
-                    if (!ok) break;
-#pragma unroll
-                    for (int h = 0; h < 1 + C::kHalves; ++h)
-#pragma unroll
-                        for (int j = 0; j < C::kWords; ++j)
-                            st_shared4(at + s * C::kStage + 512 * (C::kWords * h + j), v[i][h][u * C::kWords + j]);
-                    fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (kPair) mbar_arrive_first(scaled(s)); else mbar_arrive(scaled(s));
+                    for (int j = 0; j < 4; ++j) {
+                        const int unit = piece * (4 / C::kWords) + j / C::kWords;
+                        st_shared4(to + unit * C::kSfStride + (p * C::kWords + j % C::kWords) * 512 + i * 128, v[p][i][j]);
                     }
-                    if (++s == C::kStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                }
-                load(v[i]);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                if (kPair) mbar_arrive_first(scaled(batch & 1)); else mbar_arrive(scaled(batch & 1));
             }
+            load();
         }
     } else {
         // -------------------------------------------------------- epilogue --
