@@ -22,8 +22,6 @@
 namespace moe {
 namespace {
 
-constexpr unsigned kAll = 0xFFFFFFFFu;
-
 // Sum over the block, the same in every thread; `part` is free again after the
 // next __syncthreads.
 __device__ __forceinline__ float block_sum(float v, float* part) {
@@ -53,8 +51,8 @@ struct Norm {
 // One block a row.  kKeep chunks of C elements a thread stay in registers from the
 // sum to the codes; kKeep = 0: rows of any length, read again for each pass (from h
 // where it is written: it may lie over an input).
-template <typename A, typename G, int C, int kKeep>
-__global__ void __launch_bounds__(1024) k_norm_rows(const Norm<A> a) {
+template <typename A, typename G, int C, int kKeep, int kMost>
+__global__ void __launch_bounds__(kMost, kMost == 256 ? 6 : 1) k_norm_rows(const Norm<A> a) {
     pdl_launch_dependents();
     pdl_wait();
     __shared__ float part[32];
@@ -74,34 +72,39 @@ __global__ void __launch_bounds__(1024) k_norm_rows(const Norm<A> a) {
             for (int c = first; c < H; c += step) f(held[0], c);
         }
     };
+    auto add = [&](Chunk<A, C>& v, const Chunk<A, C>& r) {
+        float f[C], g[C];
+        unpack_chunk(v, f);
+        unpack_chunk(r, g);
+#pragma unroll
+        for (int i = 0; i < C; ++i) f[i] += g[i];
+        v = pack_chunk<A, C>(f);
+    };
     float sum = 0.f;
     each([&](Chunk<A, C>& v, int c) {
         v = load_chunk<A, C>(x + c);
-        if (a.residual) {
-            const Chunk<A, C> r = load_chunk<A, C>(a.residual + t * a.rs + c);
-#pragma unroll
-            for (int i = 0; i < C; ++i) v.v[i] = from_f32<A>(to_f32(v.v[i]) + to_f32(r.v[i]));
-        }
+        if (a.residual) add(v, load_chunk<A, C>(a.residual + t * a.rs + c));
         if (a.h) *reinterpret_cast<Chunk<A, C>*>(a.h + t * a.hs + c) = v;
+        float f[C];
+        unpack_chunk(v, f);
 #pragma unroll
-        for (int i = 0; i < C; ++i) sum = fmaf(to_f32(v.v[i]), to_f32(v.v[i]), sum);
+        for (int i = 0; i < C; ++i) sum = fmaf(f[i], f[i], sum);
     });
     const float r = 1.f / sqrtf(block_sum(sum, part) / (float)H + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[t] = r;
     // y of a chunk of h, in place
     auto scaled = [&](Chunk<A, C>& v, int c) {
-        const Chunk<G, C> g = load_chunk<G, C>(gamma + c);
+        float f[C], g[C];
+        unpack_chunk(load_chunk<G, C>(gamma + c), g);
+        unpack_chunk(v, f);
 #pragma unroll
-        for (int i = 0; i < C; ++i) v.v[i] = from_f32<A>(to_f32(v.v[i]) * r * to_f32(g.v[i]));
+        for (int i = 0; i < C; ++i) f[i] = f[i] * r * g[i];
+        v = pack_chunk<A, C>(f);
     };
     const A* from = a.h ? a.h + t * a.hs : x;
     auto again = [&](Chunk<A, C>& v, int c) {  // kKeep = 0: h of the row once more
         v = load_chunk<A, C>(from + c);
-        if (a.residual && !a.h) {
-            const Chunk<A, C> e = load_chunk<A, C>(a.residual + t * a.rs + c);
-#pragma unroll
-            for (int i = 0; i < C; ++i) v.v[i] = from_f32<A>(to_f32(v.v[i]) + to_f32(e.v[i]));
-        }
+        if (a.residual && !a.h) add(v, load_chunk<A, C>(a.residual + t * a.rs + c));
     };
     uint32_t top = 0;
     each([&](Chunk<A, C>& v, int c) {
@@ -124,8 +127,7 @@ __global__ void __launch_bounds__(1024) k_norm_rows(const Norm<A> a) {
             }
         }
         float f[C];
-#pragma unroll
-        for (int i = 0; i < C; ++i) f[i] = to_f32(v.v[i]);
+        unpack_chunk(v, f);
         Chunk<int8_t, C> out = {};
         if (by.live) out = quant_codes(f, by.c127, by.m, by.by);
         *reinterpret_cast<Chunk<int8_t, C>*>(a.q + t * a.qs + c) = out;
@@ -147,23 +149,17 @@ struct NormBack {
 
 // A block walks rows t, t + gridDim.x, ... ; a thread's columns stay the same, so
 // its share of dgamma is summed in registers and written once.
-template <typename A, typename G, int C, int kKeep>
-__global__ void __launch_bounds__(1024) k_norm_backward(const NormBack<A> a) {
+template <typename A, typename G, int C, int kKeep, int kMost>
+__global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) k_norm_backward(const NormBack<A> a) {
     pdl_launch_dependents();
     pdl_wait();
     __shared__ float part[2][32];
     const int first = threadIdx.x * C, step = blockDim.x * C, H = a.H;
-    float gamma[kKeep][C], dgamma[kKeep][C];
+    Chunk<G, C> gamma[kKeep];
+    float dgamma[kKeep][C] = {};
 #pragma unroll
-    for (int n = 0; n < kKeep; ++n) {
-        Chunk<G, C> g = {};
-        if (first + n * step < H) g = load_chunk<G, C>(reinterpret_cast<const G*>(a.gamma) + first + n * step);
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            gamma[n][i] = to_f32(g.v[i]);
-            dgamma[n][i] = 0.f;
-        }
-    }
+    for (int n = 0; n < kKeep; ++n)
+        if (first + n * step < H) gamma[n] = load_chunk<G, C>(reinterpret_cast<const G*>(a.gamma) + first + n * step);
     int turn = 0;
     for (long long t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         Chunk<A, C> dy[kKeep], h[kKeep], dh[kKeep];
@@ -180,11 +176,15 @@ __global__ void __launch_bounds__(1024) k_norm_backward(const NormBack<A> a) {
 #pragma unroll
         for (int n = 0; n < kKeep; ++n)
             if (first + n * step < H) {
+                float v[C], w[C], g[C];
+                unpack_chunk(dy[n], v);
+                unpack_chunk(h[n], w);
+                unpack_chunk(gamma[n], g);
 #pragma unroll
                 for (int i = 0; i < C; ++i) {
-                    const float v = to_f32(dy[n].v[i]), w = to_f32(h[n].v[i]) * r;
-                    dot = fmaf(v * gamma[n][i], w, dot);
-                    dgamma[n][i] = fmaf(v, w, dgamma[n][i]);
+                    w[i] *= r;
+                    dot = fmaf(v[i] * g[i], w[i], dot);
+                    dgamma[n][i] = fmaf(v[i], w[i], dgamma[n][i]);
                 }
             }
         const float mean = block_sum(dot, part[turn]) / (float)H;  // of g h r
@@ -192,11 +192,16 @@ __global__ void __launch_bounds__(1024) k_norm_backward(const NormBack<A> a) {
         for (int n = 0; n < kKeep; ++n) {
             const int c = first + n * step;
             if (c >= H) continue;
-            float f[C];
+            float f[C], w[C], g[C];
+            unpack_chunk(dy[n], f);
+            unpack_chunk(h[n], w);
+            unpack_chunk(gamma[n], g);
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                f[i] = r * (to_f32(dy[n].v[i]) * gamma[n][i] - to_f32(h[n].v[i]) * r * mean);
-                if (a.dh) f[i] += to_f32(dh[n].v[i]);
+            for (int i = 0; i < C; ++i) f[i] = r * (f[i] * g[i] - w[i] * r * mean);
+            if (a.dh) {
+                unpack_chunk(dh[n], w);
+#pragma unroll
+                for (int i = 0; i < C; ++i) f[i] += w[i];
             }
             store_chunk<A, C>(a.dx + t * a.dxs + c, f);
         }
@@ -257,28 +262,37 @@ __global__ void __launch_bounds__(1024) k_join_parts(const float* part, int part
 }
 
 // ----------------------------------------------------------------- launches --
-constexpr int kParts = 608;  // blocks of the gradient at most, four an SM
+// Blocks of the gradient at most: three an SM of 256 threads, and more of the smaller ones
+// (8192 x 1024 bf16: 29 us with 456, 20 with 912; 8192 x 4096: 52 and 54).
+int most_parts(int H) { return H <= 2048 ? 912 : 456; }
 
-int threads_for(int chunks) { return chunks >= 1024 ? 1024 : (chunks + 31) / 32 * 32; }
+int threads_for(int chunks) { return (chunks + 31) / 32 * 32; }
 
+// Many rows: four chunks a thread, so that more rows are on an SM at once; few: more
+// threads for each.
 template <typename A, typename G, int C>
 cudaError_t norm_c(const Norm<A>& a, int T, cudaStream_t s) {
     const int chunks = (a.H + C - 1) / C;
-    if (chunks <= 512) return launch_pdl(k_norm_rows<A, G, C, 1>, dim3(T), dim3(threads_for(chunks)), 0, s, a);
-    if (chunks <= 2048) return launch_pdl(k_norm_rows<A, G, C, 4>, dim3(T), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
-    return launch_pdl(k_norm_rows<A, G, C, 0>, dim3(T), dim3(1024), 0, s, a);
+    if (chunks <= 128 || (chunks <= 512 && T < 608))
+        return launch_pdl(k_norm_rows<A, G, C, 1, 512>, dim3(T), dim3(threads_for(chunks)), 0, s, a);
+    if (chunks <= 1024) return launch_pdl(k_norm_rows<A, G, C, 4, 256>, dim3(T), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
+    if (chunks <= 4096) return launch_pdl(k_norm_rows<A, G, C, 4, 1024>, dim3(T), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
+    return launch_pdl(k_norm_rows<A, G, C, 0, 1024>, dim3(T), dim3(1024), 0, s, a);
 }
 
 template <typename A, typename G, int C>
 cudaError_t back_c(const NormBack<A>& a, float* dgamma, cudaStream_t s) {
     const int chunks = (a.H + C - 1) / C;
-    int parts = a.T < kParts ? a.T : kParts;
+    const int most = most_parts(a.H);
+    int parts = a.T < most ? a.T : most;
     cudaError_t e = cudaSuccess;
     if (a.T == 0) {
-    } else if (chunks <= 4096) {
-        if (chunks <= 256) e = launch_pdl(k_norm_backward<A, G, C, 1>, dim3(parts), dim3(threads_for(chunks)), 0, s, a);
-        else if (chunks <= 512) e = launch_pdl(k_norm_backward<A, G, C, 2>, dim3(parts), dim3(threads_for((chunks + 1) / 2)), 0, s, a);
-        else e = launch_pdl(k_norm_backward<A, G, C, 4>, dim3(parts), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
+    } else if (chunks <= 2048) {
+        const dim3 grid(parts);
+        if (chunks <= 256) e = launch_pdl(k_norm_backward<A, G, C, 1, 256>, grid, dim3(threads_for(chunks)), 0, s, a);
+        else if (chunks <= 512) e = launch_pdl(k_norm_backward<A, G, C, 2, 256>, grid, dim3(threads_for((chunks + 1) / 2)), 0, s, a);
+        else if (chunks <= 1024) e = launch_pdl(k_norm_backward<A, G, C, 2, 512>, grid, dim3(threads_for((chunks + 1) / 2)), 0, s, a);
+        else e = launch_pdl(k_norm_backward<A, G, C, 4, 512>, grid, dim3(threads_for((chunks + 3) / 4)), 0, s, a);
     } else {
         e = launch_pdl(k_norm_backward_long<A, G>, dim3(a.T), dim3(1024), 0, s, a);
         parts = parts < 16 ? parts : 16;
@@ -380,7 +394,8 @@ extern "C" moe_status moe_norm_rows(const void* x, moe_dtype dtype, long long x_
 
 extern "C" size_t moe_norm_scratch_bytes(int T, int hidden) {
     if (T < 0 || T > (1 << 24) || hidden < 1 || hidden > 131072) return 0;
-    return (size_t)(T < 1 ? 1 : T < kParts ? T : kParts) * hidden * sizeof(float);
+    const int most = most_parts(hidden);
+    return (size_t)(T < 1 ? 1 : T < most ? T : most) * hidden * sizeof(float);
 }
 
 extern "C" moe_status moe_norm_rows_backward(const void* dy, moe_dtype dtype, long long dy_stride, const void* dh,

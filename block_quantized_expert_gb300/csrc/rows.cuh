@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
@@ -28,12 +30,51 @@ __device__ __forceinline__ Chunk<T, C> load_chunk(const T* p) {
     return *reinterpret_cast<const Chunk<T, C>*>(p);
 }
 
+// 16-bit types two at a time, in one conversion.
+template <typename T, int C>
+__device__ __forceinline__ Chunk<T, C> pack_chunk(const float (&f)[C]) {
+    Chunk<T, C> c;
+    if constexpr (sizeof(T) == 2 && C % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < C; i += 2) {
+            if constexpr (std::is_same<T, __half>::value)
+                *reinterpret_cast<__half2*>(&c.v[i]) = __floats2half2_rn(f[i], f[i + 1]);
+            else
+                *reinterpret_cast<__nv_bfloat162*>(&c.v[i]) = __floats2bfloat162_rn(f[i], f[i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) c.v[i] = from_f32<T>(f[i]);
+    }
+    return c;
+}
+
+// The other way: 16-bit types by words (as single elements the compiler gives each bf16 a
+// register of its own).
+template <typename T, int C>
+__device__ __forceinline__ void unpack_chunk(const Chunk<T, C>& c, float (&f)[C]) {
+    if constexpr (sizeof(T) == 2 && C % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < C; i += 2) {
+            if constexpr (std::is_same<T, __half>::value) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&c.v[i]));
+                f[i] = v.x;
+                f[i + 1] = v.y;
+            } else {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(&c.v[i]);
+                f[i] = __uint_as_float(w << 16);
+                f[i + 1] = __uint_as_float(w & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) f[i] = to_f32(c.v[i]);
+    }
+}
+
 template <typename T, int C>
 __device__ __forceinline__ void store_chunk(T* p, const float (&f)[C]) {
-    Chunk<T, C> c;
-#pragma unroll
-    for (int i = 0; i < C; ++i) c.v[i] = from_f32<T>(f[i]);
-    *reinterpret_cast<Chunk<T, C>*>(p) = c;
+    *reinterpret_cast<Chunk<T, C>*>(p) = pack_chunk<T, C>(f);
 }
 
 inline int dtype_size(moe_dtype d) { return d == MOE_F32 ? 4 : 2; }
