@@ -617,6 +617,20 @@ def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, t
         _check(st)
 
 
+def _device_of(t) -> int:
+    """The tensor's device if it is the current one, else -1."""
+    dev = t.get_device()
+    return dev if dev >= 0 and dev == torch._C._cuda_getDevice() else -1
+
+
+def _dense(dev, t, dtype, shape) -> int:
+    """The pointer of a dense tensor of this type and shape on the device `dev`, else 0: what
+    calls look for first, in as few steps as it takes.  0 is for the checks that can say why."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    return 0
+
+
 def _same_rows(t, name, dt, T, H):
     """_rows of an optional operand: (None, 0) without it."""
     if t is None:
@@ -638,9 +652,27 @@ def moe_norm_rows(x, gamma, y, eps: float = 1e-6, residual=None, h=None, rstd=No
     """h = x + residual, rstd = 1 / sqrt(mean h^2 + eps) [T], y = h * rstd * gamma, and y as int8
     codes q with one float32 scale a row.  x, residual, h, y [T][H] in one floating dtype, gamma
     [H] in it or float32; without a residual h = x; y may be None where q is given."""
-    T, H = x.shape
+    T, H = shape = x.shape
     if T == 0:
         return
+    dt = _ROW_TYPES.get(x.dtype)
+    dev = _device_of(x)
+    if stream is None and dt is not None and dev >= 0:
+        d, f = x.dtype, torch.float32
+        g = gamma.dtype
+        p = [_dense(dev, x, d, shape), _dense(dev, gamma, g, (H,)) if g is f or g is d else 0]
+        for t in (residual, h, y):
+            p.append(None if t is None else _dense(dev, t, d, shape))
+        p.append(None if rstd is None else _dense(dev, rstd, f, (T,)))
+        p.append(None if q is None else _dense(dev, q, torch.int8, shape))
+        p.append(None if scale is None else _dense(dev, scale, f, (T,)))
+        if 0 not in p:
+            st = (_lib or load_library()).moe_norm_rows(
+                p[0], dt, H, p[2], H, p[1], MOE_F32 if g is f else dt, T, H, eps, p[3], H, p[4], H, p[5], p[6], H, p[7],
+                torch._C._cuda_getCurrentRawStream(dev))
+            if st:
+                _check(st)
+            return
     px, dt, sx = _rows(x, "x")
     pr, sr = _same_rows(residual, "residual", dt, T, H)
     ph, sh = _same_rows(h, "h", dt, T, H)
@@ -671,7 +703,26 @@ def moe_norm_rows_backward(dy, h, gamma, rstd, dx, dgamma=None, scratch=None, dh
     """dx [T][H] (of x and of the residual alike) and dgamma [H] in float32 from dy and, where the
     residual stream goes on, dh; h and rstd as moe_norm_rows gave them.  dgamma needs scratch, a
     CUDA uint8 tensor of moe_norm_scratch_bytes."""
-    T, H = h.shape
+    T, H = shape = h.shape
+    dt = _ROW_TYPES.get(h.dtype)
+    dev = _device_of(h)
+    if stream is None and dt is not None and T and dev >= 0:
+        d, f = h.dtype, torch.float32
+        g = gamma.dtype
+        p = [_dense(dev, dy, d, shape), _dense(dev, h, d, shape), _dense(dev, dx, d, shape), _dense(dev, rstd, f, (T,)),
+             _dense(dev, gamma, g, (H,)) if g is f or g is d else 0, None if dh is None else _dense(dev, dh, d, shape),
+             None if dgamma is None else _dense(dev, dgamma, f, (H,)), None]
+        n = 0
+        if scratch is not None:
+            n = scratch.numel()
+            p[7] = _dense(dev, scratch, torch.uint8, scratch.shape)
+        if 0 not in p:
+            st = (_lib or load_library()).moe_norm_rows_backward(
+                p[0], dt, H, p[5], H, p[1], H, p[4], MOE_F32 if g is f else dt, p[3], T, H, p[2], H, p[6], p[7], n,
+                torch._C._cuda_getCurrentRawStream(dev))
+            if st:
+                _check(st)
+            return
     ph, dt, sh = _rows(h, "h")
     if dt is None:
         raise ValueError("h must be a floating tensor")
@@ -717,6 +768,20 @@ def moe_quantize_blocks(x, q, s, scale=None, fmt: int = MOE_WEIGHTS_NVFP4, gated
     4-bit codes q [rows][K / 2], two a byte, with scale bytes s [rows][K / 16] and a float32
     scale a row (NVFP4; `given`: read, not written) or s [rows][K / 32] and no scale (MXFP4)."""
     n = _block(fmt)
+    rows, half = shape = q.shape if q.dim() == 2 else (0, 0)
+    dt = _ROW_TYPES.get(x.dtype)
+    dev = _device_of(x)
+    if stream is None and dt is not None and rows and dev >= 0:
+        K = 2 * half
+        width = 2 * K if gated else K
+        p = [_dense(dev, x, x.dtype, (rows, width)), _dense(dev, q, torch.uint8, shape),
+             _dense(dev, s, torch.uint8, (rows, K // n)), None if scale is None else _dense(dev, scale, torch.float32, (rows,))]
+        if 0 not in p:
+            st = (_lib or load_library()).moe_quantize_blocks(p[0], dt, width, 1 if gated else 0, rows, K, fmt, p[1], half, p[2],
+                                                              p[3], 1 if given else 0, torch._C._cuda_getCurrentRawStream(dev))
+            if st:
+                _check(st)
+            return
     pq, sq, rows, K = _codes(q, "q")
     if rows == 0:
         return
@@ -735,6 +800,19 @@ def moe_quantize_blocks(x, q, s, scale=None, fmt: int = MOE_WEIGHTS_NVFP4, gated
 def moe_dequantize_blocks(q, s, x, scale=None, fmt: int = MOE_WEIGHTS_NVFP4, stream=None):
     """Blocks of 4-bit codes (moe_quantize_blocks) back to rows x [rows][K]."""
     n = _block(fmt)
+    rows, half = shape = q.shape if q.dim() == 2 else (0, 0)
+    dt = _ROW_TYPES.get(x.dtype)
+    dev = _device_of(x)
+    if stream is None and dt is not None and rows and dev >= 0:
+        K = 2 * half
+        p = [_dense(dev, x, x.dtype, (rows, K)), _dense(dev, q, torch.uint8, shape), _dense(dev, s, torch.uint8, (rows, K // n)),
+             None if scale is None else _dense(dev, scale, torch.float32, (rows,))]
+        if 0 not in p:
+            st = (_lib or load_library()).moe_dequantize_blocks(p[1], half, p[2], p[3], rows, K, fmt, p[0], dt, K,
+                                                                torch._C._cuda_getCurrentRawStream(dev))
+            if st:
+                _check(st)
+            return
     pq, sq, rows, K = _codes(q, "q")
     if rows == 0:
         return
@@ -763,6 +841,22 @@ def moe_block_product(q, s, wq, ws, out, offsets=None, row_src=None, top_k: int 
         raise ValueError(f"wq must have shape (E, N, K / 2), got {tuple(wq.shape)}")
     E, _, half = wq.shape
     K = 2 * half
+    dt = _ROW_TYPES.get(out.dtype)
+    dev = _device_of(out)
+    if stream is None and dt is not None and dev >= 0:
+        u, f, i = torch.uint8, torch.float32, torch.int32
+        rows = q.shape[0]
+        p = [_dense(dev, q, u, (rows, half)), _dense(dev, s, u, (rows, K // n)), _dense(dev, wq, u, (E, N, half)),
+             _dense(dev, ws, u, (E, N, K // n)), _dense(dev, out, out.dtype, (R, N)),
+             None if scale is None else _dense(dev, scale, f, (rows,)), None if w_scale is None else _dense(dev, w_scale, f, (E, N)),
+             None if offsets is None else _dense(dev, offsets, i, (E + 1,)), None if row_src is None else _dense(dev, row_src, i, (R,))]
+        if 0 not in p:
+            st = (_lib or load_library()).moe_block_product(
+                p[0], half, rows, p[1], p[5], K, fmt, p[2], p[3], p[6], E, N, p[7], p[8], top_k, R, p[4], dt, N,
+                torch._C._cuda_getCurrentRawStream(dev))
+            if st:
+                _check(st)
+            return
     pq, sq, rows, _ = _codes(q, "q", q.shape[0], K)
     po, dto, so = _rows(out, "out")
     if dto is None:

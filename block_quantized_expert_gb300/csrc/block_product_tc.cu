@@ -140,7 +140,7 @@ __device__ uint32_t g_block_seen;  // what the check under way has taken
 __global__ void k_take_block_flag() { g_block_seen = atomicExch(&g_block_err, 0u); }
 
 // 16 scale bytes of one row from byte `at` on, zeros from byte `all` on: no row (nullptr)
-// is all zeros.  bytes: 16 or 4 where every row's pieces of that size are whole and aligned.
+// is all zeros.  bytes: 16, 4 or 2 where every row's pieces of that size are whole and aligned.
 __device__ __forceinline__ void load_scales(uint32_t (&w)[4], const uint8_t* row, int at, int all, int bytes) {
     w[0] = w[1] = w[2] = w[3] = 0;
     if (row == nullptr || at >= all) return;
@@ -154,6 +154,12 @@ __device__ __forceinline__ void load_scales(uint32_t (&w)[4], const uint8_t* row
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (4 * i < n) w[i] = *reinterpret_cast<const uint32_t*>(row + 4 * i);
+        return;
+    }
+    if (bytes == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (2 * i < n) w[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(row + 2 * i) << (16 * (i & 1));
         return;
     }
 #pragma unroll
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
         const int piece = lane & 3, r0 = ((lane >> 2) & 3) * 32 + (lane >> 4) + 2 * warp;
         const int blocks = a.K / kSpan;
         const uintptr_t low = (uintptr_t)a.s | (uintptr_t)a.ws | (uintptr_t)blocks;
-        const int bytes = low % 16 == 0 ? 16 : low % 4 == 0 ? 4 : 1;
+        const int bytes = low % 16 == 0 ? 16 : low % 4 == 0 ? 4 : low % 2 == 0 ? 2 : 1;
         uint32_t v[kParts][4][4];
         const uint8_t* rows[kParts][4];
         int at_t = first_tile, at_b = 0, at_n = 0;
@@ -603,11 +609,24 @@ cudaError_t launch_o(const BlockProduct& a, const CUtensorMap& wmap, const CUten
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
+    // Narrow or wide tiles, by rounds over the GPU times what a round takes, in us.  A segment
+    // of m positions has about m / cap + 1/2 tiles (those of the dense product are known) and at
+    // least one; it is taken as equal to the others, for the segments are on the device.
+    // Measured at K = 4096, narrow and wide: 256 rows of one expert 11.3 and 13.8, 512 17.8 and
+    // 15.9, 1024 31 and 23; at K = 2048 and 256 experts of 32 rows 209 and 225, of 48 226 and 231,
+    // of 64 316 and 234; 777 rows at K = 1120, N = 1001 9.8 and 16.1.
     const double segs = a.E < a.R ? a.E : a.R;
+    auto cost = [&](int cap, int channels, int at_once, double fixed, double base, double a_row) {
+        const double mean = a.R / segs, each = a.E == 1 ? (a.R + cap - 1) / cap : mean / cap + 0.5;
+        const double n = each > 1 ? each : 1;
+        const double rounds = std::ceil(segs * n * ((a.N + channels - 1) / channels) / at_once);
+        return fixed + rounds * (base + a_row * mean / n) * a.K / 4096;
+    };
     auto most = [&](int cap, int channels) {  // tiles
         return (a.R / cap + (long long)segs) * ((a.N + channels - 1) / channels);
     };
-    if (a.R > 48 * segs) return launch_kind<true, kNv, O>(a, most(Cfg<true, kNv>::kCap, 256), dev, wmap, qmap, s);
+    if (cost(Cfg<true, kNv>::kCap, 256, sms / 2, 5.8, 7.4, 0.01) < cost(Cfg<false, kNv>::kCap, 128, sms, 4.3, 6.6, 0))
+        return launch_kind<true, kNv, O>(a, most(Cfg<true, kNv>::kCap, 256), dev, wmap, qmap, s);
     return launch_kind<false, kNv, O>(a, most(Cfg<false, kNv>::kCap, 128), dev, wmap, qmap, s);
 }
 
