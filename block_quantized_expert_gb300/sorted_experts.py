@@ -1,5 +1,6 @@
-"""Experts of the caller's own around the sorted-row operators: a served expert
-layer with 8-bit integer weights, and the pieces of a training step.
+"""Experts of the caller's own around the sorted-row operators: served expert
+layers with 8-bit integer weights or weights in 4-bit blocks, the norm in front of
+them, and the pieces of a training step.
 
 The layer of moe_create holds 4-bit experts and only runs forward.  This module
 is the same path (route, sort, SwiGLU experts, combine: "DeepSeek-V4-Flash 284B -
@@ -10,9 +11,14 @@ hold:
   five operators: moe_quantize_rows on the tokens, moe_expert_product (gate and
   up in one, each sorted position gathering its token), moe_quantize_rows with the
   gate, moe_expert_product (down), moe_combine.
-* dispatch, combine and router_weights: differentiable forms of moe_dispatch,
-  moe_combine and the router's weights, for products that run in between.  They
-  are differentiable once: a gradient of their gradient raises.
+* BlockExperts: weights in blocks of 4 bits (MXFP4 or NVFP4), tokens in the same
+  blocks: moe_quantize_blocks, moe_block_product, and the same for the down product.
+  quantize_layer_weights makes the blocks that moe_create takes.
+* norm_codes: the norm in front of Int8Experts with the residual's addition, the rows
+  for the router and the codes for the experts in one pass.
+* norm, dispatch, combine and router_weights: differentiable forms of moe_norm_rows,
+  moe_dispatch, moe_combine and the router's weights, for products that run in between.
+  They are differentiable once: a gradient of their gradient raises.
 
     python -m block_quantized_expert_gb300.sorted_experts
 
@@ -76,26 +82,148 @@ class Int8Experts:
         self.gate_up, self.gate_up_scale = quantize_weights(torch.cat([gate, up], dim=1))
         self.down, self.down_scale = quantize_weights(down)
 
-    def __call__(self, x: torch.Tensor, s: Sorted, w: torch.Tensor) -> torch.Tensor:
+    def __call__(self, x: torch.Tensor, s: Sorted, w: torch.Tensor, codes=None) -> torch.Tensor:
         """x [T][H] in bf16, fp16 or fp32; w [T][k] the routing weights; fp32 [T][H].
+        codes: (q, scale) of x where they are there already (norm_codes).
 
         Asynchronous: whether a device-side wait of the products ran out, which leaves
         the output undefined, is what moe_check_product tells, and the caller asks it."""
         T, k = w.shape
         R, dev = T * k, x.device
-        q = torch.empty((T, self.H), dtype=torch.int8, device=dev)
-        scale = torch.empty(T, dtype=torch.float32, device=dev)
+        if codes is None:
+            codes = (torch.empty((T, self.H), dtype=torch.int8, device=dev), torch.empty(T, dtype=torch.float32, device=dev))
+            bqe.moe_quantize_rows(x, *codes)
+        q, scale = codes
         gu = torch.empty((R, 2 * self.I), dtype=self.rows, device=dev)
         h = torch.empty((R, self.I), dtype=torch.int8, device=dev)
         h_scale = torch.empty(R, dtype=torch.float32, device=dev)
         y = torch.empty((R, self.H), dtype=self.rows, device=dev)
         out = torch.empty((T, self.H), dtype=torch.float32, device=dev)
-        bqe.moe_quantize_rows(x, q, scale)
         bqe.moe_expert_product(q, scale, self.gate_up, self.gate_up_scale, gu, s.offsets, s.row_src, k)
         bqe.moe_quantize_rows(gu, h, h_scale, gated=True)
         bqe.moe_expert_product(h, h_scale, self.down, self.down_scale, y, s.offsets)
         bqe.moe_combine(y, w, s.row_dst, out)
         return out
+
+
+def quantize_block_weights(w: torch.Tensor, fmt: int = bqe.MOE_WEIGHTS_NVFP4):
+    """[E][N][K] weights to blocks of 4 bits: codes [E][N][K / 2], scale bytes [E][N][K / 16 or
+    K / 32] and, for NVFP4, one float32 scale an output channel [E][N], else None."""
+    E, N, K = w.shape
+    q = torch.empty((E, N, K // 2), dtype=torch.uint8, device=w.device)
+    s = torch.empty((E, N, K // (16 if fmt == bqe.MOE_WEIGHTS_NVFP4 else 32)), dtype=torch.uint8, device=w.device)
+    scale = torch.empty((E, N), dtype=torch.float32, device=w.device) if fmt == bqe.MOE_WEIGHTS_NVFP4 else None
+    bqe.moe_quantize_blocks(w.reshape(E * N, K), q.view(E * N, -1), s.view(E * N, -1),
+                            None if scale is None else scale.view(E * N), fmt)
+    return q, s, scale
+
+
+def quantize_layer_weights(w: torch.Tensor, fmt: int = bqe.MOE_WEIGHTS_MXFP4):
+    """[E][N][K] weights to the tensors that moe_create takes for one of its matrices: codes,
+    scale bytes and, for NVFP4, one float32 scale a matrix [E] (max|w| / 2688), else None."""
+    if fmt != bqe.MOE_WEIGHTS_NVFP4:
+        return quantize_block_weights(w, fmt)
+    E, N, K = w.shape
+    most = w.abs().amax((1, 2)).float()
+    g = torch.where(most > 0, most / torch.full_like(most, 2688.0), 1.0)  # a quotient, not a product with 1 / 2688
+    q = torch.empty((E, N, K // 2), dtype=torch.uint8, device=w.device)
+    s = torch.empty((E, N, K // 16), dtype=torch.uint8, device=w.device)
+    bqe.moe_quantize_blocks(w.reshape(E * N, K), q.view(E * N, -1), s.view(E * N, -1), g.repeat_interleave(N), fmt, given=True)
+    return q, s, g
+
+
+class BlockExperts:
+    """SwiGLU experts in blocks of 4 bits: gate and up [E][I][H], down [E][H][I], H and I
+    multiples of 32.  The tokens and the gated rows are quantised to the same blocks.
+    `rows`: the type of the rows between the products, as in Int8Experts; bf16's rounding is
+    far below a 4-bit code's half step."""
+
+    def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, fmt: int = bqe.MOE_WEIGHTS_NVFP4,
+                 rows: torch.dtype = torch.bfloat16):
+        if rows not in (torch.float32, torch.bfloat16, torch.float16):
+            raise ValueError(f"rows must be float32, bfloat16 or float16, got {rows}")
+        self.rows, self.fmt = rows, fmt
+        self.E, self.I, self.H = gate.shape
+        self.gate_up = quantize_block_weights(torch.cat([gate, up], dim=1), fmt)
+        self.down = quantize_block_weights(down, fmt)
+
+    def blocks(self, x: torch.Tensor, gated: bool = False):
+        """Rows to blocks: codes, scale bytes and the rows' scales (NVFP4) or None."""
+        rows, K = x.shape[0], x.shape[1] // (2 if gated else 1)
+        nv = self.fmt == bqe.MOE_WEIGHTS_NVFP4
+        q = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+        s = torch.empty((rows, K // (16 if nv else 32)), dtype=torch.uint8, device=x.device)
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device) if nv else None
+        bqe.moe_quantize_blocks(x, q, s, scale, self.fmt, gated=gated)
+        return q, s, scale
+
+    def __call__(self, x: torch.Tensor, s: Sorted, w: torch.Tensor) -> torch.Tensor:
+        """x [T][H] in bf16, fp16 or fp32; w [T][k] the routing weights; fp32 [T][H].
+        Asynchronous, as Int8Experts is: moe_check_product is its caller's."""
+        T, k = w.shape
+        R, dev = T * k, x.device
+        gu = torch.empty((R, 2 * self.I), dtype=self.rows, device=dev)
+        y = torch.empty((R, self.H), dtype=self.rows, device=dev)
+        out = torch.empty((T, self.H), dtype=torch.float32, device=dev)
+        q, sb, scale = self.blocks(x)
+        wq, ws, w_scale = self.gate_up
+        bqe.moe_block_product(q, sb, wq, ws, gu, s.offsets, s.row_src, k, scale, w_scale, self.fmt)
+        q, sb, scale = self.blocks(gu, gated=True)
+        wq, ws, w_scale = self.down
+        bqe.moe_block_product(q, sb, wq, ws, y, s.offsets, None, 1, scale, w_scale, self.fmt)
+        bqe.moe_combine(y, w, s.row_dst, out)
+        return out
+
+
+def norm_codes(x: torch.Tensor, gamma: torch.Tensor, residual=None, eps: float = 1e-6):
+    """(y, h, (q, scale)): the norm of h = x + residual for a router, the residual stream to go
+    on with (x itself without a residual), and y's 8-bit codes for Int8Experts."""
+    T, H = x.shape
+    h = x if residual is None else torch.empty_like(x)
+    y = torch.empty_like(x)
+    q = torch.empty((T, H), dtype=torch.int8, device=x.device)
+    scale = torch.empty(T, dtype=torch.float32, device=x.device)
+    bqe.moe_norm_rows(x, gamma, y, eps, residual, None if residual is None else h, None, q, scale)
+    return y, h, (q, scale)
+
+
+class _Norm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, gamma, eps):
+        h = x if residual is None else torch.empty_like(x)
+        y = torch.empty_like(x)
+        rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        bqe.moe_norm_rows(x, gamma, y, eps, residual, None if residual is None else h, rstd)
+        ctx.save_for_backward(h, gamma, rstd)
+        ctx.set_materialize_grads(False)
+        return y if residual is None else (y, h)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, gamma, rstd = ctx.saved_tensors
+        T, H = h.shape
+        if dy is None:
+            return dh, dh, None, None
+        dx = torch.empty_like(h)
+        dgamma = scratch = None
+        if ctx.needs_input_grad[2]:
+            dgamma = torch.empty(H, dtype=torch.float32, device=h.device)
+            scratch = torch.empty(bqe.moe_norm_scratch_bytes(T, H), dtype=torch.uint8, device=h.device)
+        bqe.moe_norm_rows_backward(dy.contiguous(), h, gamma, rstd, dx, dgamma, scratch,
+                                   None if dh is None else dh.contiguous())
+        return dx, dx if ctx.needs_input_grad[1] else None, None if dgamma is None else dgamma.to(gamma.dtype), None
+
+
+def norm(x: torch.Tensor, gamma: torch.Tensor, residual=None, eps: float = 1e-6):
+    """(y, h) of [T][H] rows: h = x + residual (x itself without one) and its root-mean-square
+    norm y; differentiable in x, residual and gamma, through y and through h."""
+    for name, t in (("x", x), ("residual", residual)):
+        if t is not None and (t.dim() != 2 or t.dtype != x.dtype or t.shape != x.shape):
+            raise ValueError(f"{name} must be 2-D rows of x's shape and dtype, got {t.dtype} {tuple(t.shape)}")
+    if residual is None:
+        return _Norm.apply(x.contiguous(), None, gamma.contiguous(), eps), x
+    return _Norm.apply(x.contiguous(), residual.contiguous(), gamma.contiguous(), eps)
 
 
 class _Dispatch(torch.autograd.Function):
@@ -207,18 +335,28 @@ def _example() -> None:
     got = Int8Experts(gate, up, down)(x, s, router_weights(logits, ids))
     bqe.moe_check_product()
     print("8-bit experts: relative L2 distance from fp32 experts %.2e" % ((got - want).norm() / want.norm()).item())
+    for name, fmt in (("MXFP4", bqe.MOE_WEIGHTS_MXFP4), ("NVFP4", bqe.MOE_WEIGHTS_NVFP4)):
+        got = BlockExperts(gate, up, down, fmt)(x, s, router_weights(logits, ids))
+        bqe.moe_check_product()
+        print("%s experts: relative L2 distance from fp32 experts %.2e" % (name, ((got - want).norm() / want.norm()).item()))
 
-    leaves = [t.clone().requires_grad_() for t in (x, gate, up, down, logits)]
-    plain(*leaves).square().sum().backward()
-    mine = [t.clone().requires_grad_() for t in (x, gate, up, down, logits)]
-    xs, rows = dispatch(mine[0], s), []
+    gamma, stream = 0.5 + torch.rand(H, device=dev), torch.randn(T, H, device=dev)
+
+    def block(x, gate, up, down, logits, gamma):
+        h = x + stream
+        return h + plain(h * (h.square().mean(1, keepdim=True) + 1e-6).rsqrt() * gamma, gate, up, down, logits)
+
+    leaves = [t.clone().requires_grad_() for t in (x, gate, up, down, logits, gamma)]
+    block(*leaves).square().sum().backward()
+    mine = [t.clone().requires_grad_() for t in (x, gate, up, down, logits, gamma)]
+    y, h = norm(mine[0], mine[5], stream)
+    xs, rows = dispatch(y, s), []
     ends = s.offsets.tolist()
     for e in range(E):
         r = xs[ends[e]:ends[e + 1]]
-        h = torch.nn.functional.silu(r @ mine[1][e].T) * (r @ mine[2][e].T)
-        rows.append(h @ mine[3][e].T)
-    combine(torch.cat(rows), router_weights(mine[4], ids), s).square().sum().backward()
-    for name, a, b in zip(("x", "gate", "up", "down", "logits"), mine, leaves):
+        rows.append((torch.nn.functional.silu(r @ mine[1][e].T) * (r @ mine[2][e].T)) @ mine[3][e].T)
+    (h + combine(torch.cat(rows), router_weights(mine[4], ids), s)).square().sum().backward()
+    for name, a, b in zip(("x", "gate", "up", "down", "logits", "gamma"), mine, leaves):
         print("training step: d%-6s relative L2 distance %.2e" % (name, ((a.grad - b.grad).norm() / b.grad.norm()).item()))
 
 
