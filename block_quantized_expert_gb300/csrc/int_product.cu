@@ -197,16 +197,19 @@ __global__ void __launch_bounds__(128) k_product_few(const Product a) {
 // 64 channels, 64 bytes of K at a time through shared memory, 4 x 4 sums a thread
 // by __dp4a (exact 32-bit integers): 8192 rows, K = N = 1000, 166 us (bound by the
 // issue of loads and sums, 0.1 PFLOP/s).  kWords: K, stride and bases allow four codes a
-// load, else they come one by one (777 rows, K = 1101, N = 1001: 78 us for 35 at K = 1100).
+// load, else they are shifted together from two (as single bytes 777 rows at K = 1101, N = 1001
+// took 78 us for 35 at K = 1100).
 template <bool kWords>
 __device__ __forceinline__ int codes4(const int8_t* row, int c, int K) {
     if (row == nullptr || c >= K) return 0;
     if (kWords) return *reinterpret_cast<const int*>(row + c);
-    uint32_t v = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (c + i < K) v |= (uint32_t)(uint8_t)row[c + i] << (8 * i);
-    return (int)v;
+    // the one or two aligned words that hold them, and no word without one of them
+    const int8_t* p = row + c;
+    const int off = (int)((uintptr_t)p & 3), n = K - c;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p - off);
+    const uint32_t lo = w[0], hi = off && n > 4 - off ? w[1] : 0u;
+    const uint32_t v = __funnelshift_r(lo, hi, 8 * off);
+    return (int)(n < 4 ? v & ((1u << (8 * n)) - 1u) : v);
 }
 
 template <typename O, bool kWords>
