@@ -183,6 +183,7 @@ extern "C" moe_status moe_block_product(const uint8_t* q, long long q_stride, in
     if (!offsets && n_experts != 1) return refuse(MOE_ERR_INVALID_ARG, "%s: several experts need offsets", what);
     if (q_stride < K / 2 || out_stride < N || q_stride > kMostStride || out_stride > kMostStride)
         return refuse(MOE_ERR_INVALID_ARG, "%s: a row stride is below the row or above 2^40", what);
+    if (q_stride >= kMostStride) return refuse(MOE_ERR_INVALID_ARG, "%s: q_stride must be below 2^40", what);
     if (q_stride % 16 != 0) return refuse(MOE_ERR_INVALID_ARG, "%s: q_stride must be a multiple of 16", what);
     if (R == 0) return MOE_OK;
     if (!q || !s || !wq || !ws || !out) return refuse(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);

@@ -340,7 +340,9 @@ __global__ void __launch_bounds__(1024) k_join_parts(const float* part, int part
 // ----------------------------------------------------------------- launches --
 // Blocks of the gradient at most: three an SM of 256 threads, and more of the smaller ones
 // (8192 x 1024 bf16: 29 us with 456, 20 with 912; 8192 x 4096: 52 and 54).
-int most_parts(int H) { return H <= 2048 ? 912 : 456; }
+// Rows past 16384 are long whatever their type.
+constexpr int kLongParts = 16;
+int most_parts(int H) { return H <= 2048 ? 912 : H <= 16384 ? 456 : kLongParts; }
 
 int threads_for(int chunks) { return (chunks + 31) / 32 * 32; }
 
@@ -382,9 +384,10 @@ cudaError_t back_c(const NormBack<A>& a, float* dgamma, cudaStream_t s) {
         else if (chunks <= 1024) e = launch_pdl(k_norm_backward<A, G, C, 2, 512>, grid, dim3(threads_for((chunks + 1) / 2)), 0, s, a);
         else e = launch_pdl(k_norm_backward<A, G, C, 4, 512>, grid, dim3(threads_for((chunks + 3) / 4)), 0, s, a);
     } else {
-        e = launch_pdl(k_norm_backward_long<A, G>, dim3(a.T), dim3(1024), 0, s, a);
-        parts = parts < 16 ? parts : 16;
-        if (e == cudaSuccess && a.part) e = launch_pdl(k_dgamma_long<A>, dim3((a.H + 255) / 256, parts), dim3(256), 0, s, a);
+        // dgamma first: dx may lie over dy
+        parts = parts < kLongParts ? parts : kLongParts;
+        if (a.part) e = launch_pdl(k_dgamma_long<A>, dim3((a.H + 255) / 256, parts), dim3(256), 0, s, a);
+        if (e == cudaSuccess) e = launch_pdl(k_norm_backward_long<A, G>, dim3(a.T), dim3(1024), 0, s, a);
     }
     if (e == cudaSuccess && dgamma)
         e = launch_pdl(k_join_parts, dim3((a.H + 31) / 32), dim3(1024), 0, s, (const float*)a.part, parts, a.H, dgamma);

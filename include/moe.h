@@ -494,7 +494,7 @@ moe_status moe_expert_product(const int8_t* q, long long q_stride, int q_rows, c
  *   rstd   device f32 [T] or NULL: moe_norm_rows_backward reads it
  *   q      device i8 [T][hidden] with its stride, scale device f32 [T]; both
  *          or neither
- * eps >= 0; 1 <= hidden <= 131072, T <= 2^24.  The sum of squares is held in
+ * eps >= 0 (with 0 a row of zeros is 0 / 0); 1 <= hidden <= 131072, T <= 2^24.  The sum of squares is held in
  * fp32: a row where it overflows (|h| of 1e18 and more) has rstd 0.        */
 moe_status moe_norm_rows(const void* x, moe_dtype dtype, long long x_stride, const void* residual,
                          long long residual_stride, const void* gamma, moe_dtype gamma_dtype, int T,
@@ -561,7 +561,8 @@ moe_status moe_dequantize_blocks(const uint8_t* q, long long q_stride, const uin
  * Products of block values (which must stay in fp32's normal range) are exact
  * and summed in fp32, in a fixed order; the sum is
  * multiplied by scale and by w_scale, in this order, and rounded to out_dtype.
- * K a multiple of 32 in [32, 131072], 1 <= N <= 2^20, R <= 2^20.           */
+ * K a multiple of 32 in [32, 131072], 1 <= N <= 2^20, R <= 2^20, q_stride
+ * below 2^40.                                                             */
 moe_status moe_block_product(const uint8_t* q, long long q_stride, int q_rows, const uint8_t* s,
                              const float* scale, int K, int format, const uint8_t* wq, const uint8_t* ws,
                              const float* w_scale, int n_experts, int N, const int32_t* offsets,

@@ -44,7 +44,7 @@ REFUSALS = [
     ("moe_dequantize_blocks", 4, -1, "rows"), ("moe_dequantize_blocks", 5, 40, "K"), ("moe_dequantize_blocks", 6, -1, "format"),
     ("moe_dequantize_blocks", 7, P + 1, "aligned"), ("moe_dequantize_blocks", 8, 3, "dtype"), ("moe_dequantize_blocks", 9, 63, "stride"),
     ("moe_block_product", 0, None, "NULL"), ("moe_block_product", 0, P + 8, "aligned"), ("moe_block_product", 1, 31, "stride"),
-    ("moe_block_product", 1, 40, "stride"), ("moe_block_product", 2, -1, "R"), ("moe_block_product", 3, None, "NULL"),
+    ("moe_block_product", 1, 40, "stride"), ("moe_block_product", 1, 1 << 40, "stride"), ("moe_block_product", 2, -1, "R"), ("moe_block_product", 3, None, "NULL"),
     ("moe_block_product", 5, 0, "K"), ("moe_block_product", 5, 48, "K"), ("moe_block_product", 6, 3, "format"),
     ("moe_block_product", 7, None, "NULL"), ("moe_block_product", 7, P + 4, "aligned"), ("moe_block_product", 8, None, "NULL"),
     ("moe_block_product", 10, 0, "n_experts"), ("moe_block_product", 10, 1025, "n_experts"), ("moe_block_product", 11, 0, "N"),

@@ -18,7 +18,8 @@ from tests.test_gpu_sorted_rows import BF16, EPS, F16, F32, between, f64, rows_o
 pytestmark = pytest.mark.gpu
 # T, H, padding between rows
 SHAPES = [(1, 1, 0), (1, 4096, 0), (3, 7, 1), (33, 128, 3), (257, 1030, 0), (64, 4096, 8), (130, 2047, 2), (19, 8200, 0),
-          (5, 16384, 0), (3, 33001, 0), (2, 131072, 0), (700, 256, 0), (1300, 96, 5), (9, 6144, 4), (4, 12288, 0)]
+          (5, 16384, 0), (3, 33001, 0), (2, 131072, 0), (700, 256, 0), (1300, 96, 5), (9, 6144, 4), (4, 12288, 0),
+          (1000, 2048, 8), (459, 4096, 0), (460, 8192, 0)]
 TYPES = [(F32, F32), (BF16, BF16), (BF16, F32), (F16, F16), (F16, F32)]
 
 
@@ -141,16 +142,17 @@ def test_norm_rows_backward(T, H, pad, dtype, gamma_dtype, stream):
     assert torch.equal(alone, dx)
 
 
-@pytest.mark.parametrize("H", [96, 2047, 9000])
-def test_gradient_in_place(H):
-    h, dy, dh, gamma = rows_of(8, H, BF16, 1), rows_of(8, H, BF16, 2), rows_of(8, H, BF16, 3), gamma_of(H, F32)
-    rstd = torch.rand(8, device="cuda") + 0.5
-    dx = torch.empty(8, H, dtype=BF16, device="cuda")
-    bqe.moe_norm_rows_backward(dy, h, gamma, rstd, dx, dh=dh)
+@pytest.mark.parametrize("T,H", [(8, 96), (8, 2047), (8, 9000), (8, 33001), (500, 4096), (1000, 2048), (470, 8192)])
+def test_gradient_in_place(T, H):
+    h, dy, dh, gamma = rows_of(T, H, BF16, 1), rows_of(T, H, BF16, 2), rows_of(T, H, BF16, 3), gamma_of(H, F32)
+    rstd = torch.rand(T, device="cuda") + 0.5
+    dx, g = torch.empty(T, H, dtype=BF16, device="cuda"), [torch.empty(H, device="cuda") for _ in range(2)]
+    scratch = torch.empty(bqe.moe_norm_scratch_bytes(T, H), dtype=torch.uint8, device="cuda")
+    bqe.moe_norm_rows_backward(dy, h, gamma, rstd, dx, g[0], scratch, dh)
     for over in (dy.clone(), dh.clone()):
         one = torch.equal(over, dy)
-        bqe.moe_norm_rows_backward(over if one else dy, h, gamma, rstd, over, dh=dh if one else over)
-        assert torch.equal(over, dx)
+        bqe.moe_norm_rows_backward(over if one else dy, h, gamma, rstd, over, g[1], scratch, dh if one else over)
+        assert torch.equal(over, dx) and torch.equal(g[0], g[1])
 
 
 def test_gradient_of_differences():
