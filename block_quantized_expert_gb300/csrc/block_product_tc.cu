@@ -346,28 +346,38 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
     } else if (warp == C::kMma) {
         // ------------------------------------------------------------- MMA --
         // (the first CTA of a pair issues for both)
+        // The loops run by values that the compiler knows to be uniform over the warp (kernel
+        // arguments and reductions; what comes from memory is not), so that stages' addresses are,
+        // and the next unit is looked for between this one's issues: a wait, its vote and fence
+        // take longer than the MMAs of a few positions.
         const uint32_t on = elect_lane();
-        int s = 0, n = 0, batch = 0;  // batch: of all so far
+        const int mine = __reduce_max_sync(kAll, rank == 0 && first_tile < tiles ? (tiles - first_tile + tile_step - 1) / tile_step : 0);
+        const int units = (a.K + C::kUnit - 1) / C::kUnit;
+        int s = 0, batch = 0;  // batch: of all so far
         uint32_t phase = 0;
-        for (int t = first_tile; t < tiles && ok && rank == 0; t += tile_step, ++n) {
-            // (the reduction's result is known to be uniform, a value from memory is not)
-            const uint32_t cols = __reduce_max_sync(kAll, columns(tile_at(t).count));
+        bool ready = false;    // stage s has been seen
+        for (int n = 0; n < mine && ok; ++n) {
+            const uint32_t cols = __reduce_max_sync(kAll, columns(tile_at(first_tile + n * tile_step).count));
             // e2m1 both, N >> 3, UE8M0 scales: bit 23, M >> 4
             const uint32_t idesc = (1u << 7) | (1u << 10) | ((cols >> 3) << 17) | ((kNv ? 0u : 1u) << 23) | ((128u * C::kCtas >> 4) << 24);
             const int b = n & 1;
-            const uint32_t d = __reduce_max_sync(kAll, (uint32_t)(b * kCap));
+            const uint32_t d = b * kCap;
             ok = __all_sync(kAll, wait_for<kPair>(d_empty(b), ((n >> 1) & 1) ^ 1, abort, a.wait_ns));
             tc_fence_after();
             int unit = 0;  // of the batch
-            for (int k = a.K; k > 0 && ok; k -= C::kUnit) {
+            for (int u = 0; u < units && ok; ++u) {
                 if (unit == 0) ok = __all_sync(kAll, wait_for<kPair>(scaled(batch & 1), (batch >> 1) & 1, abort, a.wait_ns));
-                ok = ok && __all_sync(kAll, wait_for<kPair>(landed(s), phase, abort, a.wait_ns));
+                if (!ready) ok = ok && __all_sync(kAll, wait_for<kPair>(landed(s), phase, abort, a.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t st = base + __reduce_max_sync(kAll, (uint32_t)s) * C::kStage;
-                const uint32_t sf = sf_base + __reduce_max_sync(kAll, (uint32_t)((batch & 1) * C::kBatch + unit)) * C::kSfStride;
+                const uint32_t st = base + s * C::kStage, sf = sf_base + ((batch & 1) * C::kBatch + unit) * C::kSfStride, done = empty(s);
                 const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + C::kABytes), fd = desc_sf(sf);
-                const int steps = min(k + 63, 256) / 64;
+                const int steps = min(a.K - u * C::kUnit + 63, 256) / 64;
+                if (++s == C::kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+                const bool seen = test_wait<kPair>(landed(s), phase);
 #pragma unroll
                 for (int j = 0; j < C::kWords; ++j) {
                     copy_scales<kPair>(on, C::kSfCol + 4 * j, fd + 32 * j);
@@ -383,18 +393,15 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
                     const int word = kNv ? j : j / 2;
                     const uint32_t id = kNv ? 0u : (j & 1) * 2u;  // which half of a word's bytes
                     mma_fp4<kPair, kNv>(on, d, ad + 2 * j, bd + 2 * j, idesc | (id << 4) | (id << 29), C::kSfCol + 4 * word,
-                                        C::kSfCol + C::kSfA + 4 * word * C::kHalves, j > 0 || k != a.K);
+                                        C::kSfCol + C::kSfA + 4 * word * C::kHalves, j > 0 || u > 0);
                 }
-                mma_commit_by<kPair>(on, empty(s));
-                if (++unit == C::kBatch || k <= C::kUnit) {
+                mma_commit_by<kPair>(on, done);
+                if (++unit == C::kBatch || u == units - 1) {
                     mma_commit_by<kPair>(on, sf_empty(batch & 1));
                     ++batch;
                     unit = 0;
                 }
-                if (++s == C::kStages) {
-                    s = 0;
-                    phase ^= 1;
-                }
+                ready = __all_sync(kAll, seen);
             }
             if (ok) mma_commit_by<kPair>(on, d_full(b));
         }
