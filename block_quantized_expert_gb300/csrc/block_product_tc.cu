@@ -5,13 +5,25 @@
 // A CTA (or a pair of CTAs on one MMA, cta_group::2) walks tiles of 128 (256) output
 // channels (A, one tensor-memory lane a channel) x up to kCap positions of one
 // segment (B), K in units of 256, 128 bytes of codes a row:
-//   1 warp    TMA: a box of 128 channels' codes, and the positions' rows four at a
-//             time (tile::gather4: a gather by row_src costs what adjacent rows cost)
-//   4 warps   block scales: both sides' from their rows in global memory, one unit ahead,
-//             into the 512-byte atoms that tcgen05.cp takes to tensor memory
-//   1 warp    the copies of the scales and the MMAs, four of K = 64 a unit
-//   4 warps   accumulators -> row and channel scales -> out, two accumulators in turn
-//   1 warp    rows and row scales of up to kTabs tiles ahead
+//   4 or 6 warps  TMA: a box of 128 channels' codes, and the positions' rows four at a time
+//                 (tile::gather4: a gather by row_src costs what adjacent rows cost); one
+//                 warp of copies took 2.2 times as long, for a lane issues one in some 130 cycles
+//   4 warps       block scales of both sides, from their rows in global memory through
+//                 registers into the 512-byte atoms that tcgen05.cp takes to tensor memory, in
+//                 batches of 64 bytes a row (whole sectors: in pieces of a unit, 16 bytes, the
+//                 49152 rows below took 708 us for 667, in sectors by one lane a row 656 for 620)
+//   1 warp        the copies of the scales and the MMAs, four of K = 64 a unit
+//   4 warps       accumulators -> row and channel scales -> out, two accumulators in turn
+//   1 warp        rows and row scales of up to kTabs tiles ahead
+//
+// Measured at K = N = 4096, bf16 out, the copy rate being 6.78 TB/s: 3000 rows over some 231 of
+// 256 experts 317 us in MXFP4, 337 in NVFP4, 7.3 TB/s; 49152 rows over 256 experts 557 and
+// 587 us, 2.8 PFLOP/s; 8192 rows of one expert 66 and 71 us, 4.2 and 3.9 PFLOP/s.  The
+// narrow form is bound by the stream of weights.  The wide one takes in codes and scales and gives
+// out sums at about 62 bytes a ns an SM in every variant that was timed (fewer or more stages,
+// narrower tiles, a cluster of four that shares its gathers, streaming hints), and that is
+// what bounds it: 25 KB of codes a unit of 140 positions, half of it weights that other
+// tiles of the expert bring again.
 #include <cuda.h>
 
 #include <cmath>
@@ -619,9 +631,10 @@ cudaError_t launch_o(const BlockProduct& a, const CUtensorMap& wmap, const CUten
     // Narrow or wide tiles, by rounds over the GPU times what a round takes, in us.  A segment
     // of m positions has about m / cap + 1/2 tiles (those of the dense product are known) and at
     // least one; it is taken as equal to the others, for the segments are on the device.
-    // Measured at K = 4096, narrow and wide: 256 rows of one expert 11.3 and 13.8, 512 17.8 and
-    // 15.9, 1024 31 and 23; at K = 2048 and 256 experts of 32 rows 209 and 225, of 48 226 and 231,
-    // of 64 316 and 234; 777 rows at K = 1120, N = 1001 9.8 and 16.1.
+    // Measured at K = 4096, narrow and wide: 256 rows of one expert 11.1 and 12.6, 512 17.6 and
+    // 14.9, 1024 30 and 22; 32 experts of 48 rows 55 and 57, of 64 70 and 58; at K = 2048 and 256
+    // experts of 32 rows 204 and 209, of 48 223 and 218, of 64 316 and 223; 777 rows at K = 1120,
+    // N = 1001 9.7 and 16.1.
     const double segs = a.E < a.R ? a.E : a.R;
     auto cost = [&](int cap, int channels, int at_once, double fixed, double base, double a_row) {
         const double mean = a.R / segs, each = a.E == 1 ? (a.R + cap - 1) / cap : mean / cap + 0.5;

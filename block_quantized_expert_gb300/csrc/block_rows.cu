@@ -10,6 +10,10 @@
 // bits, so that the quotients amax / 6 / g and v / (s g), which fp32 rounds once,
 // fall on a value half way between two codes exactly where the real ones do.
 // With amax / 2688 itself one value in 500 of 16-bit rows is within 2^-24 of half way.
+//
+// 65536 x 4096 bf16 to codes: 122 us in NVFP4 (5.6 TB/s), 96 in MXFP4 (7.0); back 101 and 98
+// (6.8).  Gated, 49152 x 2048: 127 and 104 (4.0 TB/s), bound by the arithmetic of the gate and
+// of the codes, as NVFP4 is in part (65 % of all issue slots).
 #include <cmath>
 #include <type_traits>
 
