@@ -38,7 +38,7 @@ struct Norm {
     const A *x, *residual;
     long long xs, rs;
     const void* gamma;
-    int H;
+    int T, H;
     float eps;
     A *h, *y;  // either may be NULL
     long long hs, ys;
@@ -48,19 +48,21 @@ struct Norm {
     float* scale;
 };
 
-// One block a row.  kKeep chunks of C elements a thread stay in registers from the
-// sum to the codes; kKeep = 0: rows of any length, read again for each pass (from h
+// One block a row, or with kWarp a warp.  kKeep chunks of C elements a thread stay in
+// registers from the sum to the codes; kKeep = 0: rows of any length, read again for each pass (from h
 // where it is written: it may lie over an input).  Bound by HBM where rows move in 16-byte
 // words: 8192 x 4096 bf16 with a residual 42 us, 6.4 TB/s, with codes 55; in single
 // elements (H = 4095) 134.  40 registers leave six blocks of 256 threads on an SM.
-template <typename A, typename G, int C, int kKeep, int kMost>
+template <typename A, typename G, int C, int kKeep, int kMost, bool kWarp>
 __global__ void __launch_bounds__(kMost, kMost == 256 ? 6 : 1) k_norm_rows(const Norm<A> a) {
     pdl_launch_dependents();
     pdl_wait();
     __shared__ float part[32];
     __shared__ uint32_t tops[32];
-    const long long t = blockIdx.x;
-    const int first = threadIdx.x * C, step = blockDim.x * C, H = a.H;
+    const long long t = kWarp ? blockIdx.x * 8LL + (threadIdx.x >> 5) : blockIdx.x;
+    if (kWarp && t >= a.T) return;
+    const int lane = kWarp ? threadIdx.x & 31 : threadIdx.x;
+    const int first = lane * C, step = kWarp ? 32 * C : blockDim.x * C, H = a.H;
     const A* x = a.x + t * a.xs;
     const G* gamma = reinterpret_cast<const G*>(a.gamma);
     constexpr int kHeld = kKeep ? kKeep : 1;
@@ -92,8 +94,8 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 6 : 1) k_norm_rows(const
 #pragma unroll
         for (int i = 0; i < C; ++i) sum = fmaf(f[i], f[i], sum);
     });
-    const float r = 1.f / sqrtf(block_sum(sum, part) / (float)H + a.eps);
-    if (threadIdx.x == 0 && a.rstd) a.rstd[t] = r;
+    const float r = 1.f / sqrtf((kWarp ? warp_sum(sum) : block_sum(sum, part)) / (float)H + a.eps);
+    if (lane == 0 && a.rstd) a.rstd[t] = r;
     // y of a chunk of h, in place
     auto scaled = [&](Chunk<A, C>& v, int c) {
         float f[C], g[C];
@@ -116,9 +118,9 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 6 : 1) k_norm_rows(const
         if (a.q) top = top_bits<A, C>(v, top);
     });
     if (!a.q) return;
-    const float most = block_most<A>(top, tops);
+    const float most = kWarp ? __uint_as_float(warp_most<A>(top)) : block_most<A>(top, tops);
     const RowScale by = row_scale(most);
-    if (threadIdx.x == 0) a.scale[t] = by.scale;
+    if (lane == 0) a.scale[t] = by.scale;
     each([&](Chunk<A, C>& v, int c) {
         if (!kKeep) {
             if (a.y) {
@@ -184,20 +186,23 @@ __device__ __forceinline__ void back_dx(const Chunk<A, C>& dy, const Chunk<A, C>
 }
 
 // A block walks rows t, t + gridDim.x, ... ; a thread's columns stay the same, so
-// its share of dgamma is summed in registers and written once.
-template <typename A, typename G, int C, int kKeep, int kMost>
-__global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) k_norm_backward(const NormBack<A> a) {
+// its share of dgamma is summed in registers and written once.  With kWarp each of its
+// eight warps walks rows of its own, and the warps' shares are summed in their order.
+template <typename A, typename G, int C, int kKeep, int kMost, bool kWarp>
+__global__ void __launch_bounds__(kMost, kMost == 256 ? (kWarp && kKeep > 2 ? 2 : 3) : 1) k_norm_backward(const NormBack<A> a) {
     pdl_launch_dependents();
     pdl_wait();
     __shared__ float part[2][32];
-    const int first = threadIdx.x * C, step = blockDim.x * C, H = a.H;
+    const int warp = threadIdx.x >> 5, H = a.H;
+    const int first = (kWarp ? threadIdx.x & 31 : threadIdx.x) * C, step = kWarp ? 32 * C : blockDim.x * C;
     Chunk<G, C> gamma[kKeep];
     float dgamma[kKeep][C] = {};
 #pragma unroll
     for (int n = 0; n < kKeep; ++n)
         if (first + n * step < H) gamma[n] = load_chunk<G, C>(reinterpret_cast<const G*>(a.gamma) + first + n * step);
     int turn = 0;
-    for (long long t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+    const long long start = kWarp ? blockIdx.x * 8LL + warp : blockIdx.x, rows = kWarp ? gridDim.x * 8LL : gridDim.x;
+    for (long long t = start; t < a.T; t += rows, turn ^= 1) {
         Chunk<A, C> dy[kKeep], h[kKeep], dh[kKeep];
         const float r = a.rstd[t];
 #pragma unroll
@@ -212,12 +217,25 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) k_norm_backward(c
 #pragma unroll
         for (int n = 0; n < kKeep; ++n)
             if (first + n * step < H) back_dot(dy[n], h[n], gamma[n], r, dot, dgamma[n]);
-        const float mean = block_sum(dot, part[turn]) / (float)H;  // of g h r
+        const float mean = (kWarp ? warp_sum(dot) : block_sum(dot, part[turn])) / (float)H;  // of g h r
 #pragma unroll
         for (int n = 0; n < kKeep; ++n)
             if (first + n * step < H) back_dx(dy[n], h[n], gamma[n], dh[n], a.dh != nullptr, r, mean, a.dx + t * a.dxs + first + n * step);
     }
-    if (a.part) {
+    if (!a.part) return;
+    if constexpr (kWarp) {
+        __shared__ alignas(32) float sums[8][kKeep * 32 * C];
+#pragma unroll
+        for (int n = 0; n < kKeep; ++n)
+            if (first + n * step < H) store_chunk<float, C>(&sums[warp][first + n * step], dgamma[n]);
+        __syncthreads();
+        for (int c = threadIdx.x; c < H; c += blockDim.x) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) sum += sums[w][c];
+            a.part[(long long)blockIdx.x * H + c] = sum;
+        }
+    } else {
 #pragma unroll
         for (int n = 0; n < kKeep; ++n)
             if (first + n * step < H) store_chunk<float, C>(a.part + (long long)blockIdx.x * H + first + n * step, dgamma[n]);
@@ -341,23 +359,40 @@ __global__ void __launch_bounds__(1024) k_join_parts(const float* part, int part
 
 // ----------------------------------------------------------------- launches --
 // Blocks of the gradient at most: three an SM of 256 threads, and more of the smaller ones
-// (8192 x 1024 bf16: 29 us with 456, 20 with 912; 8192 x 4096: 52 and 54).
+// (8192 x 1024 bf16: 29 us with 456, 20 with 912; 2048 wide 33 and 33; 8192 x 4096: 47.6 and
+// 51).  fp32 rows are twice as long and take 456 (8192 x 1024: 28 for 30; 2048 wide 44 for 47).
 // Rows past 16384 are long whatever their type.
 constexpr int kLongParts = 16;
 int most_parts(int H) { return H <= 2048 ? 912 : H <= 16384 ? 456 : kLongParts; }
+
+
+// Short rows take a warp each: the GPU starts a block in about 1 ns, so that 65536 rows of any
+// width took 67 us and more (of 64 bf16: 11.4 now, 1024: 45).  The warp pays with more chunks a
+// lane where rows are few: 1024 x 1024 bf16 2.6 us by blocks and 3.0 by warps, 2048 rows
+// 4.4 and 4.3, 8192 8.8 and 7.5.  The gradient's blocks walk rows, and there the warps win as long as
+// a lane has 16 columns (8192 x 256 bf16: 6.4 us for 10.3, 65536: 29 for 81; 8192 x 512
+// fp32 15.5 for 18.4, but x 1024 bf16, 32 columns, 27.6 for 20.3); 456 blocks of them (912:
+// 7.9 us for the first, 304: 7.0).
+constexpr int kWarpRows = 2048, kWarpBlocks = 456;
 
 int threads_for(int chunks) { return (chunks + 31) / 32 * 32; }
 
 // Many rows: four chunks a thread, so that more rows are on an SM at once; few: more
 // threads for each.
 template <typename A, typename G, int C>
-cudaError_t norm_c(const Norm<A>& a, int T, cudaStream_t s) {
+cudaError_t norm_c(const Norm<A>& a, cudaStream_t s) {
     const int chunks = (a.H + C - 1) / C;
-    if (chunks <= 128 || (chunks <= 512 && T < 608))
-        return launch_pdl(k_norm_rows<A, G, C, 1, 512>, dim3(T), dim3(threads_for(chunks)), 0, s, a);
-    if (chunks <= 1024) return launch_pdl(k_norm_rows<A, G, C, 4, 256>, dim3(T), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
-    if (chunks <= 4096) return launch_pdl(k_norm_rows<A, G, C, 4, 1024>, dim3(T), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
-    return launch_pdl(k_norm_rows<A, G, C, 0, 1024>, dim3(T), dim3(1024), 0, s, a);
+    if (chunks <= 32 || (chunks <= 128 && a.T >= kWarpRows)) {
+        const dim3 grid((a.T + 7) / 8);
+        if (chunks <= 32) return launch_pdl(k_norm_rows<A, G, C, 1, 256, true>, grid, dim3(256), 0, s, a);
+        if (chunks <= 64) return launch_pdl(k_norm_rows<A, G, C, 2, 256, true>, grid, dim3(256), 0, s, a);
+        return launch_pdl(k_norm_rows<A, G, C, 4, 256, true>, grid, dim3(256), 0, s, a);
+    }
+    if (chunks <= 128 || (chunks <= 512 && a.T < 608))
+        return launch_pdl(k_norm_rows<A, G, C, 1, 512, false>, dim3(a.T), dim3(threads_for(chunks)), 0, s, a);
+    if (chunks <= 1024) return launch_pdl(k_norm_rows<A, G, C, 4, 256, false>, dim3(a.T), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
+    if (chunks <= 4096) return launch_pdl(k_norm_rows<A, G, C, 4, 1024, false>, dim3(a.T), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
+    return launch_pdl(k_norm_rows<A, G, C, 0, 1024, false>, dim3(a.T), dim3(1024), 0, s, a);
 }
 
 template <typename A, typename G, int kKeep, int kDepth>
@@ -371,20 +406,26 @@ cudaError_t back_ring(const NormBack<A>& a, int parts, int threads, cudaStream_t
 template <typename A, typename G, int C>
 cudaError_t back_c(const NormBack<A>& a, float* dgamma, cudaStream_t s) {
     const int chunks = (a.H + C - 1) / C;
-    const int most = most_parts(a.H);
+    const int most = sizeof(A) == 4 && chunks > 128 && a.H <= 16384 ? 456 : most_parts(a.H);
     int parts = a.T < most ? a.T : most;
     cudaError_t e = cudaSuccess;
     if (a.T == 0) {
+    } else if (chunks <= 128 && a.H <= 512) {
+        parts = a.T < 8 * kWarpBlocks ? (a.T + 7) / 8 : kWarpBlocks;
+        const dim3 grid(parts);
+        if (chunks <= 32) e = launch_pdl(k_norm_backward<A, G, C, 1, 256, true>, grid, dim3(256), 0, s, a);
+        else if (chunks <= 64) e = launch_pdl(k_norm_backward<A, G, C, 2, 256, true>, grid, dim3(256), 0, s, a);
+        else if constexpr (C <= 4) e = launch_pdl(k_norm_backward<A, G, C, 4, 256, true>, grid, dim3(256), 0, s, a);
     } else if (C == 16 / (int)sizeof(A) && a.T > most && chunks > 128 && chunks <= 1024) {
         if (chunks <= 256) e = back_ring<A, G, 1, 4>(a, parts, threads_for(chunks), s);
         else if (chunks <= 512) e = back_ring<A, G, 2, 2>(a, parts, threads_for((chunks + 1) / 2), s);
         else e = back_ring<A, G, 4, 2>(a, parts = 152, threads_for((chunks + 3) / 4), s);
     } else if (chunks <= 2048) {
         const dim3 grid(parts);
-        if (chunks <= 256) e = launch_pdl(k_norm_backward<A, G, C, 1, 256>, grid, dim3(threads_for(chunks)), 0, s, a);
-        else if (chunks <= 512) e = launch_pdl(k_norm_backward<A, G, C, 2, 256>, grid, dim3(threads_for((chunks + 1) / 2)), 0, s, a);
-        else if (chunks <= 1024) e = launch_pdl(k_norm_backward<A, G, C, 2, 512>, grid, dim3(threads_for((chunks + 1) / 2)), 0, s, a);
-        else e = launch_pdl(k_norm_backward<A, G, C, 4, 512>, grid, dim3(threads_for((chunks + 3) / 4)), 0, s, a);
+        if (chunks <= 256) e = launch_pdl(k_norm_backward<A, G, C, 1, 256, false>, grid, dim3(threads_for(chunks)), 0, s, a);
+        else if (chunks <= 512) e = launch_pdl(k_norm_backward<A, G, C, 2, 256, false>, grid, dim3(threads_for((chunks + 1) / 2)), 0, s, a);
+        else if (chunks <= 1024) e = launch_pdl(k_norm_backward<A, G, C, 2, 512, false>, grid, dim3(threads_for((chunks + 1) / 2)), 0, s, a);
+        else e = launch_pdl(k_norm_backward<A, G, C, 4, 512, false>, grid, dim3(threads_for((chunks + 3) / 4)), 0, s, a);
     } else {
         // dgamma first: dx may lie over dy
         parts = parts < kLongParts ? parts : kLongParts;
@@ -410,14 +451,14 @@ cudaError_t by_chunk(unsigned align, const void* gamma, int H, F&& f) {
 unsigned least(unsigned a, unsigned b) { return a < b ? a : b; }
 
 template <typename A, typename G>
-cudaError_t norm_ag(Norm<A> a, int T, cudaStream_t s) {
+cudaError_t norm_ag(const Norm<A>& a, cudaStream_t s) {
     constexpr long long z = sizeof(A);
     unsigned al = row_align(a.x, a.xs * z);
     if (a.residual) al = least(al, row_align(a.residual, a.rs * z));
     if (a.h) al = least(al, row_align(a.h, a.hs * z));
     if (a.y) al = least(al, row_align(a.y, a.ys * z));
     if (a.q) al = least(al, (unsigned)z * row_align(a.q, a.qs));  // a code for each element
-    return by_chunk<A, G>(al, a.gamma, a.H, [&](auto c) { return norm_c<A, G, decltype(c)::value>(a, T, s); });
+    return by_chunk<A, G>(al, a.gamma, a.H, [&](auto c) { return norm_c<A, G, decltype(c)::value>(a, s); });
 }
 
 template <typename A, typename G>
@@ -474,9 +515,9 @@ extern "C" moe_status moe_norm_rows(const void* x, moe_dtype dtype, long long x_
     cudaStream_t s = (cudaStream_t)stream;
     auto run = [&](auto type) {
         using A = decltype(type);
-        const Norm<A> a{(const A*)x, (const A*)residual, x_stride, residual_stride, gamma, hidden, eps, (A*)h, (A*)y,
+        const Norm<A> a{(const A*)x, (const A*)residual, x_stride, residual_stride, gamma, T, hidden, eps, (A*)h, (A*)y,
                         h_stride, y_stride, rstd, q, q_stride, scale};
-        return gamma_dtype == MOE_F32 ? norm_ag<A, float>(a, T, s) : norm_ag<A, A>(a, T, s);
+        return gamma_dtype == MOE_F32 ? norm_ag<A, float>(a, s) : norm_ag<A, A>(a, s);
     };
     cudaError_t e;
     if (dtype == MOE_F32) e = run(float());

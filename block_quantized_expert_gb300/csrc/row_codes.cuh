@@ -59,14 +59,20 @@ __device__ __forceinline__ uint32_t top_bits(const Chunk<A, C>& c, uint32_t top)
     return top;
 }
 
-// The block's largest magnitude from its threads' top_bits; part: one word a warp.
+// The warp's largest magnitude, as bits of fp32, from its threads' top_bits.
 template <typename A>
-__device__ __forceinline__ float block_most(uint32_t top, uint32_t* part) {
-    if (sizeof(A) == 2) {  // to the bits of that magnitude in fp32
+__device__ __forceinline__ uint32_t warp_most(uint32_t top) {
+    if (sizeof(A) == 2) {
         const uint16_t h = (uint16_t)max(top & 0xFFFFu, top >> 16);
         top = __float_as_uint(to_f32(*reinterpret_cast<const A*>(&h)));
     }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    return __reduce_max_sync(0xFFFFFFFFu, top);
+}
+
+// The block's; part: one word a warp.
+template <typename A>
+__device__ __forceinline__ float block_most(uint32_t top, uint32_t* part) {
+    top = warp_most<A>(top);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
     __syncthreads();
     top = part[0];

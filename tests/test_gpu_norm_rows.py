@@ -229,3 +229,37 @@ def test_offsets_past_32_bits(T):
     bqe.moe_norm_rows_backward(y, h, gamma, rstd, dx)
     bqe.moe_norm_rows_backward(small, x.contiguous(), gamma, rstd, small)
     assert torch.equal(dx, small)
+
+
+# Rows of up to 128 chunks, a warp each: every number of chunks a lane, more rows than the
+# warps of the grid's blocks walk at once, and a last block that is not full.
+SHORT = [(3001, 64, 0), (2049, 504, 0), (5000, 512, 8), (2051, 1024, 0), (4099, 128, 0), (4001, 127, 0), (2500, 33, 2),
+         (2048, 1000, 8), (9, 250, 6), (3650, 8, 0)]
+
+
+@pytest.mark.parametrize("T,H,pad", SHORT)
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_short_rows(T, H, pad, dtype):
+    test_norm_rows(T, H, pad, dtype, F32, True)
+    test_norm_rows(T, H, pad, dtype, dtype, False)
+    test_codes_are_those_of_the_rows(T, H, pad, dtype, "both")
+    test_codes_are_those_of_the_rows(T, H, pad, dtype, "codes alone")
+
+
+@pytest.mark.parametrize("T,H,pad", SHORT)
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_short_rows_backward(T, H, pad, dtype):
+    test_norm_rows_backward(T, H, pad, dtype, F32, True)
+    test_norm_rows_backward(T, H, pad, dtype, dtype, False)
+
+
+@pytest.mark.parametrize("T,H", [(2500, 64), (4000, 256), (2049, 1024), (5000, 127)])
+def test_short_rows_in_place(T, H):
+    """h over an input, dx over dy: a warp has read its row before it writes it."""
+    test_gradient_in_place(T, H)
+    x, res, gamma = rows_of(T, H, BF16, 1), rows_of(T, H, BF16, 2), gamma_of(H, F32)
+    y0, h0, y = (torch.empty(T, H, dtype=BF16, device="cuda") for _ in range(3))
+    bqe.moe_norm_rows(x, gamma, y0, 1e-6, res, h0)
+    stream = res.clone()
+    bqe.moe_norm_rows(x, gamma, y, 1e-6, stream, stream)
+    assert torch.equal(stream, h0) and torch.equal(y, y0)
