@@ -51,10 +51,10 @@ struct Norm {
 // One block a row, or with kWarp a warp.  kKeep chunks of C elements a thread stay in
 // registers from the sum to the codes; kKeep = 0: rows of any length, read again for each pass (from h
 // where it is written: it may lie over an input).  Bound by HBM where rows move in 16-byte
-// words: 8192 x 4096 bf16 with a residual 42 us, 6.4 TB/s, with codes 55; in single
-// elements (H = 4095) 134.  40 registers leave six blocks of 256 threads on an SM.
+// words: 8192 x 4096 bf16 with a residual 41.3 us, 6.5 TB/s, 32768 rows 154, 7.0; with codes
+// 54.5; without a residual 27, 5.0; in single elements (H = 4095) 132.
 template <typename A, typename G, int C, int kKeep, int kMost, bool kWarp>
-__global__ void __launch_bounds__(kMost, kMost == 256 ? 6 : 1) k_norm_rows(const Norm<A> a) {
+__global__ void __launch_bounds__(kMost, kMost > 256 ? 1 : kKeep == 2 ? 8 : 6) k_norm_rows(const Norm<A> a) {
     pdl_launch_dependents();
     pdl_wait();
     __shared__ float part[32];
@@ -377,8 +377,11 @@ constexpr int kWarpRows = 2048, kWarpBlocks = 456;
 
 int threads_for(int chunks) { return (chunks + 31) / 32 * 32; }
 
-// Many rows: four chunks a thread, so that more rows are on an SM at once; few: more
-// threads for each.
+// Few rows, all of them on the GPU at once: a thread a chunk (1000 x 2048 bf16: 3.0 us; 3.9 with two
+// chunks, 4.4 with four).  Many: two chunks a thread and eight blocks of 256 an SM (8192 x 4096 bf16
+// 26.9 us and with a residual 41.3; four chunks 28.2 and 42.2, one 33 and 43), or four for
+// fp32 rows without a residual (32768 x 2048: 79 us for 89) and for long rows.
+constexpr long long kAtOnce = 152 * 2048;
 template <typename A, typename G, int C>
 cudaError_t norm_c(const Norm<A>& a, cudaStream_t s) {
     const int chunks = (a.H + C - 1) / C;
@@ -388,8 +391,10 @@ cudaError_t norm_c(const Norm<A>& a, cudaStream_t s) {
         if (chunks <= 64) return launch_pdl(k_norm_rows<A, G, C, 2, 256, true>, grid, dim3(256), 0, s, a);
         return launch_pdl(k_norm_rows<A, G, C, 4, 256, true>, grid, dim3(256), 0, s, a);
     }
-    if (chunks <= 128 || (chunks <= 512 && a.T < 608))
+    if (chunks <= 128 || (chunks <= 512 && (long long)a.T * chunks <= kAtOnce))
         return launch_pdl(k_norm_rows<A, G, C, 1, 512, false>, dim3(a.T), dim3(threads_for(chunks)), 0, s, a);
+    if (chunks <= 512 && (sizeof(A) == 2 || a.residual))
+        return launch_pdl(k_norm_rows<A, G, C, 2, 256, false>, dim3(a.T), dim3(threads_for((chunks + 1) / 2)), 0, s, a);
     if (chunks <= 1024) return launch_pdl(k_norm_rows<A, G, C, 4, 256, false>, dim3(a.T), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
     if (chunks <= 4096) return launch_pdl(k_norm_rows<A, G, C, 4, 1024, false>, dim3(a.T), dim3(threads_for((chunks + 3) / 4)), 0, s, a);
     return launch_pdl(k_norm_rows<A, G, C, 0, 1024, false>, dim3(a.T), dim3(1024), 0, s, a);

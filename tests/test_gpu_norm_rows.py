@@ -235,6 +235,8 @@ def test_offsets_past_32_bits(T):
 # warps of the grid's blocks walk at once, and a last block that is not full.
 SHORT = [(3001, 64, 0), (2049, 504, 0), (5000, 512, 8), (2051, 1024, 0), (4099, 128, 0), (4001, 127, 0), (2500, 33, 2),
          (2048, 1000, 8), (9, 250, 6), (3650, 8, 0)]
+# two chunks a thread, with a last one that some threads do not have
+SHORT += [(1300, 2040, 0), (700, 4088, 0), (1300, 1100, 4), (650, 511, 1)]
 
 
 @pytest.mark.parametrize("T,H,pad", SHORT)
