@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(128) k_block_product_few(const BlockProduct a)
     }
 }
 
-// At K = N = 4096 one position of one expert takes 5.4 us here and 8.7 on the tensor cores, two
-// 8.7 and 8.7 (7.9 with four positions a warp), four 11.3 and 8.7; six of six experts 17.2 and 16.1.
+// At K = N = 4096 one position of one expert takes 5.4 us here and 8.6 on the tensor cores, two
+// 8.7 and 8.6 (7.9 with four positions a warp), four 11.3 and 8.6; six of six experts 17.2 and 16.1.
 bool few_rows(const BlockProduct& a) { return a.R <= 2; }
 
 cudaError_t launch_few(const BlockProduct& a, bool nv, moe_dtype out, cudaStream_t s) {

@@ -5,25 +5,27 @@
 // A CTA (or a pair of CTAs on one MMA, cta_group::2) walks tiles of 128 (256) output
 // channels (A, one tensor-memory lane a channel) x up to kCap positions of one
 // segment (B), K in units of 256, 128 bytes of codes a row:
-//   4 or 6 warps  TMA: a box of 128 channels' codes, and the positions' rows four at a time
-//                 (tile::gather4: a gather by row_src costs what adjacent rows cost); one
-//                 warp of copies took 2.2 times as long, for a lane issues one in some 130 cycles
+//   4 or 6 warps  TMA, in four or two teams that take units in turn: a box of 128 channels'
+//                 codes, and the positions' rows, four at a time by row_src (tile::gather4) or 16
+//                 where positions are rows.  A lane issues a copy in some 130 cycles and
+//                 a unit's wait, expectation and copies follow each other, so one warp's copies took 2.2
+//                 times as long, and all six on each unit 584 us for 549 (49152 rows below)
 //   4 warps       block scales of both sides, from their rows in global memory through
 //                 registers into the 512-byte atoms that tcgen05.cp takes to tensor memory, in
-//                 batches of 64 bytes a row (whole sectors: in pieces of a unit, 16 bytes, the
-//                 49152 rows below took 708 us for 667, in sectors by one lane a row 656 for 620)
+//                 batches of 64 bytes a row (in pieces of a unit, 16 bytes, 708 us for 667, in
+//                 sectors by one lane a row 656 for 620; two batches of 32 bytes in flight 646
+//                 for 549: the rest of a line is in L1 when the next batch wants it)
 //   1 warp        the copies of the scales and the MMAs, four of K = 64 a unit
 //   4 warps       accumulators -> row and channel scales -> out, two accumulators in turn
 //   1 warp        rows and row scales of up to kTabs tiles ahead
 //
-// Measured at K = N = 4096, bf16 out, the copy rate being 6.78 TB/s: 3000 rows over some 231 of
-// 256 experts 317 us in MXFP4, 337 in NVFP4, 7.3 TB/s; 49152 rows over 256 experts 557 and
-// 587 us, 2.8 PFLOP/s; 8192 rows of one expert 66 and 71 us, 4.2 and 3.9 PFLOP/s.  The
-// narrow form is bound by the stream of weights.  The wide one takes in codes and scales and gives
-// out sums at about 62 bytes a ns an SM in every variant that was timed (fewer or more stages,
-// narrower tiles, a cluster of four that shares its gathers, streaming hints), and that is
-// what bounds it: 25 KB of codes a unit of 140 positions, half of it weights that other
-// tiles of the expert bring again.
+// Measured at K = N = 4096, bf16 out, the copy rate being 6.78 TB/s: 3000 rows over some 234 of
+// 256 experts 312 us in MXFP4, 332 in NVFP4, 7.4 TB/s; 49152 rows over 256 experts 514 and
+// 549 us, 3.2 and 3.0 PFLOP/s; 8192 rows of one expert 53 and 63 us, 5.2 and 4.4 PFLOP/s.
+// The narrow form is bound by the stream of weights; of six rows of six experts (16 us) the
+// scales' loads, one batch after the other, set the pace: tiles of 64 channels took as long each.
+// The wide one has no single bound left: without the weights' boxes 49152 rows take 9 to 17 %
+// less, without the scales' loads 4 to 7, without the stores 4 to 7, with one MMA of four 4.
 #include <cuda.h>
 
 #include <cmath>
@@ -61,12 +63,13 @@ struct Cfg {
     static constexpr int kSfA = 4 * kWords, kSfB = 4 * kWords * kHalves;
     static constexpr int kSfWarps = 4, kEpiWarps = 4;
     static constexpr int kEpi = kSfWarps;                // warps: scales, epilogue, TMA, MMA, rows
-    static constexpr int kTmaWarps = kPair ? 6 : 4, kGroups = (kRows / 4 + kTmaWarps - 1) / kTmaWarps;  // copies of a warp
+    static constexpr int kTmaWarps = kPair ? 6 : 4, kTeams = kPair ? 2 : 4;  // teams take units in turn
+    static constexpr int kPer = kTmaWarps / kTeams, kGroups = (kRows / 4 + kPer - 1) / kPer;  // warps of a team, copies of a warp
     static constexpr int kTma = kEpi + kEpiWarps, kMma = kTma + kTmaWarps, kLook = kMma + 1;
     static constexpr int kThreads = (kLook + 1) * 32;
     static constexpr int kSmem = 1024 + kStages * kStage + 2 * kBatch * kSfStride;
     static_assert(kSfCol + kSfA + kSfB <= 512 && kCap % (16 * kCtas) == 0 && kBBytes % 1024 == 0, "tensor memory");
-    static_assert(kSfWarps == 4, "scales");
+    static_assert(kSfWarps == 4 && kTeams <= kStages && kTmaWarps % kTeams == 0 && kGroups <= 32, "roles");
 };
 
 // D[tmem] (+)= (A sfa)(B sfb)^T over K = 64, both operands in shared memory; issued
@@ -158,7 +161,7 @@ __device__ __forceinline__ void load_scales(uint32_t (&w)[4], const uint8_t* row
     if (row == nullptr || at >= all) return;
     row += at;
     if (bytes == 16) {
-        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(row));
+        asm volatile("ld.global.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(row));
         return;
     }
     const int n = all - at;
@@ -307,37 +310,42 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
 
     if (warp >= C::kTma && warp < C::kTma + C::kTmaWarps) {
         // ------------------------------------------------------ codes (TMA) --
-        // The first warp brings the weights; the positions' rows, four a copy, are shared
-        // out over all of them.
-        int s = 0, n = 0;
+        // A team's first warp brings the weights; the positions' rows, four a copy, are shared out
+        // over its warps.
+        const int team = (warp - C::kTma) / C::kPer, part = (warp - C::kTma) % C::kPer;
+        const int group = lane * C::kPer + part, units = (a.K + C::kUnit - 1) / C::kUnit;
+        const bool boxes = a.row_src == nullptr;  // the map's are 16 rows then
+        int s = team, next = team, n = 0;  // next: unit of this team, counted from the tile's first
         uint32_t phase = 1;
         for (int t = first_tile; t < tiles && ok; t += tile_step, ++n) {
             const Tile w = tile_at(t);
             const int tab = n % C::kTabs, half = columns(w.count) / C::kCtas;
             ok = __all_sync(kAll, wait_for<false>(tab_full(tab), (n / C::kTabs) & 1, abort, a.wait_ns));
             if (!ok) break;
-            const int group = lane * C::kTmaWarps + warp - C::kTma;
-            const bool mine = lane < C::kGroups && 4 * group < half;
+            const bool mine = !boxes && lane < C::kGroups && 4 * group < half, box = boxes && 16 * group < half;
             int4 y = make_int4(none, none, none, none);
             if (mine) y = *reinterpret_cast<const int4*>(&token_row[tab][rank * half + 4 * group]);
             leave_tab(tab);
-            for (int k0 = 0; k0 < a.K && ok; k0 += C::kUnit) {
+            for (; next < units && ok; next += C::kTeams) {
                 ok = __all_sync(kAll, wait_for<kPair>(empty(s), phase, abort, a.wait_ns));
                 if (!ok) break;
-                const int su = __reduce_max_sync(kAll, s);
+                const int su = __reduce_max_sync(kAll, s), x = next * (C::kUnit / 2);
                 const uint32_t st = base + su * C::kStage, bar = kPair ? in_first(landed(su)) : landed(su);
-                if (warp == C::kTma && lane == 0) {
+                if (part == 0 && lane == 0) {
                     if (kPair) arrive_expect_in(bar, C::kABytes + half * 128);
                     else mbar_arrive_expect_tx(bar, C::kABytes + half * 128);
-                    if (!a.stall) load_box<kPair>(st, &wmap, k0 / 2, w.e * a.N + w.n0, bar);
+                    if (!a.stall) load_box<kPair>(st, &wmap, x, w.e * a.N + w.n0, bar);
                 }
                 __syncwarp();
-                if (mine) gather_rows<kPair>(st + C::kABytes + group * 512, &qmap, k0 / 2, y, bar);
-                if (++s == C::kStages) {
-                    s = 0;
+                if (mine) gather_rows<kPair>(st + C::kABytes + group * 512, &qmap, x, y, bar);
+                if (box) load_box<kPair>(st + C::kABytes + group * 2048, &qmap, x, w.p0 + rank * half + 16 * group, bar);
+                s += C::kTeams;
+                if (s >= C::kStages) {
+                    s -= C::kStages;
                     phase ^= 1;
                 }
             }
+            next -= units;
         }
     } else if (warp == C::kLook) {
         // --------------------------------------- rows and scales of the tiles --
@@ -510,7 +518,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
                 tmem_ld32(((uint32_t)(ew * 32) << 16) + b * kCap + c0, v);
                 tmem_ld_wait();
                 if (c0 + 32 >= w.count) release(b);  // the accumulator is free when its columns are in registers
-                const bool whole = c0 + 32 <= w.count && w.n0 + 128 <= a.N;
+                const bool whole = c0 + 32 <= w.count && w.n0 + ew * 32 + 32 <= a.N;
                 if (sizeof(O) == 2 && pairs) {
                     // neighbouring lanes swap: the even one stores both channels of an even
                     // position, the odd one those of the next
@@ -631,10 +639,10 @@ cudaError_t launch_o(const BlockProduct& a, const CUtensorMap& wmap, const CUten
     // Narrow or wide tiles, by rounds over the GPU times what a round takes, in us.  A segment
     // of m positions has about m / cap + 1/2 tiles (those of the dense product are known) and at
     // least one; it is taken as equal to the others, for the segments are on the device.
-    // Measured at K = 4096, narrow and wide: 256 rows of one expert 11.1 and 12.6, 512 17.6 and
-    // 14.9, 1024 30 and 22; 32 experts of 48 rows 55 and 57, of 64 70 and 58; at K = 2048 and 256
-    // experts of 32 rows 204 and 209, of 48 223 and 218, of 64 316 and 223; 777 rows at K = 1120,
-    // N = 1001 9.7 and 16.1.
+    // Measured at K = 4096 in NVFP4, narrow and wide: 256 rows of one expert 10.1 and 12.5, 300 14.0
+    // and 13.7, 1024 23 and 21; 32 experts of 32 rows 56 and 57, of 64 66 and 59; at K = 2048 and
+    // 256 experts of 24 rows 216 and 211 (MXFP4 181 and 190), of 48 272 and 228 (216 and 204); 777
+    // rows at K = 1120, N = 1001 10.3 and 17.3.
     const double segs = a.E < a.R ? a.E : a.R;
     auto cost = [&](int cap, int channels, int at_once, double fixed, double base, double a_row) {
         const double mean = a.R / segs, each = a.E == 1 ? (a.R + cap - 1) / cap : mean / cap + 0.5;
@@ -666,7 +674,7 @@ cudaError_t launch_block_product_tc(const BlockProduct& a, bool nv, moe_dtype ou
     CUtensorMap wmap, qmap;
     const uint64_t bytes = (uint64_t)a.K / 2;
     if (!map_codes(&wmap, a.wq, bytes, (uint64_t)a.E * a.N, bytes, 128) ||
-        !map_codes(&qmap, a.q, bytes, (uint64_t)(a.rows > 0 ? a.rows : 1), (uint64_t)a.qs, 1))
+        !map_codes(&qmap, a.q, bytes, (uint64_t)(a.rows > 0 ? a.rows : 1), (uint64_t)a.qs, a.row_src ? 1 : 16))
         return cudaErrorInvalidValue;
     auto run = [&](auto type) {
         using O = decltype(type);
