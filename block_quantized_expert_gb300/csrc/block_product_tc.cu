@@ -14,7 +14,7 @@
 //                 registers into the 512-byte atoms that tcgen05.cp takes to tensor memory, in
 //                 batches of 64 bytes a row (in pieces of a unit, 16 bytes, 708 us for 667, in
 //                 sectors by one lane a row 656 for 620; two batches of 32 bytes in flight 646
-//                 for 549: the rest of a line is in L1 when the next batch wants it)
+//                 for 549, two of 64 in the narrow form 346 for 332)
 //   1 warp        the copies of the scales and the MMAs, four of K = 64 a unit
 //   4 warps       accumulators -> row and channel scales -> out, two accumulators in turn
 //   1 warp        rows and row scales of up to kTabs tiles ahead
@@ -56,7 +56,7 @@ struct Cfg {
     // Scales come in batches of 64 bytes a row, four units or eight; the units of two batches
     // lie apart by a few banks more than their atoms, so that the stores of one row's meet
     // other banks.
-    static constexpr int kBatch = 16 / kWords;
+    static constexpr int kBatch = 16 / kWords, kSfBufs = 2;
     static constexpr int kSfStride = kWords * (1 + kHalves) * 512 + 8 * kWords;
     static constexpr int kTabs = 4;                      // tiles whose rows are looked up
     static constexpr int kSfCol = 2 * kCap;              // tensor memory: two accumulators, scales
@@ -67,7 +67,7 @@ struct Cfg {
     static constexpr int kPer = kTmaWarps / kTeams, kGroups = (kRows / 4 + kPer - 1) / kPer;  // warps of a team, copies of a warp
     static constexpr int kTma = kEpi + kEpiWarps, kMma = kTma + kTmaWarps, kLook = kMma + 1;
     static constexpr int kThreads = (kLook + 1) * 32;
-    static constexpr int kSmem = 1024 + kStages * kStage + 2 * kBatch * kSfStride;
+    static constexpr int kSmem = 1024 + kStages * kStage + kSfBufs * kBatch * kSfStride;
     static_assert(kSfCol + kSfA + kSfB <= 512 && kCap % (16 * kCtas) == 0 && kBBytes % 1024 == 0, "tensor memory");
     static_assert(kSfWarps == 4 && kTeams <= kStages && kTmaWarps % kTeams == 0 && kGroups <= 32, "roles");
 };
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
     using C = Cfg<kPair, kNv>;
     constexpr int kCap = C::kCap, kSpan = kNv ? 16 : 32;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * C::kStages + 8 + 2 * C::kTabs];
+    __shared__ uint64_t bars[2 * C::kStages + 2 * C::kSfBufs + 4 + 2 * C::kTabs];
     __shared__ __align__(16) int token_row[C::kTabs][kCap];  // rows of q, or `none`
     __shared__ __align__(8) float token_scale[C::kTabs][kCap];
     __shared__ int first[kMaxExperts + 1];  // token tiles before each expert
@@ -210,20 +210,23 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
     auto landed = [&](int i) { return bar0 + 8u * i; };                     // codes
     auto empty = [&](int i) { return bar0 + 8u * (C::kStages + i); };
     auto scaled = [&](int i) { return bar0 + 8u * (2 * C::kStages + i); };  // a batch of scales
-    auto sf_empty = [&](int i) { return bar0 + 8u * (2 * C::kStages + 2 + i); };
-    auto d_full = [&](int i) { return bar0 + 8u * (2 * C::kStages + 4 + i); };
-    auto d_empty = [&](int i) { return bar0 + 8u * (2 * C::kStages + 6 + i); };
-    auto tab_full = [&](int i) { return bar0 + 8u * (2 * C::kStages + 8 + i); };
-    auto tab_empty = [&](int i) { return bar0 + 8u * (2 * C::kStages + 8 + C::kTabs + i); };
+    auto sf_empty = [&](int i) { return bar0 + 8u * (2 * C::kStages + C::kSfBufs + i); };
+    constexpr int kOther = 2 * (C::kStages + C::kSfBufs);
+    auto d_full = [&](int i) { return bar0 + 8u * (kOther + i); };
+    auto d_empty = [&](int i) { return bar0 + 8u * (kOther + 2 + i); };
+    auto tab_full = [&](int i) { return bar0 + 8u * (kOther + 4 + i); };
+    auto tab_empty = [&](int i) { return bar0 + 8u * (kOther + 4 + C::kTabs + i); };
     volatile int* abort = &abort_flag;
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(landed(i), C::kCtas);
             mbar_init(empty(i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kSfBufs; ++i) {
             mbar_init(scaled(i), C::kCtas * C::kSfWarps);
             mbar_init(sf_empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(d_full(i), 1);
             mbar_init(d_empty(i), C::kCtas * C::kEpiWarps);
         }
@@ -373,8 +376,8 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
         const uint32_t on = elect_lane();
         const int mine = __reduce_max_sync(kAll, rank == 0 && first_tile < tiles ? (tiles - first_tile + tile_step - 1) / tile_step : 0);
         const int units = (a.K + C::kUnit - 1) / C::kUnit;
-        int s = 0, batch = 0;  // batch: of all so far
-        uint32_t phase = 0;
+        int s = 0, buf = 0;  // stage, buffer of scales
+        uint32_t phase = 0, sf_phase = 0;
         bool ready = false;    // stage s has been seen
         for (int n = 0; n < mine && ok; ++n) {
             const uint32_t cols = __reduce_max_sync(kAll, columns(tile_at(first_tile + n * tile_step).count));
@@ -386,11 +389,11 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
             tc_fence_after();
             int unit = 0;  // of the batch
             for (int u = 0; u < units && ok; ++u) {
-                if (unit == 0) ok = __all_sync(kAll, wait_for<kPair>(scaled(batch & 1), (batch >> 1) & 1, abort, a.wait_ns));
+                if (unit == 0) ok = __all_sync(kAll, wait_for<kPair>(scaled(buf), sf_phase, abort, a.wait_ns));
                 if (!ready) ok = ok && __all_sync(kAll, wait_for<kPair>(landed(s), phase, abort, a.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t st = base + s * C::kStage, sf = sf_base + ((batch & 1) * C::kBatch + unit) * C::kSfStride, done = empty(s);
+                const uint32_t st = base + s * C::kStage, sf = sf_base + (buf * C::kBatch + unit) * C::kSfStride, done = empty(s);
                 const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + C::kABytes), fd = desc_sf(sf);
                 const int steps = min(a.K - u * C::kUnit + 63, 256) / 64;
                 if (++s == C::kStages) {
@@ -417,9 +420,12 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
                 }
                 mma_commit_by<kPair>(on, done);
                 if (++unit == C::kBatch || u == units - 1) {
-                    mma_commit_by<kPair>(on, sf_empty(batch & 1));
-                    ++batch;
+                    mma_commit_by<kPair>(on, sf_empty(buf));
                     unit = 0;
+                    if (++buf == C::kSfBufs) {
+                        buf = 0;
+                        sf_phase ^= 1;
+                    }
                 }
                 ready = __all_sync(kAll, seen);
             }
@@ -469,12 +475,14 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
                 ++at_n;
             }
         };
+        int buf = 0;
+        uint32_t phase = 1;
         load();
         const int all = first_tile < tiles ? (tiles - first_tile + tile_step - 1) / tile_step * ((blocks + 63) / 64) : 0;
         for (int batch = 0; batch < all && ok; ++batch) {
-            ok = __all_sync(kAll, wait_for<kPair>(sf_empty(batch & 1), ((batch >> 1) & 1) ^ 1, abort, a.wait_ns));
+            ok = __all_sync(kAll, wait_for<kPair>(sf_empty(buf), phase, abort, a.wait_ns));
             if (!ok) break;
-            const uint32_t to = sf_base + (batch & 1) * C::kBatch * C::kSfStride + (r0 & 31) * 16 + (r0 >> 5) * 4;
+            const uint32_t to = sf_base + buf * C::kBatch * C::kSfStride + (r0 & 31) * 16 + (r0 >> 5) * 4;
 #pragma unroll
             for (int p = 0; p < kParts; ++p)
 #pragma unroll
@@ -487,7 +495,11 @@ __global__ void __launch_bounds__(Cfg<kPair, kNv>::kThreads, 1)
             fence_async_shared();
             __syncwarp();
             if (lane == 0) {
-                if (kPair) mbar_arrive_first(scaled(batch & 1)); else mbar_arrive(scaled(batch & 1));
+                if (kPair) mbar_arrive_first(scaled(buf)); else mbar_arrive(scaled(buf));
+            }
+            if (++buf == C::kSfBufs) {
+                buf = 0;
+                phase ^= 1;
             }
             load();
         }

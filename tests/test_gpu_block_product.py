@@ -254,3 +254,27 @@ def test_offsets_past_32_bits():
         a, b = ends[e], ends[e + 1]
         w, x = values(wq[e], ws[e], fmt), values(q[a:b], s[a:b], fmt)
         check(out[a:b], f64(x @ w.T), f64(x.abs() @ w.abs().T), K, BF16)
+
+
+@pytest.mark.parametrize("form", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("counts", [(5, 0, 37), (1, 16, 15, 33), (500, 3, 0, 700, 225), (2000, 17)])
+def test_adjacent_rows_are_those_of_row_src(form, counts):
+    """Without row_src a tile's rows come in boxes, which take the next segment's rows with them: equal bits
+    to rows looked up one by one, and one bad row stays alone."""
+    K, N, E, R = 352, 264, len(counts), sum(counts)
+    n, fmt = (32, 0) if form == "mxfp4" else (16, 1)
+    g = torch.Generator(device="cuda").manual_seed(R)
+    rand = lambda *shape, top=256: torch.randint(0, top, shape, generator=g, device="cuda", dtype=torch.uint8)
+    q, wq = rand(R, K // 2), rand(E, N, K // 2)
+    s, ws = (rand(*shape, top=16) + (120 if form == "mxfp4" else 48) for shape in ((R, K // n), (E, N, K // n)))
+    bad = R // 2
+    s[bad, 1] = 255 if form == "mxfp4" else 127
+    scale = torch.rand(R, generator=g, device="cuda") if fmt else None
+    offsets = torch.tensor([0, *np.cumsum(counts)], dtype=torch.int32, device="cuda")
+    outs = [torch.zeros(R, N, device="cuda") for _ in range(2)]
+    for out, src in zip(outs, (None, torch.arange(R, dtype=torch.int32, device="cuda"))):
+        bqe.moe_block_product(q, s, wq, ws, out, offsets, src, 1, scale, None, fmt)
+    bqe.moe_check_product()
+    assert torch.equal(outs[0].view(torch.int32), outs[1].view(torch.int32))
+    nan = torch.isnan(outs[0])
+    assert nan[bad].all() and not nan[:bad].any() and not nan[bad + 1:].any()
