@@ -22,8 +22,9 @@
 // Measured at K = N = 4096, bf16 out, the copy rate being 6.78 TB/s: 3000 rows over some 234 of
 // 256 experts 312 us in MXFP4, 332 in NVFP4, 7.4 TB/s; 49152 rows over 256 experts 514 and
 // 549 us, 3.2 and 3.0 PFLOP/s; 8192 rows of one expert 53 and 63 us, 5.2 and 4.4 PFLOP/s.
-// The narrow form is bound by the stream of weights; of six rows of six experts (16 us) the
-// scales' loads, one batch after the other, set the pace: tiles of 64 channels took as long each.
+// The narrow form is bound by the stream of weights; six rows of six experts (16 us) are two
+// rounds of tiles, each some 5 us whatever a tile's height (of 64 channels 20 us in all, of
+// 32 33), of which the scales' loads are 0.5, the MMAs 0.2 and the copies' issue 0.5.
 // The wide one has no single bound left: without the weights' boxes 49152 rows take 9 to 17 %
 // less, without the scales' loads 4 to 7, without the stores 4 to 7, with one MMA of four 4.
 #include <cuda.h>
