@@ -176,11 +176,14 @@ __device__ __forceinline__ void back_dx(const Chunk<A, C>& dy, const Chunk<A, C>
     unpack_chunk(h, w);
     unpack_chunk(gamma, g);
 #pragma unroll
-    for (int i = 0; i < C; ++i) f[i] = r * (f[i] * g[i] - w[i] * r * mean);
+    for (int i = 0; i < C; ++i) f[i] = fmaf(-w[i], r * mean, f[i] * g[i]);
     if (has_dh) {
         unpack_chunk(dh, w);
 #pragma unroll
-        for (int i = 0; i < C; ++i) f[i] += w[i];
+        for (int i = 0; i < C; ++i) f[i] = fmaf(r, f[i], w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) f[i] *= r;
     }
     store_chunk<A, C>(dx, f);
 }
@@ -244,17 +247,21 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? (kWarp && kKeep > 2 ? 2 
 
 // The same for rows in 16-byte words, with the rows on their way held in shared memory, not in
 // registers: a thread copies its own chunks of kDepth rows ahead and reads them back itself, so
-// no barrier is between them.  8192 x 4096 bf16 with dh: 47.6 us, 5.6 TB/s, dgamma's two passes
-// over 7 MB of parts within; with the rows in registers 52 (8192 wide: 50 and 69).  Three rows
-// ahead on three blocks an SM take 51, four on two 48.
-template <typename A, typename G, int kKeep, int kDepth>
-__global__ void __launch_bounds__(256, kKeep <= 2 ? 3 : 1) k_norm_backward_ring(const NormBack<A> a) {
+// no barrier is between them.  A block an SM, of kGroups groups of threads with a row each, whose
+// shares of dgamma meet in shared memory.  8192 x 4096 bf16 with dh: 45.6 us, 5.9 TB/s, dgamma's
+// passes over 2.5 MB of parts within; with the rows in registers 52 (8192 wide: 50 and 69).
+// Two groups and 128 registers there (three: 57; three blocks an SM 46.8; three rows ahead
+// 46.2), three groups with half the chunks (8192 x 2048: 28.3; three blocks an SM 33, four groups 34).
+template <typename A, typename G, int kKeep, int kDepth, int kGroups>
+__global__ void __launch_bounds__(256 * kGroups, 1) k_norm_backward_ring(const NormBack<A> a) {
     constexpr int C = 16 / (int)sizeof(A);
     extern __shared__ __align__(16) uint4 ring[];  // [kDepth][3][kKeep][blockDim.x]
-    __shared__ float part[2][32];
+    __shared__ float part[2][kGroups][8];
     pdl_launch_dependents();
     pdl_wait();
-    const int first = threadIdx.x * C, step = blockDim.x * C, H = a.H;
+    const int threads = blockDim.x / kGroups, group = threadIdx.x / threads, id = threadIdx.x % threads;
+    const int first = id * C, step = threads * C, H = a.H;
+    const long long start = (long long)blockIdx.x * kGroups + group, rows = (long long)gridDim.x * kGroups;
     Chunk<G, C> gamma[kKeep];
     float dgamma[kKeep][C] = {};
 #pragma unroll
@@ -278,9 +285,9 @@ __global__ void __launch_bounds__(256, kKeep <= 2 ? 3 : 1) k_norm_backward_ring(
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i) ahead(blockIdx.x + (long long)i * gridDim.x, i);
+    for (int i = 0; i < kDepth; ++i) ahead(start + i * rows, i);
     int turn = 0, slot = 0;
-    for (long long t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+    for (long long t = start; t < a.T; t += rows, turn ^= 1) {
         const float r = a.rstd[t];
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
         Chunk<A, C> dy[kKeep], h[kKeep], dh[kKeep];
@@ -291,21 +298,36 @@ __global__ void __launch_bounds__(256, kKeep <= 2 ? 3 : 1) k_norm_backward_ring(
             *reinterpret_cast<uint4*>(&h[n]) = ring[at(slot, 1, n)];
             if (a.dh) *reinterpret_cast<uint4*>(&dh[n]) = ring[at(slot, 2, n)];
         }
-        ahead(t + (long long)kDepth * gridDim.x, slot);
+        ahead(t + kDepth * rows, slot);
         slot = slot + 1 == kDepth ? 0 : slot + 1;
         float dot = 0.f;
 #pragma unroll
         for (int n = 0; n < kKeep; ++n)
             if (first + n * step < H) back_dot(dy[n], h[n], gamma[n], r, dot, dgamma[n]);
-        const float mean = block_sum(dot, part[turn]) / (float)H;  // of g h r
+        dot = warp_sum(dot);
+        if (id % 32 == 0) part[turn][group][id / 32] = dot;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");  // the group's own
+        dot = 0.f;
+        for (int i = 0; i < threads / 32; ++i) dot += part[turn][group][i];
+        const float mean = dot / (float)H;  // of g h r
 #pragma unroll
         for (int n = 0; n < kKeep; ++n)
             if (first + n * step < H) back_dx(dy[n], h[n], gamma[n], dh[n], a.dh != nullptr, r, mean, a.dx + t * a.dxs + first + n * step);
     }
-    if (a.part) {
+    if (!a.part) return;
+    // the groups' shares of dgamma, summed in their order: the ring has room for them
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(ring);
 #pragma unroll
-        for (int n = 0; n < kKeep; ++n)
-            if (first + n * step < H) store_chunk<float, C>(a.part + (long long)blockIdx.x * H + first + n * step, dgamma[n]);
+    for (int n = 0; n < kKeep; ++n)
+        if (first + n * step < H) store_chunk<float, C>(sums + group * H + first + n * step, dgamma[n]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < H; c += blockDim.x) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) sum += sums[i * H + c];
+        a.part[(long long)blockIdx.x * H + c] = sum;
     }
 }
 
@@ -359,8 +381,7 @@ __global__ void __launch_bounds__(1024) k_join_parts(const float* part, int part
 
 // ----------------------------------------------------------------- launches --
 // Blocks of the gradient at most: three an SM of 256 threads, and more of the smaller ones
-// (8192 x 1024 bf16: 29 us with 456, 20 with 912; 2048 wide 33 and 33; 8192 x 4096: 47.6 and
-// 51).  fp32 rows are twice as long and take 456 (8192 x 1024: 28 for 30; 2048 wide 44 for 47).
+// (8192 x 1024 bf16: 29 us with 456, 20 with 912).
 // Rows past 16384 are long whatever their type.
 constexpr int kLongParts = 16;
 int most_parts(int H) { return H <= 2048 ? 912 : H <= 16384 ? 456 : kLongParts; }
@@ -400,18 +421,18 @@ cudaError_t norm_c(const Norm<A>& a, cudaStream_t s) {
     return launch_pdl(k_norm_rows<A, G, C, 0, 1024, false>, dim3(a.T), dim3(1024), 0, s, a);
 }
 
-template <typename A, typename G, int kKeep, int kDepth>
+template <typename A, typename G, int kKeep, int kDepth, int kGroups>
 cudaError_t back_ring(const NormBack<A>& a, int parts, int threads, cudaStream_t s) {
-    auto* kernel = k_norm_backward_ring<A, G, kKeep, kDepth>;
-    const int smem = kDepth * 3 * kKeep * threads * 16;
+    auto* kernel = k_norm_backward_ring<A, G, kKeep, kDepth, kGroups>;
+    const int smem = kDepth * 3 * kKeep * kGroups * threads * 16;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return e != cudaSuccess ? e : launch_pdl(kernel, dim3(parts), dim3(threads), smem, s, a);
+    return e != cudaSuccess ? e : launch_pdl(kernel, dim3(parts), dim3(kGroups * threads), smem, s, a);
 }
 
 template <typename A, typename G, int C>
 cudaError_t back_c(const NormBack<A>& a, float* dgamma, cudaStream_t s) {
     const int chunks = (a.H + C - 1) / C;
-    const int most = sizeof(A) == 4 && chunks > 128 && a.H <= 16384 ? 456 : most_parts(a.H);
+    const int most = most_parts(a.H);
     int parts = a.T < most ? a.T : most;
     cudaError_t e = cudaSuccess;
     if (a.T == 0) {
@@ -421,10 +442,11 @@ cudaError_t back_c(const NormBack<A>& a, float* dgamma, cudaStream_t s) {
         if (chunks <= 32) e = launch_pdl(k_norm_backward<A, G, C, 1, 256, true>, grid, dim3(256), 0, s, a);
         else if (chunks <= 64) e = launch_pdl(k_norm_backward<A, G, C, 2, 256, true>, grid, dim3(256), 0, s, a);
         else if constexpr (C <= 4) e = launch_pdl(k_norm_backward<A, G, C, 4, 256, true>, grid, dim3(256), 0, s, a);
-    } else if (C == 16 / (int)sizeof(A) && a.T > most && chunks > 128 && chunks <= 1024) {
-        if (chunks <= 256) e = back_ring<A, G, 1, 4>(a, parts, threads_for(chunks), s);
-        else if (chunks <= 512) e = back_ring<A, G, 2, 2>(a, parts, threads_for((chunks + 1) / 2), s);
-        else e = back_ring<A, G, 4, 2>(a, parts = 152, threads_for((chunks + 3) / 4), s);
+    } else if (C == 16 / (int)sizeof(A) && a.T > 456 && chunks > 128 && chunks <= 1024) {
+        parts = 152;
+        if (chunks <= 256) e = back_ring<A, G, 1, 3, 3>(a, parts, threads_for(chunks), s);
+        else if (chunks <= 512) e = back_ring<A, G, 2, 2, 2>(a, parts, threads_for((chunks + 1) / 2), s);
+        else e = back_ring<A, G, 4, 2, 1>(a, parts, threads_for((chunks + 3) / 4), s);
     } else if (chunks <= 2048) {
         const dim3 grid(parts);
         if (chunks <= 256) e = launch_pdl(k_norm_backward<A, G, C, 1, 256, false>, grid, dim3(threads_for(chunks)), 0, s, a);

@@ -265,3 +265,12 @@ def test_short_rows_in_place(T, H):
     stream = res.clone()
     bqe.moe_norm_rows(x, gamma, y, 1e-6, stream, stream)
     assert torch.equal(stream, h0) and torch.equal(y, y0)
+
+
+# Rows of 129 to 1024 chunks of 16 bytes, more of them than fit at once: the last rows of each group of threads
+@pytest.mark.parametrize("T,H,pad", [(457, 2048, 0), (611, 1096, 8), (913, 1536, 0), (500, 4088, 8), (610, 2056, 0),
+                                     (458, 8192, 0), (760, 4096, 0)])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_backward_of_many_rows(T, H, pad, dtype):
+    test_norm_rows_backward(T, H, pad, dtype, F32, True)
+    test_norm_rows_backward(T, H, pad, dtype, dtype, False)
