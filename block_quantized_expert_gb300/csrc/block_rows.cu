@@ -289,7 +289,9 @@ __device__ __forceinline__ void store_unit(O* p, const float (&f)[kUnit]) {
 
 // (code s) g, one rounding in fp32 and one to the rows' type.  blockDim.y rows a block,
 // blockDim.x threads each, four units a thread on their way at once.  NVFP4: code times
-// e4m3 has six bits at most and is exact in fp16; MXFP4: s, a power of two, times g is exact.
+// e4m3 has six bits at most and is exact in fp16; MXFP4: code times s, a power of two, is exact
+// in fp32 up to 2^125 (in subnormals, too), and from there on s lends g three bits.  s g is not
+// formed: it can overflow, or lose bits, where code s g does neither.
 template <typename O, bool kNv, bool kWide>
 __global__ void __launch_bounds__(256) k_dequantize_blocks(const Dequantize<O> a) {
     pdl_launch_dependents();
@@ -324,7 +326,9 @@ __global__ void __launch_bounds__(256) k_dequantize_blocks(const Dequantize<O> a
             if (u >= units) break;
             float f[kUnit];
             const __half2 sh = __half2half2(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte[n], __NV_E4M3)));
-            const float by = kNv ? g : ue8m0_value(byte[n]) * g;
+            const float e8 = ue8m0_value(byte[n]);
+            const bool lend = !kNv && byte[n] > 252u;
+            const float by = lend && fabsf(g) < 0x1p125f ? 8.f * g : g, p = lend ? 0.125f * e8 : e8;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t c[4];
@@ -336,7 +340,8 @@ __global__ void __launch_bounds__(256) k_dequantize_blocks(const Dequantize<O> a
                 for (int i = 0; i < 4; ++i) {
                     __half2 v2 = *reinterpret_cast<const __half2*>(&c[i]);
                     if (kNv) v2 = __hmul2(v2, sh);
-                    const float2 v = __half22float2(v2);
+                    float2 v = __half22float2(v2);
+                    if (!kNv) v = make_float2(v.x * p, v.y * p);
                     f[8 * h + 2 * i] = v.x * by;
                     f[8 * h + 2 * i + 1] = v.y * by;
                 }
