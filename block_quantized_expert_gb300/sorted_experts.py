@@ -65,6 +65,15 @@ def quantize_weights(w: torch.Tensor):
     return wq, scale
 
 
+def _check_call(rows, H: int, s: Sorted, w: torch.Tensor, name: str = "x") -> None:
+    """The tokens' rows, their routing and its weights are of one batch: a token past the last row
+    would be read as zeros by the products."""
+    if w.dim() != 2 or w.shape != s.ids.shape:
+        raise ValueError(f"w must have the ids' shape {tuple(s.ids.shape)}, got {tuple(w.shape)}")
+    if rows.shape != (w.shape[0], H):
+        raise ValueError(f"{name} must have shape ({w.shape[0]}, {H}), got {tuple(rows.shape)}")
+
+
 class Int8Experts:
     """SwiGLU experts with 8-bit integer weights: gate and up [E][I][H], down [E][H][I].
 
@@ -88,6 +97,9 @@ class Int8Experts:
 
         Asynchronous: whether a device-side wait of the products ran out, which leaves
         the output undefined, is what moe_check_product tells, and the caller asks it."""
+        _check_call(x, self.H, s, w)
+        if codes is not None:
+            _check_call(codes[0], self.H, s, w, "codes")
         T, k = w.shape
         R, dev = T * k, x.device
         if codes is None:
@@ -160,6 +172,7 @@ class BlockExperts:
     def __call__(self, x: torch.Tensor, s: Sorted, w: torch.Tensor) -> torch.Tensor:
         """x [T][H] in bf16, fp16 or fp32; w [T][k] the routing weights; fp32 [T][H].
         Asynchronous, as Int8Experts is: moe_check_product is its caller's."""
+        _check_call(x, self.H, s, w)
         T, k = w.shape
         R, dev = T * k, x.device
         gu = torch.empty((R, 2 * self.I), dtype=self.rows, device=dev)
