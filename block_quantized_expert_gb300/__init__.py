@@ -166,6 +166,15 @@ if _HAS_TORCH:
     _ROW_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.int8: None}
 
 
+_MOST = (1 << 31) - 1
+
+
+def _sizes(*sizes):
+    """Refuses what the library's 32-bit arguments would hold only the low bits of."""
+    if max(sizes) > _MOST:
+        raise ValueError(f"sizes must be below 2^31, got {sizes}")
+
+
 def _rows(t, name, rows=None, width=None):
     """(pointer, moe_dtype, stride) of a 2-D CUDA tensor of rows whose elements
     are adjacent; the moe_dtype of int8 rows is None."""
@@ -176,6 +185,8 @@ def _rows(t, name, rows=None, width=None):
         raise ValueError(f"{name} must be a 2-D tensor of rows in float32, bfloat16, float16 or int8, "
                          f"got {t.dtype} {tuple(shape)}")
     n, m = shape
+    if n > _MOST or m > _MOST:
+        _sizes(n, m)
     if (rows is not None and n != rows) or (width is not None and m != width):
         raise ValueError(f"{name} must have shape ({n if rows is None else rows}, {m if width is None else width}), "
                          f"got {tuple(shape)}")
@@ -354,6 +365,7 @@ def moe_permute_noalloc(ids, n_experts: int, offsets, row_src, row_dst, stream=N
     """The grouping of moe_permute without a layer and without allocating
     (scratch in a static device array; T * top_k <= 65536)."""
     T, k = ids.shape
+    _sizes(T, k, n_experts)
     R = T * k
     st = load_library().moe_permute_noalloc(
         _ptr(ids, torch.int32, (T, k), "ids"), T, k, n_experts,
@@ -365,13 +377,14 @@ def moe_permute_noalloc(ids, n_experts: int, offsets, row_src, row_dst, stream=N
 
 def moe_permute_scratch_bytes(T: int, top_k: int, n_experts: int) -> int:
     """Bytes of scratch of moe_permute_scratch; 0 for sizes that it does not take."""
-    return load_library().moe_permute_scratch_bytes(T, top_k, n_experts)
+    return load_library().moe_permute_scratch_bytes(T, top_k, n_experts) if max(T, top_k, n_experts) <= _MOST else 0
 
 
 def moe_permute_scratch(ids, n_experts: int, offsets, row_src, row_dst, scratch, stream=None):
     """The grouping of moe_permute without a layer, in the caller's scratch (a CUDA
     uint8 tensor of moe_permute_scratch_bytes); calls share nothing."""
     T, k = ids.shape
+    _sizes(T, k, n_experts)
     R = T * k
     st = load_library().moe_permute_scratch(
         _ptr(ids, torch.int32, (T, k), "ids"), T, k, n_experts,
@@ -564,6 +577,7 @@ def moe_route_backward(logits, ids, dw, dlogits, w_scale: float = 1.5, stream=No
     k = ids.shape[1]
     if T == 0:
         return
+    _sizes(T, E, k)
     lib = _lib or load_library()
     st = lib.moe_route_backward(_ptr(logits, torch.float32, (T, E), "logits"),
                                 _ptr(ids, torch.int32, (T, k), "ids"), _ptr(dw, torch.float32, (T, k), "dw"),
@@ -601,6 +615,9 @@ def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, t
     if wq.dim() != 3:
         raise ValueError(f"wq must have shape (E, N, K), got {tuple(wq.shape)}")
     E, _, K = wq.shape
+    top_k = int(top_k)
+    if E | top_k > _MOST:
+        _sizes(E, top_k)
     pq, dtq, sq = _rows(q, "q", None, K)
     po, dto, so = _rows(out, "out")
     if dtq is not None or dto is None:
@@ -612,7 +629,7 @@ def moe_expert_product(q, scale, wq, w_scale, out, offsets=None, row_src=None, t
                                 _ptr(w_scale, torch.float32, (E, N), "w_scale"), E, N,
                                 None if offsets is None else _ptr(offsets, torch.int32, (E + 1,), "offsets"),
                                 None if row_src is None else _ptr(row_src, torch.int32, (R,), "row_src"),
-                                int(top_k), R, po, dto, so, _here(stream, q, scale, wq, w_scale, out, offsets, row_src))
+                                top_k, R, po, dto, so, _here(stream, q, scale, wq, w_scale, out, offsets, row_src))
     if st:
         _check(st)
 
@@ -655,6 +672,8 @@ def moe_norm_rows(x, gamma, y, eps: float = 1e-6, residual=None, h=None, rstd=No
     T, H = shape = x.shape
     if T == 0:
         return
+    if T > _MOST or H > _MOST:
+        _sizes(T, H)
     dt = _ROW_TYPES.get(x.dtype)
     dev = _device_of(x)
     if stream is None and dt is not None and dev >= 0:
@@ -696,7 +715,7 @@ def moe_norm_rows(x, gamma, y, eps: float = 1e-6, residual=None, h=None, rstd=No
 
 def moe_norm_scratch_bytes(T: int, hidden: int) -> int:
     """Bytes of scratch of moe_norm_rows_backward with dgamma; 0 for sizes that it does not take."""
-    return (_lib or load_library()).moe_norm_scratch_bytes(T, hidden)
+    return (_lib or load_library()).moe_norm_scratch_bytes(T, hidden) if T <= _MOST and hidden <= _MOST else 0
 
 
 def moe_norm_rows_backward(dy, h, gamma, rstd, dx, dgamma=None, scratch=None, dh=None, stream=None):
@@ -704,6 +723,8 @@ def moe_norm_rows_backward(dy, h, gamma, rstd, dx, dgamma=None, scratch=None, dh
     residual stream goes on, dh; h and rstd as moe_norm_rows gave them.  dgamma needs scratch, a
     CUDA uint8 tensor of moe_norm_scratch_bytes."""
     T, H = shape = h.shape
+    if T > _MOST or H > _MOST:
+        _sizes(T, H)
     dt = _ROW_TYPES.get(h.dtype)
     dev = _device_of(h)
     if stream is None and dt is not None and T and dev >= 0:
@@ -748,6 +769,7 @@ def _codes(q, name, rows=None, K=None):
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dtype != torch.uint8 or q.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA uint8 tensor of codes, two a byte")
     n, half = q.shape
+    _sizes(n, 2 * half)
     if (rows is not None and n != rows) or (K is not None and 2 * half != K):
         raise ValueError(f"{name} must have shape ({rows}, {K // 2}), got {tuple(q.shape)}")
     step, inner = q.stride()
@@ -771,7 +793,7 @@ def moe_quantize_blocks(x, q, s, scale=None, fmt: int = MOE_WEIGHTS_NVFP4, gated
     rows, half = shape = q.shape if q.dim() == 2 else (0, 0)
     dt = _ROW_TYPES.get(x.dtype)
     dev = _device_of(x)
-    if stream is None and dt is not None and rows and dev >= 0:
+    if stream is None and dt is not None and 0 < rows <= _MOST and half < 1 << 30 and dev >= 0:
         K = 2 * half
         width = 2 * K if gated else K
         p = [_dense(dev, x, x.dtype, (rows, width)), _dense(dev, q, torch.uint8, shape),
@@ -803,7 +825,7 @@ def moe_dequantize_blocks(q, s, x, scale=None, fmt: int = MOE_WEIGHTS_NVFP4, str
     rows, half = shape = q.shape if q.dim() == 2 else (0, 0)
     dt = _ROW_TYPES.get(x.dtype)
     dev = _device_of(x)
-    if stream is None and dt is not None and rows and dev >= 0:
+    if stream is None and dt is not None and 0 < rows <= _MOST and half < 1 << 30 and dev >= 0:
         K = 2 * half
         p = [_dense(dev, x, x.dtype, (rows, K)), _dense(dev, q, torch.uint8, shape), _dense(dev, s, torch.uint8, (rows, K // n)),
              None if scale is None else _dense(dev, scale, torch.float32, (rows,))]
@@ -840,12 +862,13 @@ def moe_block_product(q, s, wq, ws, out, offsets=None, row_src=None, top_k: int 
     if wq.dim() != 3:
         raise ValueError(f"wq must have shape (E, N, K / 2), got {tuple(wq.shape)}")
     E, _, half = wq.shape
-    K = 2 * half
+    K, rows, top_k = 2 * half, q.shape[0], int(top_k)
+    if R | N | E | K | rows | top_k > _MOST:
+        _sizes(R, N, E, K, rows, top_k)
     dt = _ROW_TYPES.get(out.dtype)
     dev = _device_of(out)
     if stream is None and dt is not None and dev >= 0:
         u, f, i = torch.uint8, torch.float32, torch.int32
-        rows = q.shape[0]
         p = [_dense(dev, q, u, (rows, half)), _dense(dev, s, u, (rows, K // n)), _dense(dev, wq, u, (E, N, half)),
              _dense(dev, ws, u, (E, N, K // n)), _dense(dev, out, out.dtype, (R, N)),
              None if scale is None else _dense(dev, scale, f, (rows,)), None if w_scale is None else _dense(dev, w_scale, f, (E, N)),
@@ -857,7 +880,7 @@ def moe_block_product(q, s, wq, ws, out, offsets=None, row_src=None, top_k: int 
             if st:
                 _check(st)
             return
-    pq, sq, rows, _ = _codes(q, "q", q.shape[0], K)
+    pq, sq, _, _ = _codes(q, "q", rows, K)
     po, dto, so = _rows(out, "out")
     if dto is None:
         raise ValueError("out must be a floating tensor")
@@ -867,7 +890,7 @@ def moe_block_product(q, s, wq, ws, out, offsets=None, row_src=None, top_k: int 
                                _ptr(wq, torch.uint8, (E, N, half), "wq"), _ptr(ws, torch.uint8, (E, N, K // n), "ws"),
                                None if w_scale is None else _ptr(w_scale, torch.float32, (E, N), "w_scale"), E, N,
                                None if offsets is None else _ptr(offsets, torch.int32, (E + 1,), "offsets"),
-                               None if row_src is None else _ptr(row_src, torch.int32, (R,), "row_src"), int(top_k), R,
+                               None if row_src is None else _ptr(row_src, torch.int32, (R,), "row_src"), top_k, R,
                                po, dto, so, _here(stream, q, s, scale, wq, ws, w_scale, out, offsets, row_src))
     if st:
         _check(st)
