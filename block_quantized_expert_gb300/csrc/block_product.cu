@@ -105,12 +105,13 @@ __global__ void __launch_bounds__(128) k_block_product_few(const BlockProduct a)
 #pragma unroll
         for (int r = 0; r < kFew; ++r) {
             if (r >= rows) break;
-            uint4 x = {};  // no row: zeros, which a channel with a NaN byte still makes NaN
-            float2 xs = {};
-            if (src[r] >= 0) {
-                x = reinterpret_cast<const uint4*>(a.q + src[r] * a.qs)[i];
-                xs = lane_scales<kNv>(a.s + (long long)src[r] * blocks, i);
+            if (src[r] < 0) {  // no row: zeros, which a channel with a NaN byte still makes NaN
+#pragma unroll
+                for (int c = 0; c < kChan; ++c) acc[c][r] = fmaf(0.f, by[c].x, fmaf(0.f, by[c].y, acc[c][r]));
+                continue;
             }
+            const uint4 x = reinterpret_cast<const uint4*>(a.q + src[r] * a.qs)[i];
+            const float2 xs = lane_scales<kNv>(a.s + (long long)src[r] * blocks, i);
             const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int c = 0; c < kChan; ++c) {
