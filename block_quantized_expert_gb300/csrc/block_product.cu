@@ -146,8 +146,15 @@ __global__ void __launch_bounds__(128) k_block_product_few(const BlockProduct a)
     }
 }
 
-// At K = N = 4096 one position of one expert takes 5.4 us here and 8.6 on the tensor cores, two
-// 8.7 and 8.6 (7.9 with four positions a warp), four 11.3 and 8.6; six of six experts 17.2 and 16.1.
+// Here and on the tensor cores, NVFP4, us (each call's weights from HBM):
+//   K x N         one position   two of one expert   two of two experts
+//   4096 x 4096   6.6            10.0 / 8.6          7.8 / 9.7
+//   2048 x 4096   4.4             6.3 / 6.8          5.1 / 7.6
+//   4096 x 1024   5.4             7.3 / 8.6          5.9 / 8.8
+//   512 x 512     2.4             3.1 / 5.3          2.6 / 5.6
+// MXFP4 at 4096 x 4096 10.9 / 8.0 and 9.1 / 9.0: two positions of one large expert alone lose, and which
+// experts they are of is on the device.  One position of 4096 x 4096 takes 8.6 on the tensor cores; four take 11.3
+// and 8.6 with two positions a warp, six of six experts 17.2 and 16.1.
 bool few_rows(const BlockProduct& a) { return a.R <= 2; }
 
 cudaError_t launch_few(const BlockProduct& a, bool nv, moe_dtype out, cudaStream_t s) {
