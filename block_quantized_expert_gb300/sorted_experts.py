@@ -132,12 +132,14 @@ def quantize_block_weights(w: torch.Tensor, fmt: int = bqe.MOE_WEIGHTS_NVFP4):
 
 def quantize_layer_weights(w: torch.Tensor, fmt: int = bqe.MOE_WEIGHTS_MXFP4):
     """[E][N][K] weights to the tensors that moe_create takes for one of its matrices: codes,
-    scale bytes and, for NVFP4, one float32 scale a matrix [E] (max|w| / 2688), else None."""
+    scale bytes and, for NVFP4, one float32 scale a matrix [E] (max|w| / 2688), else None.  All of a
+    matrix with an infinity or a NaN comes back as NaN (MXFP4: the block that holds it)."""
     if fmt != bqe.MOE_WEIGHTS_NVFP4:
         return quantize_block_weights(w, fmt)
     E, N, K = w.shape
     most = w.abs().amax((1, 2)).float()
-    g = torch.where(most > 0, most / torch.full_like(most, 2688.0), 1.0)  # a quotient, not a product with 1 / 2688
+    # a quotient, not a product with 1 / 2688; NaN of a matrix that holds one
+    g = torch.where(most == 0, 1.0, most / torch.full_like(most, 2688.0))
     q = torch.empty((E, N, K // 2), dtype=torch.uint8, device=w.device)
     s = torch.empty((E, N, K // 16), dtype=torch.uint8, device=w.device)
     bqe.moe_quantize_blocks(w.reshape(E * N, K), q.view(E * N, -1), s.view(E * N, -1), g.repeat_interleave(N), fmt, given=True)
