@@ -13,6 +13,7 @@
 
 #include "block_product.cuh"
 #include "int_product.cuh"
+#include "row_bytes.cuh"
 #include "row_codes.cuh"
 
 namespace moe {
@@ -197,23 +198,22 @@ __global__ void __launch_bounds__(128) k_product_few(const Product a) {
 // 64 channels, 64 bytes of K at a time through shared memory, 4 x 4 sums a thread
 // by __dp4a (exact 32-bit integers): 8192 rows, K = N = 1000, 166 us (bound by the
 // issue of loads and sums, 0.1 PFLOP/s).  kWords: K, stride and bases allow four codes a
-// load, else they are shifted together from two (as single bytes 777 rows at K = 1101, N = 1001
-// took 78 us for 35 at K = 1100).
+// load, else they are shifted together from two (777 rows at K = 1101, N = 1001: 53 us, as single bytes 78;
+// 51 at K = 1100).  Three blocks an SM there, 80 registers: left to itself the compiler takes 64, in which
+// fewer loads are on their way (66 us; 2000 rows at K = 2047, N = 2048 254 for 212), two blocks lose (53, 311).
+struct Rows {
+    const int8_t *lo, *hi;  // the matrix
+};
+
 template <bool kWords>
-__device__ __forceinline__ int codes4(const int8_t* row, int c, int K) {
+__device__ __forceinline__ int codes4(const int8_t* row, int c, int K, bool inside, const Rows& m) {
     if (row == nullptr || c >= K) return 0;
     if (kWords) return *reinterpret_cast<const int*>(row + c);
-    // the one or two aligned words that hold them, and no word without one of them
-    const int8_t* p = row + c;
-    const int off = (int)((uintptr_t)p & 3), n = K - c;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(p - off);
-    const uint32_t lo = w[0], hi = off && n > 4 - off ? w[1] : 0u;
-    const uint32_t v = __funnelshift_r(lo, hi, 8 * off);
-    return (int)(n < 4 ? v & ((1u << (8 * n)) - 1u) : v);
+    return (int)row_bytes4<PlainLoads>(row, c, K, inside, m.lo, m.hi);
 }
 
 template <typename O, bool kWords>
-__global__ void __launch_bounds__(256) k_product_any(const Product a) {
+__global__ void __launch_bounds__(256, kWords ? 0 : 3) k_product_any(const Product a) {
     pdl_launch_dependents();
     pdl_wait();
     constexpr int kTile = 64;
@@ -250,12 +250,14 @@ __global__ void __launch_bounds__(256) k_product_any(const Product a) {
         xrow[i] = src[r] >= 0 ? a.q + src[r] * a.qs : nullptr;
         wrow[i] = n0 + r < a.N ? a.wq + ((long long)e * a.N + n0 + r) * a.K : nullptr;
     }
+    const Rows q = {a.q, a.q + (a.rows - 1) * a.qs + a.K}, w = {a.wq, a.wq + (long long)a.E * a.N * a.K};
     int acc[4][4] = {};
     for (int k0 = 0; k0 < a.K; k0 += 64) {
+        const bool inside = k0 > 0 && k0 + 68 <= a.K;  // all words here are inside their rows
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            xs[lr + 16 * i][lw] = codes4<kWords>(xrow[i], k0 + 4 * lw, a.K);
-            ws[lr + 16 * i][lw] = codes4<kWords>(wrow[i], k0 + 4 * lw, a.K);
+            xs[lr + 16 * i][lw] = codes4<kWords>(xrow[i], k0 + 4 * lw, a.K, inside, q);
+            ws[lr + 16 * i][lw] = codes4<kWords>(wrow[i], k0 + 4 * lw, a.K, inside, w);
         }
         __syncthreads();
 #pragma unroll
