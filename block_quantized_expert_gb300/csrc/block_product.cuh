@@ -30,8 +30,7 @@ __device__ __forceinline__ int source_row(const BlockProduct& a, int p) {
 
 // The tensor-core form (block_product_tc.cu): q and wq 16-byte aligned, qs a multiple of 16.
 cudaError_t launch_block_product_tc(const BlockProduct& a, bool nv, moe_dtype out, cudaStream_t s);
-// Its sticky error flag (common.cuh), taken (read and cleared in one step) after the
-// stream's work.
-cudaError_t block_product_flag(uint32_t* flag, cudaStream_t s);
+// Where the current device has its sticky error flag (common.cuh).
+cudaError_t block_product_flag_at(uint32_t** flag);
 
 }  // namespace moe

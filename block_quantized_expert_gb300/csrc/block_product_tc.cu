@@ -151,9 +151,6 @@ struct Tile {
 };
 
 __device__ uint32_t g_block_err;   // sticky, taken by moe_check_product
-__device__ uint32_t g_block_seen;  // what the check under way has taken
-
-__global__ void k_take_block_flag() { g_block_seen = atomicExch(&g_block_err, 0u); }
 
 // 16 scale bytes of one row from byte `at` on, zeros from byte `all` on: no row (nullptr)
 // is all zeros.  bytes: 16, 4 or 2 where every row's pieces of that size are whole and aligned.
@@ -673,15 +670,7 @@ cudaError_t launch_o(const BlockProduct& a, const CUtensorMap& wmap, const CUten
 
 }  // namespace
 
-cudaError_t block_product_flag(uint32_t* flag, cudaStream_t s) {
-    static std::mutex lock;  // one check at a time: they share g_block_seen
-    std::lock_guard<std::mutex> hold(lock);
-    k_take_block_flag<<<1, 1, 0, s>>>();
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(flag, g_block_seen, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
-    const cudaError_t done = cudaStreamSynchronize(s);
-    return e == cudaSuccess ? done : e;
-}
+cudaError_t block_product_flag_at(uint32_t** flag) { return cudaGetSymbolAddress((void**)flag, g_block_err); }
 
 cudaError_t launch_block_product_tc(const BlockProduct& a, bool nv, moe_dtype out, cudaStream_t s) {
     CUtensorMap wmap, qmap;

@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <mutex>
 
 #include "block_product.cuh"
 #include "int_product.cuh"
@@ -364,6 +365,29 @@ cudaError_t product_o(const Product& a, cudaStream_t s) {
     return e;
 }
 
+__device__ uint32_t g_taken;  // what the check under way has found: 1 and 2 for the two flags
+
+// Both flags, read and cleared in one step each.
+__global__ void k_take_flags(uint32_t* ints, uint32_t* blocks) {
+    const uint32_t a = atomicExch(ints, 0u), b = atomicExch(blocks, 0u);
+    g_taken = (a ? 1u : 0u) | (b ? 2u : 0u);
+}
+
+// The flags of both products, taken after the stream's work.
+cudaError_t take_flags(uint32_t* out, cudaStream_t s) {
+    static std::mutex lock;  // one check at a time: they share g_taken
+    std::lock_guard<std::mutex> hold(lock);
+    uint32_t *ints = nullptr, *blocks = nullptr;
+    cudaError_t e = product_flag_at(&ints);
+    if (e == cudaSuccess) e = block_product_flag_at(&blocks);
+    if (e != cudaSuccess) return e;
+    k_take_flags<<<1, 1, 0, s>>>(ints, blocks);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(out, g_taken, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
+    const cudaError_t done = cudaStreamSynchronize(s);
+    return e == cudaSuccess ? done : e;
+}
+
 }  // namespace
 
 bool take_product_stall() { return g_stall_next.exchange(false); }
@@ -431,13 +455,11 @@ extern "C" moe_status moe_expert_product(const int8_t* q, long long q_stride, in
 
 extern "C" moe_status moe_check_product(moe_stream_t stream) {
     const char* what = "moe_check_product";
-    uint32_t flag = 0, blocks = 0;
-    cudaError_t e = product_flag(&flag, (cudaStream_t)stream);
-    if (e == cudaSuccess) e = block_product_flag(&blocks, (cudaStream_t)stream);
+    uint32_t out = 0;
+    const cudaError_t e = take_flags(&out, (cudaStream_t)stream);
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    if (flag) return fail(MOE_ERR_TIMEOUT, "%s: a device-side wait of moe_expert_product ran out", what);
-    if (blocks) return fail(MOE_ERR_TIMEOUT, "%s: a device-side wait of moe_block_product ran out", what);
-    return MOE_OK;
+    const char* names[] = {"moe_expert_product", "moe_block_product", "moe_expert_product and one of moe_block_product"};
+    return out ? fail(MOE_ERR_TIMEOUT, "%s: a device-side wait of %s ran out", what, names[out - 1]) : MOE_OK;
 }
 
 extern "C" moe_status moe_test_stall_next_product(void) {

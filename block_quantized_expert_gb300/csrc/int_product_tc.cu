@@ -144,11 +144,8 @@ struct Tile {
 };
 
 __device__ uint32_t g_product_err;   // sticky, taken by moe_check_product
-__device__ uint32_t g_product_seen;  // what the check under way has taken
 
 // Reads and clears the flag in one step: what is raised after it stays for the next.
-__global__ void k_take_flag() { g_product_seen = atomicExch(&g_product_err, 0u); }
-
 template <bool kPair, typename O>
 __global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1) k_product_tc(const Product a, const __grid_constant__ CUtensorMap wmap) {
     using C = Cfg<kPair>;
@@ -682,15 +679,7 @@ cudaError_t launch_o(const Product& a, const CUtensorMap& map, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t product_flag(uint32_t* flag, cudaStream_t s) {
-    static std::mutex lock;  // one check at a time: they share g_product_seen
-    std::lock_guard<std::mutex> hold(lock);
-    k_take_flag<<<1, 1, 0, s>>>();
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(flag, g_product_seen, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
-    const cudaError_t done = cudaStreamSynchronize(s);
-    return e == cudaSuccess ? done : e;
-}
+cudaError_t product_flag_at(uint32_t** flag) { return cudaGetSymbolAddress((void**)flag, g_product_err); }
 
 bool product_tc_fits(const Product& a) {
     return a.rows > 0 && a.K % 16 == 0 && a.qs % 16 == 0 && a.rows * (a.qs / 16) < 0xFFFFFFFFLL && (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.wq % 16 == 0;
