@@ -202,6 +202,8 @@ extern "C" moe_status moe_block_product(const uint8_t* q, long long q_stride, in
         return refuse(MOE_ERR_INVALID_ARG, "%s: q and wq must be aligned to 16 bytes", what);
     if ((uintptr_t)out % dtype_size(out_dtype))
         return refuse(MOE_ERR_INVALID_ARG, "%s: out is not aligned to its elements", what);
+    if (!aligned4(scale, w_scale, offsets, row_src))
+        return refuse(MOE_ERR_INVALID_ARG, "%s: scale, w_scale, offsets or row_src is not aligned to its elements", what);
     BlockProduct a{q, q_stride, q_rows, s, scale, K, wq, ws, w_scale, n_experts, N, offsets, row_src, top_k, R, out,
                          out_stride, 2000000000ull, 0};
     cudaStream_t str = (cudaStream_t)stream;

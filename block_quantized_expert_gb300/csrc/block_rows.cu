@@ -422,6 +422,7 @@ extern "C" moe_status moe_quantize_blocks(const void* x, moe_dtype dtype, long l
     if (!x || !q || !s || (nv && !scale)) return refuse(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
     if (!nv && scale) return refuse(MOE_ERR_INVALID_ARG, "%s: MXFP4 rows have no scale", what);
     if ((uintptr_t)x % dtype_size(dtype)) return refuse(MOE_ERR_INVALID_ARG, "%s: x is not aligned to its elements", what);
+    if (!aligned4(scale)) return refuse(MOE_ERR_INVALID_ARG, "%s: scale is not aligned to its elements", what);
     cudaStream_t str = (cudaStream_t)stream;
     auto run = [&](auto type) {
         using A = decltype(type);
@@ -445,6 +446,7 @@ extern "C" moe_status moe_dequantize_blocks(const uint8_t* q, long long q_stride
     if (rows == 0) return MOE_OK;
     if (!x || !q || !s) return refuse(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
     if ((uintptr_t)x % dtype_size(dtype)) return refuse(MOE_ERR_INVALID_ARG, "%s: x is not aligned to its elements", what);
+    if (!aligned4(scale)) return refuse(MOE_ERR_INVALID_ARG, "%s: scale is not aligned to its elements", what);
     cudaStream_t str = (cudaStream_t)stream;
     const bool nv = format == MOE_WEIGHTS_NVFP4;
     auto run = [&](auto type) {

@@ -538,6 +538,8 @@ extern "C" moe_status moe_norm_rows(const void* x, moe_dtype dtype, long long x_
     if (st == MOE_OK) st = check_matrix(what, "gamma", gamma, hidden, hidden, dtype_size(gamma_dtype), true);
     if (st == MOE_OK && (q == nullptr) != (scale == nullptr))
         st = refuse(MOE_ERR_INVALID_ARG, "%s: of q and scale one is NULL", what);
+    if (st == MOE_OK && !aligned4(rstd, scale))
+        st = refuse(MOE_ERR_INVALID_ARG, "%s: rstd or scale is not aligned to its elements", what);
     if (st != MOE_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
     auto run = [&](auto type) {
@@ -570,6 +572,7 @@ extern "C" moe_status moe_norm_rows_backward(const void* dy, moe_dtype dtype, lo
     if (dgamma && (!scratch || scratch_bytes < moe_norm_scratch_bytes(T, hidden)))
         return refuse(MOE_ERR_INVALID_ARG, "%s: scratch is NULL or below moe_norm_scratch_bytes", what);
     if (dgamma && (uintptr_t)scratch % 16) return refuse(MOE_ERR_INVALID_ARG, "%s: scratch is not aligned to 16 bytes", what);
+    if (!aligned4(rstd, dgamma)) return refuse(MOE_ERR_INVALID_ARG, "%s: rstd or dgamma is not aligned to its elements", what);
     if (T == 0 && !dgamma) return MOE_OK;
     const int z = dtype_size(dtype);
     if (T > 0) {
