@@ -643,7 +643,7 @@ def _device_of(t) -> int:
 def _dense(dev, t, dtype, shape) -> int:
     """The pointer of a dense tensor of this type and shape on the device `dev`, else 0: what
     calls look for first, in as few steps as it takes.  0 is for the checks that can say why."""
-    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+    if t is not None and t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     return 0
 
@@ -678,7 +678,7 @@ def moe_norm_rows(x, gamma, y, eps: float = 1e-6, residual=None, h=None, rstd=No
     dev = _device_of(x)
     if stream is None and dt is not None and dev >= 0:
         d, f = x.dtype, torch.float32
-        g = gamma.dtype
+        g = getattr(gamma, "dtype", None)
         p = [_dense(dev, x, d, shape), _dense(dev, gamma, g, (H,)) if g is f or g is d else 0]
         for t in (residual, h, y):
             p.append(None if t is None else _dense(dev, t, d, shape))
@@ -729,7 +729,7 @@ def moe_norm_rows_backward(dy, h, gamma, rstd, dx, dgamma=None, scratch=None, dh
     dev = _device_of(h)
     if stream is None and dt is not None and T and dev >= 0:
         d, f = h.dtype, torch.float32
-        g = gamma.dtype
+        g = getattr(gamma, "dtype", None)
         p = [_dense(dev, dy, d, shape), _dense(dev, h, d, shape), _dense(dev, dx, d, shape), _dense(dev, rstd, f, (T,)),
              _dense(dev, gamma, g, (H,)) if g is f or g is d else 0, None if dh is None else _dense(dev, dh, d, shape),
              None if dgamma is None else _dense(dev, dgamma, f, (H,)), None]
