@@ -42,7 +42,7 @@ EXPORTS = ("moe_create", "moe_destroy", "moe_route", "moe_route_hash", "moe_perm
            "moe_combine", "moe_combine_backward", "moe_route_backward", "moe_quantize_rows",
            "moe_expert_product", "moe_check_product", "moe_test_stall_next_product", "moe_permute_scratch",
            "moe_permute_scratch_bytes", "moe_norm_rows", "moe_norm_rows_backward", "moe_norm_scratch_bytes",
-           "moe_quantize_blocks", "moe_dequantize_blocks", "moe_block_product")
+           "moe_quantize_blocks", "moe_dequantize_blocks", "moe_block_product", "moe_test_block_product_form")
 
 
 class MoeError(RuntimeError):
@@ -123,6 +123,7 @@ def load_library(build: bool = True) -> C.CDLL:
         "moe_block_product": ([vp, ll, i, vp, vp, i, i, vp, vp, vp, i, i, vp, vp, i, i, vp, i, ll, vp], i),
         "moe_check_product": ([vp], i),
         "moe_test_stall_next_product": ([], i),
+        "moe_test_block_product_form": ([i, i, i, i, i], i),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
@@ -905,3 +906,8 @@ def moe_check_product(stream=None):
 def moe_test_stall_next_product():
     """Test hook: the next tensor-core moe_expert_product runs out its bounded waits."""
     _check(load_library().moe_test_stall_next_product())
+
+
+def moe_test_block_product_form(n_experts: int, R: int, K: int, N: int, num_sms: int) -> int:
+    """The form of moe_block_product for these sizes: 0 CUDA cores, 1 a CTA and 2 a pair of CTAs a tile."""
+    return load_library().moe_test_block_product_form(n_experts, R, K, N, num_sms)

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(128) k_block_product_few(const BlockProduct a)
 // MXFP4 at 4096 x 4096 10.9 / 8.0 and 9.1 / 9.0: two positions of one large expert alone lose, and which
 // experts they are of is on the device.  One position of 4096 x 4096 takes 8.6 on the tensor cores; four take 11.3
 // and 8.6 with two positions a warp, six of six experts 17.2 and 16.1.
-bool few_rows(const BlockProduct& a) { return a.R <= 2; }
+bool few_rows(int R) { return R <= 2; }
 
 cudaError_t launch_few(const BlockProduct& a, bool nv, moe_dtype out, cudaStream_t s) {
     const dim3 grid((a.N + 4 * kChan - 1) / (4 * kChan), a.R);
@@ -208,10 +208,15 @@ extern "C" moe_status moe_block_product(const uint8_t* q, long long q_stride, in
                          out_stride, 2000000000ull, 0};
     cudaStream_t str = (cudaStream_t)stream;
     const bool nv = format == MOE_WEIGHTS_NVFP4;
-    if (few_rows(a)) return status_of(launch_few(a, nv, out_dtype, str), what);
+    if (few_rows(R)) return status_of(launch_few(a, nv, out_dtype, str), what);
     if (take_product_stall()) {
         a.stall = 1;
         a.wait_ns = 5000000ull;
     }
     return status_of(launch_block_product_tc(a, nv, out_dtype, str), what);
+}
+
+extern "C" int moe_test_block_product_form(int n_experts, int R, int K, int N, int num_sms) {
+    if (n_experts < 1 || R < 1 || K < 1 || N < 1 || num_sms < 2) return -1;
+    return few_rows(R) ? 0 : block_product_pairs(n_experts, R, K, N, num_sms) ? 2 : 1;
 }

@@ -30,6 +30,8 @@ __device__ __forceinline__ int source_row(const BlockProduct& a, int p) {
 
 // The tensor-core form (block_product_tc.cu): q and wq 16-byte aligned, qs a multiple of 16.
 cudaError_t launch_block_product_tc(const BlockProduct& a, bool nv, moe_dtype out, cudaStream_t s);
+// Whether it takes a call with pairs of CTAs (else one CTA a tile) on a GPU of `sms` SMs.
+bool block_product_pairs(int E, int R, int K, int N, int sms);
 // Where the current device has its sticky error flag (common.cuh).
 cudaError_t block_product_flag_at(uint32_t** flag);
 

@@ -646,29 +646,34 @@ cudaError_t launch_o(const BlockProduct& a, const CUtensorMap& wmap, const CUten
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    // Narrow or wide tiles, by rounds over the GPU times what a round takes, in us.  A segment
-    // of m positions has about m / cap + 1/2 tiles (those of the dense product are known) and at
-    // least one; it is taken as equal to the others, for the segments are on the device.
-    // Measured at K = 4096 in NVFP4, narrow and wide: 256 rows of one expert 10.1 and 12.5, 300 14.0
-    // and 13.7, 1024 23 and 21; 32 experts of 32 rows 56 and 57, of 64 66 and 59; at K = 2048 and
-    // 256 experts of 24 rows 216 and 211 (MXFP4 181 and 190), of 48 272 and 228 (216 and 204); 777
-    // rows at K = 1120, N = 1001 10.3 and 17.3.
-    const double segs = a.E < a.R ? a.E : a.R;
-    auto cost = [&](int cap, int channels, int at_once, double fixed, double base, double a_row) {
-        const double mean = a.R / segs, each = a.E == 1 ? (a.R + cap - 1) / cap : mean / cap + 0.5;
-        const double n = each > 1 ? each : 1;
-        const double rounds = std::ceil(segs * n * ((a.N + channels - 1) / channels) / at_once);
-        return fixed + rounds * (base + a_row * mean / n) * a.K / 4096;
-    };
     auto most = [&](int cap, int channels) {  // tiles
-        return (a.R / cap + (long long)segs) * ((a.N + channels - 1) / channels);
+        return (a.R / cap + (long long)(a.E < a.R ? a.E : a.R)) * ((a.N + channels - 1) / channels);
     };
-    if (cost(Cfg<true, kNv>::kCap, 256, sms / 2, 5.8, 7.4, 0.01) < cost(Cfg<false, kNv>::kCap, 128, sms, 4.3, 6.6, 0))
+    if (block_product_pairs(a.E, a.R, a.K, a.N, sms))
         return launch_kind<true, kNv, O>(a, most(Cfg<true, kNv>::kCap, 256), dev, wmap, qmap, s);
     return launch_kind<false, kNv, O>(a, most(Cfg<false, kNv>::kCap, 128), dev, wmap, qmap, s);
 }
 
 }  // namespace
+
+// Narrow or wide tiles, by rounds over the GPU times what a round takes, in us.  A segment
+// of m positions has about m / cap + 1/2 tiles (those of the dense product are known) and at
+// least one; it is taken as equal to the others, for the segments are on the device.
+// Measured at K = 4096 in NVFP4, narrow and wide: 256 rows of one expert 10.1 and 12.5, 300 14.0
+// and 13.7, 1024 23 and 21; 32 experts of 32 rows 56 and 57, of 64 66 and 59; at K = 2048 and
+// 256 experts of 24 rows 216 and 211 (MXFP4 181 and 190), of 48 272 and 228 (216 and 204); 777
+// rows at K = 1120, N = 1001 10.3 and 17.3.
+bool block_product_pairs(int E, int R, int K, int N, int sms) {
+    static_assert(Cfg<true, true>::kCap == Cfg<true, false>::kCap && Cfg<false, true>::kCap == Cfg<false, false>::kCap, "one rule");
+    const double segs = E < R ? E : R;
+    auto cost = [&](int cap, int channels, int at_once, double fixed, double base, double a_row) {
+        const double mean = R / segs, each = E == 1 ? (R + cap - 1) / cap : mean / cap + 0.5;
+        const double n = each > 1 ? each : 1;
+        const double rounds = std::ceil(segs * n * ((N + channels - 1) / channels) / at_once);
+        return fixed + rounds * (base + a_row * mean / n) * K / 4096;
+    };
+    return cost(Cfg<true, true>::kCap, 256, sms / 2, 5.8, 7.4, 0.01) < cost(Cfg<false, true>::kCap, 128, sms, 4.3, 6.6, 0);
+}
 
 cudaError_t block_product_flag_at(uint32_t** flag) { return cudaGetSymbolAddress((void**)flag, g_block_err); }
 

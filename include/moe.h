@@ -587,6 +587,12 @@ moe_status moe_check_product(moe_stream_t stream);
  * One-shot, for the process.                                              */
 moe_status moe_test_stall_next_product(void);
 
+/* The form in which moe_block_product takes a call of these sizes on a GPU of
+ * num_sms SMs (host computation): 0 the CUDA cores, 1 a CTA and 2 a pair of
+ * CTAs a tile of the tensor-core kernel, -1 sizes below 1.  For tests that
+ * mean one of them.                                                       */
+int moe_test_block_product_form(int n_experts, int R, int K, int N, int num_sms);
+
 #ifdef __cplusplus
 }
 #endif

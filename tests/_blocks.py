@@ -4,6 +4,9 @@ from __future__ import annotations
 import numpy as np
 
 MXFP4, NVFP4 = 0, 1
+# experts, positions, K and N that moe_block_product takes with pairs of CTAs
+PAIRS = [(1, 4000, 4096, 1000), (1, 2500, 512, 2560), (3, 2001, 1056, 4096), (1, 4000, 256, 8192), (1, 2100, 992, 4100),
+         (4, 4096, 512, 2048), (2, 2400, 128, 8192), (7, 2691, 288, 8192), (3, 1400, 2048, 1000), (16, 4462, 4096, 2048)]
 GRID = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
 FINE = np.array([b * 2.0 ** -9 if b < 8 else (8 + b % 8) * 2.0 ** (b // 8 - 10) for b in range(127)])
 
