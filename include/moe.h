@@ -494,8 +494,10 @@ moe_status moe_expert_product(const int8_t* q, long long q_stride, int q_rows, c
  *   rstd   device f32 [T] or NULL: moe_norm_rows_backward reads it
  *   q      device i8 [T][hidden] with its stride, scale device f32 [T]; both
  *          or neither
- * eps >= 0 (with 0 a row of zeros is 0 / 0); 1 <= hidden <= 131072, T <= 2^24.  The sum of squares is held in
- * fp32: a row where it overflows (|h| of 1e18 and more) has rstd 0.        */
+ * eps >= 0; 1 <= hidden <= 131072, T <= 2^24.  The sum of squares is held in
+ * fp32: a row where it overflows (|h| of 1e18 and more) has rstd 0, and with
+ * eps = 0 a row of zeros is 0 / 0 and one whose squares leave fp32's normal
+ * numbers (all |h| below 1e-15) has an inexact rstd, or an infinite one.   */
 moe_status moe_norm_rows(const void* x, moe_dtype dtype, long long x_stride, const void* residual,
                          long long residual_stride, const void* gamma, moe_dtype gamma_dtype, int T,
                          int hidden, float eps, void* h, long long h_stride, void* y, long long y_stride,
@@ -529,7 +531,8 @@ moe_status moe_norm_rows_backward(const void* dy, moe_dtype dtype, long long dy_
  *     2^-126; 0 for a row of zeros), which makes both quotients exact where
  *     they are half way between two codes; scale_given = 1: g is read (a
  *     checkpoint's scale of the whole matrix, say), the quotients amax / 6,
- *     / g and v / (s * g) each rounded in fp32.
+ *     / g and v / (s * g) each rounded in fp32; a row whose g is not above 0
+ *     gets scale bytes and codes of 0.
  * Rounded to nearest, half to even, at most 6.  gated as in moe_quantize_rows.
  *   x device dtype [rows][K] (gated: [rows][2 K]); q device u8 [rows][K / 2]
  *   with its stride; s device u8 [rows][K / 32] or [rows][K / 16], dense;
