@@ -644,8 +644,11 @@ def _device_of(t) -> int:
 def _dense(dev, t, dtype, shape) -> int:
     """The pointer of a dense tensor of this type and shape on the device `dev`, else 0: what
     calls look for first, in as few steps as it takes.  0 is for the checks that can say why."""
-    if t is not None and t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
     return 0
 
 
@@ -673,7 +676,7 @@ def moe_norm_rows(x, gamma, y, eps: float = 1e-6, residual=None, h=None, rstd=No
     T, H = shape = x.shape
     if T == 0:
         return
-    if T > _MOST or H > _MOST:
+    if T | H > _MOST:
         _sizes(T, H)
     dt = _ROW_TYPES.get(x.dtype)
     dev = _device_of(x)
@@ -724,7 +727,7 @@ def moe_norm_rows_backward(dy, h, gamma, rstd, dx, dgamma=None, scratch=None, dh
     residual stream goes on, dh; h and rstd as moe_norm_rows gave them.  dgamma needs scratch, a
     CUDA uint8 tensor of moe_norm_scratch_bytes."""
     T, H = shape = h.shape
-    if T > _MOST or H > _MOST:
+    if T | H > _MOST:
         _sizes(T, H)
     dt = _ROW_TYPES.get(h.dtype)
     dev = _device_of(h)
