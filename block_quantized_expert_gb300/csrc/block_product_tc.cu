@@ -20,8 +20,9 @@
 //   1 warp        rows and row scales of up to kTabs tiles ahead
 //
 // Measured at K = N = 4096, bf16 out, the copy rate being 6.78 TB/s: 3000 rows over some 234 of
-// 256 experts 312 us in MXFP4, 332 in NVFP4, 7.4 TB/s; 49152 rows over 256 experts 514 and
-// 549 us, 3.2 and 3.0 PFLOP/s; 8192 rows of one expert 53 and 63 us, 5.2 and 4.4 PFLOP/s.
+// 256 experts 312 us in MXFP4, 332 in NVFP4, 6.8 and 6.7 TB/s; 49152 rows over 256 experts 514 and
+// 549 us, 3.2 and 3.0 PFLOP/s; 8192 rows of one expert 53 and 63 us, 5.2 and 4.4 PFLOP/s (what the tensor cores
+// give in fp4 is not measured here; 13.5 is the nominal rate).
 // The narrow form is bound by the stream of weights; six rows of six experts (16 us) are two
 // rounds of tiles, each some 5 us whatever a tile's height (of 64 channels 20 us in all, of
 // 32 33), of which the scales' loads are 0.5, the MMAs 0.2 and the copies' issue 0.5.
@@ -154,6 +155,8 @@ __device__ uint32_t g_block_err;   // sticky, taken by moe_check_product
 
 // 16 scale bytes of one row from byte `at` on, zeros from byte `all` on: no row (nullptr)
 // is all zeros.  bytes: 16, 4 or 2 where every row's pieces of that size are whole and aligned.
+// Small pieces cost: six of 64 experts for each of 500 and of 8192 tokens, N = 2880, MXFP4, 47.5 and 200 us at
+// K = 2560 (80 bytes a row), 53 and 240 at 2816 (88, in fours), 96 and 496 at 2880 (90, in twos).
 __device__ __forceinline__ void load_scales(uint32_t (&w)[4], const uint8_t* row, int at, int all, int bytes) {
     w[0] = w[1] = w[2] = w[3] = 0;
     if (row == nullptr || at >= all) return;

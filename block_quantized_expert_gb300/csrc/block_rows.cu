@@ -12,8 +12,9 @@
 // With amax / 2688 itself one value in 500 of 16-bit rows is within 2^-24 of half way.
 //
 // 65536 x 4096 bf16 to codes: 122 us in NVFP4 (5.6 TB/s), 96 in MXFP4 (7.0); back 101 and 98
-// (6.8).  Gated, 49152 x 2048: 127 and 104 (4.0 TB/s), bound by the arithmetic of the gate and
-// of the codes, as NVFP4 is in part (65 % of all issue slots).
+// (6.8; MXFP4 with a row scale 102).  Gated, 49152 x 2048: 127 and 104 (4.0 TB/s), bound by the
+// issue of the gate's and the codes' arithmetic (75 and 79 % of all slots), as NVFP4 is in part
+// (65 %).  With given scales 188: a division for each element.
 #include <cmath>
 #include <type_traits>
 
@@ -52,8 +53,8 @@ __device__ __forceinline__ void load_unit(const A* p, Chunk<A, kUnit>& c) {
     }
 }
 
-// 1 / v within one unit: a quotient x r corrected by its exact remainder, q + (x - q v) r,
-// is then off by 2^-46 before it is rounded.
+// 1 / v within one unit: a quotient x r corrected by its exact remainder, q + (x - q v) r
+// (Markstein's correction), is then off by 2^-46 before it is rounded.
 __device__ __forceinline__ float reciprocal(float v) {
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));

@@ -52,7 +52,8 @@ struct Norm {
 // registers from the sum to the codes; kKeep = 0: rows of any length, read again for each pass (from h
 // where it is written: it may lie over an input).  Bound by HBM where rows move in 16-byte
 // words: 8192 x 4096 bf16 with a residual 41.3 us, 6.5 TB/s, 32768 rows 154, 7.0; with codes
-// 54.5; without a residual 27, 5.0; in single elements (H = 4095) 132.
+// 54.5; without a residual 27, 5.0, where L1 is busy to 68 % (each block reads gamma, in fp32 twice its
+// row's bytes) and the issue slots to 58; in single elements (H = 4095) 132.
 template <typename A, typename G, int C, int kKeep, int kMost, bool kWarp>
 __global__ void __launch_bounds__(kMost, kMost > 256 ? 1 : kKeep == 2 ? 8 : 6) k_norm_rows(const Norm<A> a) {
     pdl_launch_dependents();
@@ -380,12 +381,12 @@ __global__ void __launch_bounds__(1024) k_join_parts(const float* part, int part
 }
 
 // ----------------------------------------------------------------- launches --
+// Numbers of blocks here are measured on, and meant for, 152 SMs; every form is right with any.
 // Blocks of the gradient at most: three an SM of 256 threads, and more of the smaller ones
 // (8192 x 1024 bf16: 29 us with 456, 20 with 912).
 // Rows past 16384 are long whatever their type.
 constexpr int kLongParts = 16;
 int most_parts(int H) { return H <= 2048 ? 912 : H <= 16384 ? 456 : kLongParts; }
-
 
 // Short rows take a warp each: the GPU starts a block in about 1 ns, so that 65536 rows of any
 // width took 67 us and more (of 64 bf16: 11.4 now, 1024: 45).  The warp pays with more chunks a

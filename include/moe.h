@@ -81,7 +81,8 @@ typedef struct {
  * granularity)", the best 4-bit scheme of that study): the same e2m1 codes,
  * one e4m3 scale per 16 elements along K and one fp32 scale per expert
  * matrix, element = e2m1 * e4m3 scale * matrix scale.  The tcgen05
- * block-scaled MMAs take UE8M0 scales per 32 elements only, so an NVFP4
+ * block-scaled MMAs of 4-bit by 8-bit values, which the layer's activations
+ * need, take UE8M0 scales per 32 elements only, so an NVFP4
  * layer runs its GEMMs on the CUDA cores (moe_set_gemm_path 2 returns
  * MOE_ERR_UNSUPPORTED); a one-token call takes the CUDA-core whole-layer
  * decode kernel where its shape rules hold (moe_set_decode_kernel), else
