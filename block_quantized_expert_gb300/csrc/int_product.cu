@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(128) k_product_few(const Product a) {
 // by __dp4a (exact 32-bit integers): 8192 rows, K = N = 1000, 166 us (bound by the
 // issue of loads and sums, 0.1 PFLOP/s).  kWords: K, stride and bases allow four codes a
 // load, else they are shifted together from two (777 rows at K = 1101, N = 1001: 53 us, as single bytes 78;
-// 51 at K = 1100).  Three blocks an SM there, 80 registers: left to itself the compiler takes 64, in which
-// fewer loads are on their way (66 us; 2000 rows at K = 2047, N = 2048 254 for 212), two blocks lose (53, 311).
+// 51 at K = 1100).  There three blocks an SM, 80 registers: 2000 rows at K = 2047, N = 2048 take 254 us.  Left to itself
+// the compiler takes 64 registers, in which fewer loads are on their way: 66 and 212 us; with two blocks 53 and 311.
 struct Rows {
     const int8_t *lo, *hi;  // the matrix
 };
