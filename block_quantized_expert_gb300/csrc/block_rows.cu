@@ -53,8 +53,9 @@ __device__ __forceinline__ void load_unit(const A* p, Chunk<A, kUnit>& c) {
     }
 }
 
-// 1 / v within one unit: a quotient x r corrected by its exact remainder, q + (x - q v) r
-// (Markstein's correction), is then off by 2^-46 before it is rounded.
+// 1 / v within one unit: a quotient x r corrected by its exact remainder, q - (q v - x) r
+// (Markstein's correction), is then off by 2^-46 before it is rounded.  In this order of signs
+// it keeps that of a zero.
 __device__ __forceinline__ float reciprocal(float v) {
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -97,7 +98,7 @@ struct Unit<A, true> {
         for (int i = 0; i < kUnit; ++i) {
             const float x = gate[i], d = 1.f + expf(-x), r = reciprocal(d), q = __fmul_rn(x, r);
             // (past 2^120 a remainder could be 0 * infinity)
-            const float y = d < 0x1p120f ? __fmaf_rn(__fmaf_rn(-q, d, x), r, q) : __fdiv_rn(x, d);
+            const float y = d < 0x1p120f ? __fmaf_rn(-r, __fmaf_rn(q, d, -x), q) : __fdiv_rn(x, d);
             v[i] = __fmul_rn(y, v[i]);
             top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
         }
@@ -165,7 +166,7 @@ __device__ __forceinline__ uint2 unit_codes(const U& v, uint32_t top, RowPower p
 #pragma unroll
             for (int i = 0; i < kUnit; ++i) {
                 const float x = y[i], q = __fmul_rn(x, r);
-                y[i] = __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+                y[i] = __fmaf_rn(-r, __fmaf_rn(q, d, -x), q);
             }
         } else {
             const float t = __fdiv_rn(__fdiv_rn(amax, 6.f), p.g);

@@ -64,3 +64,24 @@ def test_offsets_out_of_range(R, K):
     bqe.moe_block_product(q, s, wq, ws, out, far, fmt=fmt)
     want, mag = product64(q, s, None, wq, ws, None, [0, 0, R // 2, R // 2, R], np.arange(R), fmt)
     check(out, want, mag, K, F32)
+
+
+@pytest.mark.parametrize("K", [96, 4096])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("fmt", [B.MXFP4, B.NVFP4])
+def test_zeros_keep_their_sign(K, dtype, fmt):
+    """-0 is code 8 beside other values, with scales found and given and behind a gate."""
+    x = rows_of(40, 2 * K, dtype, 4)
+    x[:, 1::7], x[:, 3::7] = -0.0, 0.0
+    for gated in (False, True):
+        v = x if gated else x[:, :K]
+        q, s, g = rows_tests.outputs(40, K, fmt)
+        bqe.moe_quantize_blocks(v, q, s, g, fmt, gated=gated)
+        sign = torch.signbit(v[:, :K]) ^ torch.signbit(v[:, K:]) if gated else torch.signbit(v)
+        zero = ((v[:, :K] == 0) | (v[:, K:] == 0)) if gated else v == 0
+        codes = torch.from_numpy(B.unpack(q.cpu().numpy())).cuda()
+        assert torch.equal(codes[zero], sign[zero].to(torch.uint8) * 8)
+        if g is not None:
+            q2, s2, _ = rows_tests.outputs(40, K, fmt)
+            bqe.moe_quantize_blocks(v, q2, s2, g, fmt, gated=gated, given=True)
+            assert torch.equal(q2, q) and torch.equal(s2, s)
